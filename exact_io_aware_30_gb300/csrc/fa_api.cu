@@ -1,9 +1,10 @@
 // fa_api.cu -- host side of the C ABI declared in include/fa.h: argument
 // validation, TMA tensor-map encoding, kernel selection and launch.  This file
 // holds the shared helpers and the forward (fa_fwd, fa_fwd_fp16, fa_fwd_gqa);
-// the backward, paged decoding, the 8-bit forward and the forward from host
-// memory are in fa_api_bwd.cuh, fa_api_decode.cuh, fa_api_fp8.cuh and
-// fa_api_host.cuh, included at the end (one translation unit).
+// the backward, paged decoding, the 8-bit forward, the forward from host
+// memory, rotary positions, the paged cache's updates and decoding over the
+// 8-bit cache are in the other fa_api_*.cuh, included at the end (one
+// translation unit).
 //
 // Validation happens before anything is enqueued and never falls back to a
 // different kernel: an unsupported head dim, dtype or mask is an error
@@ -493,8 +494,13 @@ fa_status fa_get_device_error(void) {
 }  // extern "C"
 
 // The other entry points, each with its kernels: the backward, decoding over a
-// paged cache, the 8-bit forward, and the forward from host memory.
+// paged cache, the 8-bit forward, the forward from host memory, rotary
+// positions, the paged cache's bookkeeping and 8-bit writes, and decoding over
+// the 8-bit cache.
 #include "fa_api_bwd.cuh"
 #include "fa_api_decode.cuh"
 #include "fa_api_fp8.cuh"
 #include "fa_api_host.cuh"
+#include "fa_api_rope.cuh"
+#include "fa_api_paged.cuh"
+#include "fa_api_decode_fp8.cuh"

@@ -1,14 +1,17 @@
 """ctypes binding of libfa.so (include/fa.h) -- argument marshalling only.
 
-Every step of the attention forward, backward and paged decoding runs inside
-the library's CUDA kernels; this module checks tensor metadata, allocates
+Every step of the attention forward, backward and paged decoding, of rotary
+positions and of the paged cache's updates runs inside the library's CUDA
+kernels; this module checks tensor metadata, allocates
 outputs (and workspaces) with torch and passes raw pointers and sizes through
 the C ABI.  If the library is missing or
 refuses a request, it raises: there is no other code path.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -30,6 +33,15 @@ MASKS = {"none": MASK_NONE, "causal": MASK_CAUSAL, "window": MASK_SLIDING_WINDOW
 
 DTYPE_BF16 = 0
 DTYPE_FP16 = 1
+DTYPE_FP32 = 2             # fa_rope only
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+ROPE_FORWARD = 0
+ROPE_BACKWARD = 1
+PAGED_OK = 0               # per-request status of fa_paged_update
+PAGED_NO_BLOCKS = 1
+PAGED_TOO_LONG = 2
+PAGED_NO_ROWS = 3
 DECODE_AUTO = 0            # fa_decode_paged kernel choice
 DECODE_TENSOR_CORES = 1
 DECODE_CUDA_CORES = 2
@@ -40,7 +52,9 @@ _DECODE_KERNELS = {"auto": DECODE_AUTO, "tensor_cores": DECODE_TENSOR_CORES,
 EXPORTS = ("fa_fwd", "fa_fwd_fp16", "fa_fwd_gqa", "fa_fwd_fp8", "fa_bwd", "fa_bwd_noalloc",
            "fa_bwd_workspace_query", "fa_decode_paged", "fa_decode_workspace_query",
            "fa_workspace_query", "fa_status_string", "fa_describe", "fa_get_device_error",
-           "fa_fwd_host", "fa_fwd_host_workspace_query", "fa_set_debug_stall_ms")
+           "fa_fwd_host", "fa_fwd_host_workspace_query", "fa_set_debug_stall_ms",
+           "fa_rope", "fa_rope_frequencies", "fa_paged_update", "fa_cache_append_fp8",
+           "fa_decode_paged_fp8", "fa_decode_fp8_workspace_query")
 
 
 class FAError(RuntimeError):
@@ -110,6 +124,24 @@ def load(path: str | None = None):
                                            ctypes.POINTER(ctypes.c_size_t)]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_status_string.argtypes = [_i]
+        _ll = ctypes.c_longlong
+        lib.fa_rope.restype = _i
+        lib.fa_rope.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _ll, _ll, _vp,
+                                ctypes.c_float, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]
+        lib.fa_rope_frequencies.restype = _i
+        lib.fa_rope_frequencies.argtypes = [_i, ctypes.c_double, _i, ctypes.c_double,
+                                            ctypes.c_double, ctypes.c_double, ctypes.c_double, _vp,
+                                            ctypes.POINTER(ctypes.c_float)]
+        lib.fa_paged_update.restype = _i
+        lib.fa_paged_update.argtypes = [_vp] * 10 + [_i] * 5 + [_vp]
+        lib.fa_cache_append_fp8.restype = _i
+        lib.fa_cache_append_fp8.argtypes = [_vp, _vp, _ll, _ll, _ll, _ll, _vp, _vp, _vp, _vp, _vp,
+                                            _i, _i, _i, _i, _i, _i, _vp]
+        lib.fa_decode_paged_fp8.restype = _i
+        lib.fa_decode_paged_fp8.argtypes = [_vp] * 10 + [ctypes.c_size_t] + [_i] * 9 + \
+            [ctypes.c_float, _i, _i, _vp]
+        lib.fa_decode_fp8_workspace_query.restype = _i
+        lib.fa_decode_fp8_workspace_query.argtypes = [_i] * 11 + [ctypes.POINTER(ctypes.c_size_t)]
         lib.fa_describe.restype = _i
         lib.fa_describe.argtypes = [_i, _i, _i, ctypes.c_char_p, ctypes.c_size_t]
         lib.fa_get_device_error.restype = _i
@@ -494,4 +526,332 @@ def forward_host(q, k, v, scale: float | None = None, mask="none", window: int =
     _check(st, "fa_fwd_host")
     if sync:
         stream.synchronize()
+    return out, lse
+
+
+# --------------------------------------------------- rotary positions and the 8-bit paged cache
+
+class _Scope:
+    """Runs a call on the tensors' own device and on ``stream``.
+
+    Outputs and workspaces made inside are allocated for that stream, so the
+    allocator cannot hand their memory to work of another stream too early.
+    Entering gives the raw stream pointer.
+    """
+    __slots__ = ("_scope", "_device", "_stream")
+
+    def __init__(self, device, stream):
+        self._device, self._stream, self._scope = device, stream, None
+
+    def __enter__(self):
+        import torch
+        dev, stream = self._device, self._stream
+        if stream is None:
+            if torch.cuda.current_device() != dev.index:
+                self._scope = torch.cuda.device(dev)
+                self._scope.__enter__()
+            return torch.cuda.current_stream(dev).cuda_stream
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else \
+                torch.cuda.default_stream(dev)
+        if stream.device != dev:
+            raise FAError(FA_ERR_INVALID_ARG, f"the stream is on {stream.device}, the tensors on {dev}")
+        self._scope = torch.cuda.stream(stream)
+        self._scope.__enter__()
+        return stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self._scope is not None:
+            self._scope.__exit__(*exc)
+        return False
+
+
+@functools.lru_cache(maxsize=256)
+def _longs(values):
+    """A host array of long long (never written to, so one per set of values will do)."""
+    return (ctypes.c_longlong * len(values))(*values)
+
+
+def _need_tensor(name, t, device, dtype, shape, contiguous=True):
+    """Checks one tensor argument against what the call needs of it."""
+    if t.device != device:
+        raise FAError(FA_ERR_INVALID_ARG, f"{name} must be on {device}, it is on {t.device}")
+    if t.dtype != dtype:
+        raise FAError(FA_ERR_INVALID_ARG, f"{name} must be {dtype}, it is {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise FAError(FA_ERR_INVALID_ARG, f"{name} must have shape {tuple(shape)}, it has {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise FAError(FA_ERR_INVALID_ARG, f"{name} must be contiguous")
+
+
+RopePlan = collections.namedtuple("RopePlan", "rot_dim freq amplitude")
+RopePlan.__doc__ = """What ``rope`` needs of a model's rotary positions (made by ``rope_plan``):
+the rotated components, their frequencies (device int64, turns per position
+times 2^64) and the amplitude."""
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: float = 0.0, low_turns: float = 1.0, high_turns: float = 32.0):
+    """(list of rot_dim / 2 integers: turns per position * 2^64, amplitude), by fa_rope_frequencies."""
+    if scaling not in ROPE_SCALINGS:
+        raise FAError(FA_ERR_UNSUPPORTED, f"scaling {scaling!r}: one of {list(ROPE_SCALINGS)}")
+    freq = (ctypes.c_ulonglong * max(1, int(rot_dim) // 2))()
+    amplitude = ctypes.c_float(0.0)
+    st = load().fa_rope_frequencies(int(rot_dim), float(base), ROPE_SCALINGS[scaling], float(factor),
+                                    float(original_length), float(low_turns), float(high_turns), freq,
+                                    ctypes.byref(amplitude))
+    _check(st, "fa_rope_frequencies")
+    return list(freq), amplitude.value
+
+
+def rope_plan(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+              original_length: float = 0.0, low_turns: float = 1.0, high_turns: float = 32.0,
+              device="cuda") -> RopePlan:
+    """The frequencies of rotary positions over the first ``rot_dim`` components.
+
+    scaling: "none"; "linear" (positions divided by ``factor``); "ntk" (the
+    base grown so that the slowest pair is stretched by ``factor``);
+    "by_parts" (pairs of at most ``low_turns`` turns over ``original_length``
+    positions are stretched by ``factor``, those of at least ``high_turns``
+    kept, and the amplitude is 0.1 ln(factor) + 1).
+    """
+    import torch
+    freq, amplitude = rope_frequencies(rot_dim, base, scaling, factor, original_length, low_turns, high_turns)
+    return RopePlan(int(rot_dim), torch.tensor(freq, dtype=torch.int64).to(device), amplitude)
+
+
+_ROPE_DTYPES: dict = {}
+
+
+def _rope_dtype(t) -> int:
+    if not _ROPE_DTYPES:
+        import torch
+        _ROPE_DTYPES.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32})
+    if t.dtype not in _ROPE_DTYPES:
+        raise FAError(FA_ERR_UNSUPPORTED, f"dtype {t.dtype} is not supported (bf16 / fp16 / fp32 only)")
+    return _ROPE_DTYPES[t.dtype]
+
+
+def _rope(q, k, plan, positions, offset, layout, out_q, out_k, stream, direction):
+    import torch
+    if layout not in ROPE_LAYOUTS:
+        raise FAError(FA_ERR_UNSUPPORTED, f"layout {layout!r}: one of {list(ROPE_LAYOUTS)}")
+    dt = _rope_dtype(q)
+    if not q.is_cuda or q.dim() != 4:
+        raise FAError(FA_ERR_INVALID_ARG, "q must be a 4-D CUDA tensor [B,H,S,d]")
+    dev = q.device
+    B, H, S, d = q.shape
+    Hkv = 0
+    if k is not None:
+        if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, S, d):
+            raise FAError(FA_ERR_INVALID_ARG, "k must be [B,H_kv,S,d] matching q")
+        Hkv = k.shape[1]
+        _need_tensor("k", k, dev, q.dtype, k.shape, contiguous=False)
+    elif out_k is not None:
+        raise FAError(FA_ERR_INVALID_ARG, "out_k without k")
+    for name, t, like in (("q", q, q), ("k", k, k), ("out_q", out_q, q), ("out_k", out_k, k)):
+        if t is None:
+            continue
+        if t is not like:
+            _need_tensor(name, t, dev, q.dtype, like.shape, contiguous=False)
+        if t.stride(3) != 1 and t.numel():
+            raise FAError(FA_ERR_INVALID_ARG, f"{name}: the last dimension must be contiguous")
+    if plan.freq.device != dev:
+        raise FAError(FA_ERR_INVALID_ARG, f"the plan is on {plan.freq.device}, the tensors on {dev}")
+    pos_ptr, pos_stride = None, 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.device != dev:
+            raise FAError(FA_ERR_INVALID_ARG, f"positions must be int32 on {dev}")
+        if tuple(positions.shape) == (B, S):
+            pos_stride = positions.stride(0) if B > 1 else 0
+        elif tuple(positions.shape) != (S,):
+            raise FAError(FA_ERR_INVALID_ARG, "positions must be [B,S] or [S]")
+        if S > 1 and positions.stride(-1) != 1:
+            raise FAError(FA_ERR_INVALID_ARG, "positions: the last dimension must be contiguous")
+        pos_ptr = positions.data_ptr()
+    with _Scope(dev, stream) as sp:
+        if out_q is None:
+            out_q = torch.empty((B, H, S, d), dtype=q.dtype, device=dev)
+        if k is not None and out_k is None:
+            out_k = torch.empty((B, Hkv, S, d), dtype=q.dtype, device=dev)
+        if q.numel() == 0 and (k is None or k.numel() == 0):
+            return out_q if k is None else (out_q, out_k)
+        st = load().fa_rope(
+            q.data_ptr(), _longs(q.stride()[:3]), out_q.data_ptr(), _longs(out_q.stride()[:3]),
+            k.data_ptr() if Hkv else None, _longs(k.stride()[:3]) if Hkv else None,
+            out_k.data_ptr() if Hkv else None, _longs(out_k.stride()[:3]) if Hkv else None,
+            pos_ptr, pos_stride, int(offset), plan.freq.data_ptr(), plan.amplitude, B, H, Hkv, S, d,
+            plan.rot_dim, ROPE_LAYOUTS[layout], direction, dt, sp)
+    _check(st, "fa_rope")
+    return out_q if k is None else (out_q, out_k)
+
+
+def rope(q, k, plan: RopePlan, positions=None, offset: int = 0, layout: str = "half", out_q=None,
+         out_k=None, stream=None):
+    """Rotary positions on q [B, H, S, d] and k [B, H_kv, S, d] (k may be None), by fa_rope.
+
+    Any strides with the last dimension contiguous (bf16, fp16 or fp32);
+    ``positions`` int32 [B, S] or [S] (None: 0 .. S-1), ``offset`` added to
+    them; ``layout`` "half" or "interleaved".  The outputs are contiguous
+    unless given; ``out_q=q`` works in place.  Returns (q', k'), or q' alone
+    without k.
+    """
+    return _rope(q, k, plan, positions, offset, layout, out_q, out_k, stream, ROPE_FORWARD)
+
+
+def rope_backward(dq, dk, plan: RopePlan, positions=None, offset: int = 0, layout: str = "half",
+                  out_q=None, out_k=None, stream=None):
+    """Gradients of ``rope``'s inputs from those of its outputs; arguments as for ``rope``."""
+    return _rope(dq, dk, plan, positions, offset, layout, out_q, out_k, stream, ROPE_BACKWARD)
+
+
+PagedStep = collections.namedtuple("PagedStep", "seq_lens ring_state slot_map positions status")
+PagedStep.__doc__ = """What ``paged_update`` returns: the new lengths [B] and ring state [2], the slot
+and position of every row [max_tokens], and the status of every request [B]
+(PAGED_OK, PAGED_NO_BLOCKS, PAGED_TOO_LONG or PAGED_NO_ROWS); int32."""
+
+
+def paged_update(seq_lens, delta, block_table, free_ring, ring_state, block_size: int,
+                 max_tokens: int | None = None, seq_lens_out=None, ring_state_out=None, slot_map=None,
+                 positions=None, status=None, stream=None) -> PagedStep:
+    """One step of a paged cache's bookkeeping on the GPU (fa_paged_update).
+
+    seq_lens and delta int32 [B] (tokens cached, and added or taken off);
+    block_table int32 [B, max_blocks] and free_ring int32 [ring_size] are
+    updated in place; ring_state int32 [2] is (head, count) of the free
+    blocks.  ``max_tokens`` rows of slots and positions are written (given by
+    slot_map's length if that is passed).  Outputs are allocated unless given;
+    seq_lens_out and ring_state_out may be their inputs.
+    """
+    import torch
+    if not seq_lens.is_cuda or seq_lens.dim() != 1 or block_table.dim() != 2 or free_ring.dim() != 1:
+        raise FAError(FA_ERR_INVALID_ARG, "seq_lens [B] on a CUDA device, block_table [B,max_blocks], free_ring [n]")
+    dev, i32 = seq_lens.device, torch.int32
+    B, mb = seq_lens.shape[0], block_table.shape[1]
+    if max_tokens is None:
+        if slot_map is None and positions is None:
+            raise FAError(FA_ERR_INVALID_ARG, "max_tokens, or slot_map, is needed")
+        max_tokens = (slot_map if slot_map is not None else positions).shape[0]
+    _need_tensor("seq_lens", seq_lens, dev, i32, (B,))
+    _need_tensor("delta", delta, dev, i32, (B,))
+    _need_tensor("block_table", block_table, dev, i32, (B, mb))
+    _need_tensor("free_ring", free_ring, dev, i32, free_ring.shape)
+    _need_tensor("ring_state", ring_state, dev, i32, (2,))
+    with _Scope(dev, stream) as sp:
+        outs = []
+        for name, t, n in (("seq_lens_out", seq_lens_out, B), ("ring_state_out", ring_state_out, 2),
+                           ("slot_map", slot_map, max_tokens), ("positions", positions, max_tokens),
+                           ("status", status, B)):
+            if t is None:
+                t = torch.empty(n, dtype=i32, device=dev)
+            else:
+                _need_tensor(name, t, dev, i32, (n,))
+            outs.append(t)
+        st = load().fa_paged_update(
+            seq_lens.data_ptr(), delta.data_ptr(), block_table.data_ptr(), free_ring.data_ptr(),
+            ring_state.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
+            outs[3].data_ptr(), outs[4].data_ptr(), B, mb, free_ring.shape[0], int(block_size),
+            int(max_tokens), sp)
+    _check(st, "fa_paged_update")
+    return PagedStep(*outs)
+
+
+def _need_fp8_cache(k_cache, v_cache, k_scale, v_scale, dev):
+    import torch
+    if k_cache.dim() != 4 or k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise FAError(FA_ERR_INVALID_ARG,
+                      "k_cache must be [num_blocks,H_kv,block_size,d], uint8 codes or float8_e4m3fn")
+    _need_tensor("k_cache", k_cache, dev, k_cache.dtype, k_cache.shape)
+    _need_tensor("v_cache", v_cache, dev, k_cache.dtype, k_cache.shape)
+    _need_tensor("k_scale", k_scale, dev, torch.float32, k_cache.shape[:2])
+    _need_tensor("v_scale", v_scale, dev, torch.float32, k_cache.shape[:2])
+
+
+def cache_append_fp8(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
+    """Quantises new K and V rows into an 8-bit paged cache, in place (fa_cache_append_fp8).
+
+    k, v [T, H_kv, d] (bf16 or fp16; any strides with the last dimension
+    contiguous); slot_map int32 [T] (negative: the row is skipped; the rows of
+    one block stand together); k_cache, v_cache [num_blocks, H_kv, block_size,
+    d] of e4m3 (uint8 codes or float8_e4m3fn); k_scale, v_scale fp32
+    [num_blocks, H_kv].
+    """
+    import torch
+    if not k.is_cuda or k.dim() != 3 or k_cache.dim() != 4:
+        raise FAError(FA_ERR_INVALID_ARG, "k must be a CUDA tensor [T,H_kv,d], the caches [blocks,H_kv,bs,d]")
+    dev = k.device
+    dt = _dtype_code(k)
+    T, Hkv, d = k.shape
+    nb, hc, bs, dc = k_cache.shape
+    _need_tensor("v", v, dev, k.dtype, k.shape, contiguous=False)
+    if (hc, dc) != (Hkv, d):
+        raise FAError(FA_ERR_INVALID_ARG, "the caches' heads and components must be those of k")
+    if k.numel() and (k.stride(2) != 1 or v.stride(2) != 1):
+        raise FAError(FA_ERR_INVALID_ARG, "k and v: the last dimension must be contiguous")
+    _need_tensor("slot_map", slot_map, dev, torch.int32, (T,))
+    _need_fp8_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    with _Scope(dev, stream) as sp:
+        st = load().fa_cache_append_fp8(
+            k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+            slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), T, Hkv, d, bs, nb, dt, sp)
+    _check(st, "fa_cache_append_fp8")
+
+
+def decode_fp8_workspace_query(B, H, H_kv, Sq, d, block_size, max_blocks, num_blocks, max_seq_len,
+                               mask="none", dtype=DTYPE_BF16):
+    """(status, bytes) of fa_decode_fp8_workspace_query."""
+    n = ctypes.c_size_t(12345)
+    st = load().fa_decode_fp8_workspace_query(int(B), int(H), int(H_kv), int(Sq), int(d), int(block_size),
+                                              int(max_blocks), int(num_blocks), int(max_seq_len),
+                                              mask_code(mask), int(dtype), ctypes.byref(n))
+    return st, n.value
+
+
+def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, max_seq_len: int,
+                     scale: float | None = None, mask="none", out=None, lse=None, workspace=None,
+                     stream=None):
+    """Attention of q's new rows over an 8-bit paged cache (fa_decode_paged_fp8).
+
+    q [B, H, Sq, d] bf16 or fp16; the caches and scales as ``cache_append_fp8``
+    writes them; block_table int32 [B, max_blocks], seq_lens int32 [B] (0
+    allowed: the row's output is 0 and its lse -inf).  Returns (o, lse).
+    """
+    import torch
+    if not q.is_cuda or q.dim() != 4 or not q.is_contiguous() or k_cache.dim() != 4:
+        raise FAError(FA_ERR_INVALID_ARG, "q must be a contiguous CUDA tensor [B,H,Sq,d], the caches 4-D")
+    dev = q.device
+    dt = _dtype_code(q)
+    B, H, Sq, d = q.shape
+    nb, Hkv, bs, dc = k_cache.shape
+    if dc != d or block_table.dim() != 2:
+        raise FAError(FA_ERR_INVALID_ARG, "the caches' last dimension must be q's; block_table [B,max_blocks]")
+    mb = block_table.shape[1]
+    _need_tensor("block_table", block_table, dev, torch.int32, (B, mb))
+    _need_tensor("seq_lens", seq_lens, dev, torch.int32, (B,))
+    _need_fp8_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    mk = mask_code(mask)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _Scope(dev, stream) as sp:
+        st, ws_bytes = decode_fp8_workspace_query(B, H, Hkv, Sq, d, bs, mb, nb, max_seq_len, mk, dt)
+        _check(st, "fa_decode_fp8_workspace_query")
+        if workspace is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        else:
+            _need_tensor("workspace", workspace, dev, torch.uint8, workspace.shape)
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _need_tensor("out", out, dev, q.dtype, q.shape)
+        if lse is None:
+            lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
+        else:
+            _need_tensor("lse", lse, dev, torch.float32, (B, H, Sq))
+        st = load().fa_decode_paged_fp8(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), B, H, Hkv, Sq, d, bs, mb, nb, int(max_seq_len),
+            float(scale), mk, dt, sp)
+    _check(st, "fa_decode_paged_fp8")
     return out, lse

@@ -54,6 +54,15 @@ typedef enum fa_status {
 
 enum { FA_MASK_NONE = 0, FA_MASK_CAUSAL = 1, FA_MASK_SLIDING_WINDOW = 2 };
 enum { FA_DTYPE_BF16 = 0, FA_DTYPE_FP16 = 1 };
+/* fa_rope also takes fp32; the attention entry points do not. */
+enum { FA_DTYPE_FP32 = 2 };
+/* Pairs of fa_rope: components (i, i + rot_dim/2), or (2i, 2i + 1). */
+enum { FA_ROPE_HALF = 0, FA_ROPE_INTERLEAVED = 1 };
+enum { FA_ROPE_FORWARD = 0, FA_ROPE_BACKWARD = 1 };
+/* Frequency scaling for contexts longer than trained (fa_rope_frequencies). */
+enum { FA_ROPE_SCALE_NONE = 0, FA_ROPE_SCALE_LINEAR = 1, FA_ROPE_SCALE_NTK = 2, FA_ROPE_SCALE_BY_PARTS = 3 };
+/* Per-request status of fa_paged_update. */
+enum { FA_PAGED_OK = 0, FA_PAGED_NO_BLOCKS = 1, FA_PAGED_TOO_LONG = 2, FA_PAGED_NO_ROWS = 3 };
 /* Kernel choice of fa_decode_paged / fa_decode_workspace_query. */
 enum { FA_DECODE_AUTO = 0, FA_DECODE_TENSOR_CORES = 1, FA_DECODE_CUDA_CORES = 2 };
 
@@ -271,6 +280,180 @@ fa_status fa_decode_paged(const void *q, const void *k_cache, const void *v_cach
 fa_status fa_decode_workspace_query(int B, int H, int H_kv, int Sq, int d, int block_size,
                                     int max_blocks, int num_blocks, int max_seq_len,
                                     int mask_kind, int dtype, int kernel, size_t *bytes);
+
+/*
+ * fa_rope -- rotary positions on q and k before the attention, or the gradient
+ * of that.  The first rot_dim components of every row are pairs (x1, x2); pair
+ * i of a row at position n becomes
+ *     y1 = a (x1 cos t - x2 sin t),  y2 = a (x1 sin t + x2 cos t),
+ *     t = n * f_i,   a = amplitude,
+ * and components rot_dim .. d pass through.  Angles are taken modulo a turn in
+ * 64-bit fixed point, so they are as accurate at position 2^31 as at 0.
+ * Products and sums are fp32, each output is rounded once.
+ *
+ *   q, q_out   [B, H, S, d] by strides: q_strides[3] are the element strides of
+ *              batch, head and token, on the host; components are adjacent.
+ *              Rows can so be read out of a packed projection
+ *              ([B, S, heads, d]) and written as the contiguous layout the
+ *              attention takes.  Any strides >= 0 for inputs (0 repeats a
+ *              row); an output's elements must all be distinct
+ *   k, k_out   [B, H_kv, S, d] alike; H_kv == 0: no k, the four are not
+ *              examined
+ *   positions  device int32, row (b, s) at positions[b * position_stride + s]
+ *              (stride 0: one row for every batch), or NULL: 0 .. S-1;
+ *              negative ones are allowed
+ *   offset     added to every position
+ *   freq       device array of rot_dim / 2 frequencies, turns per position
+ *              times 2^64, as fa_rope_frequencies writes them; 8-byte aligned
+ *   direction  FA_ROPE_FORWARD, or FA_ROPE_BACKWARD: q and k are gradients of
+ *              the forward's outputs, q_out and k_out those of its inputs
+ *   rot_dim    even, 2 <= rot_dim <= d <= 1024
+ *   dtype      FA_DTYPE_BF16, FA_DTYPE_FP16 or FA_DTYPE_FP32 (all four tensors)
+ * In place is allowed (an output with the base and strides of its own input,
+ * also for heads inside one packed tensor); any other overlap of an output
+ * with an input, the other output, positions or freq is refused
+ * (FA_ERR_INVALID_ARG).  Base addresses are aligned to the element.  S == 0:
+ * FA_OK, nothing is enqueued.  One launch on `stream`; no workspace.
+ */
+fa_status fa_rope(const void *q, const long long *q_strides, void *q_out, const long long *q_out_strides,
+                  const void *k, const long long *k_strides, void *k_out, const long long *k_out_strides,
+                  const int *positions, long long position_stride, long long offset,
+                  const unsigned long long *freq, float amplitude, int B, int H, int H_kv, int S, int d,
+                  int rot_dim, int layout, int direction, int dtype, fa_stream_t stream);
+
+/*
+ * fa_rope_frequencies -- the frequencies fa_rope reads, computed on the host
+ * in fp64: f_i = base^(-2i / rot_dim) radians per position, written to the
+ * host array freq[rot_dim / 2] as turns times 2^64, and the amplitude.
+ *   FA_ROPE_SCALE_NONE      f_i as it is; amplitude 1
+ *   FA_ROPE_SCALE_LINEAR    f_i / factor: positions squeezed by factor
+ *   FA_ROPE_SCALE_NTK       base * factor^(rot_dim / (rot_dim - 2)): the
+ *                           slowest pair is stretched by factor, the fastest
+ *                           left as it is
+ *   FA_ROPE_SCALE_BY_PARTS  a pair that makes at least high_turns turns over
+ *                           original_length positions keeps f_i, one that
+ *                           makes at most low_turns gets f_i / factor, between
+ *                           them linear; amplitude 0.1 ln(factor) + 1
+ * base >= 1; factor >= 1 (unused for NONE); original_length > 0 and low_turns
+ * < high_turns for BY_PARTS (unused otherwise).  No GPU is needed.
+ */
+fa_status fa_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_length,
+                              double low_turns, double high_turns, unsigned long long *freq,
+                              float *amplitude);
+
+/*
+ * fa_paged_update -- one step of a paged cache's bookkeeping on the GPU: block
+ * tables, slots and positions from the requests' lengths, with the free
+ * physical blocks in a ring ("Flash attention and memory-efficient attention
+ * variants", section "PagedAttention: memory management borrowed from an
+ * operating system").  Nothing is read back to the host, so a step can be
+ * captured in a graph and replayed.
+ *
+ *   seq_lens    device int32 [B]: cached tokens of each request (values outside
+ *               [0, max_blocks * block_size] are clamped into it)
+ *   delta       device int32 [B]: tokens the step adds (> 0) or takes off the
+ *               end (< 0, at most all: rejected drafts, finished requests)
+ *   block_table device int32 [B, max_blocks], updated in place: new blocks are
+ *               entered; entries past a request's last block are not cleared
+ *   free_ring   device int32 [ring_size], updated in place: the free blocks are
+ *               entries (head + i) % ring_size, i < count
+ *   ring_state  device int32 {head, count}
+ *   seq_lens_out, ring_state_out  the new lengths and state; each may be its
+ *               input
+ *   slot_map, positions  device int32 [max_tokens]: the added tokens, request
+ *               by request in index order: the token's slot (physical block *
+ *               block_size + place in it) and its position in its request.
+ *               Rows past the last token get slot -1 and position 0
+ *   status      device int32 [B]: FA_PAGED_OK, or why the request was left as
+ *               it was (its rows then have slot -1, position 0):
+ *               FA_PAGED_TOO_LONG (past max_blocks * block_size),
+ *               FA_PAGED_NO_ROWS (its rows would pass max_tokens),
+ *               FA_PAGED_NO_BLOCKS (the free blocks ran out: blocks go to
+ *               requests in index order, and once one is short, later ones
+ *               that need any are refused too)
+ *   block_size  16, 32, 64 or 128, else FA_ERR_UNSUPPORTED
+ * New blocks are taken from the ring's head; blocks given back are added
+ * behind its tail, in index order, and can be taken from the next call on (a
+ * ring of at least the pool's blocks never overflows; blocks past ring_size
+ * are dropped).  A row whose table entry is negative, or whose slot would pass
+ * 2^31 - 1, gets slot -1 and position 0.
+ * Otherwise outputs may not overlap inputs or each other.  One launch; no
+ * workspace; the results do not depend on timing.
+ */
+fa_status fa_paged_update(const int *seq_lens, const int *delta, int *block_table, int *free_ring,
+                          const int *ring_state, int *seq_lens_out, int *ring_state_out, int *slot_map,
+                          int *positions, int *status, int B, int max_blocks, int ring_size,
+                          int block_size, int max_tokens, fa_stream_t stream);
+
+/*
+ * fa_cache_append_fp8 -- writes new K and V rows into a paged cache held in
+ * e4m3 codes with one scale per (block, K/V head), K and V apart: the value of
+ * a code is code * scale.  For every block the call writes to:
+ *     need   = the smallest power of two s >= 2^-126 with |x| <= 448 s for
+ *              every finite value x written to it
+ *     scale' = need if the block's slot 0 is written (the block starts anew),
+ *              else max(scale, need)
+ *     where scale' > scale, the codes of the block not written become
+ *     e4m3(code * scale / scale'); the written ones are e4m3(x / scale')
+ * rounded to nearest even, saturating at +-448 (infinities too; NaN stays
+ * NaN).  A stored scale that is no positive finite number counts as none.
+ *
+ *   k, v        [T, H_kv, d] 16-bit by element strides (token, head); values
+ *               of a head adjacent; the strides are >= 0
+ *   slot_map    device int32 [T], as fa_paged_update writes it: row t goes to
+ *               slot s = block * block_size + place; rows whose slot is outside
+ *               [0, num_blocks * block_size) are skipped.  Rows of one block
+ *               must stand together (skipped rows between them are fine): a
+ *               block met again behind another block's rows gives undefined
+ *               codes and scale for that block.  A slot named twice in its
+ *               block's rows gets the later row
+ *   k_cache, v_cache  [num_blocks, H_kv, block_size, d] e4m3, 16-byte aligned
+ *   k_scale, v_scale  [num_blocks, H_kv] fp32
+ *   d           64, 128 or 256; block_size 16, 32, 64 or 128
+ *   dtype       FA_DTYPE_BF16 or FA_DTYPE_FP16 (k and v)
+ * Codes and scales of blocks without a row are left as they were, and so are
+ * the slots without a row of a block that starts anew.  T == 0: FA_OK.
+ * Outputs may not overlap inputs or each other.  One launch; no workspace.
+ */
+fa_status fa_cache_append_fp8(const void *k, const void *v, long long k_token_stride,
+                              long long k_head_stride, long long v_token_stride, long long v_head_stride,
+                              const int *slot_map, void *k_cache, void *v_cache, float *k_scale,
+                              float *v_scale, int T, int H_kv, int d, int block_size, int num_blocks,
+                              int dtype, fa_stream_t stream);
+
+/*
+ * fa_decode_paged_fp8 -- fa_decode_paged over the 8-bit cache of
+ * fa_cache_append_fp8: exact softmax attention over the dequantised tokens,
+ * q and o in 16 bits.  Arguments as for fa_decode_paged, except:
+ *
+ *   k_cache, v_cache  [num_blocks, H_kv, block_size, d] e4m3
+ *   k_scale, v_scale  [num_blocks, H_kv] fp32, finite (any such scales, powers
+ *                     of two or not)
+ *   q            finite; a row with an infinity or NaN gives NaN
+ *   seq_lens     any length in [0, max_seq_len] (values outside are clamped
+ *                into it).  A row that sees no key -- length 0, or with
+ *                FA_MASK_CAUSAL a row in front of the request's first token --
+ *                gets O = 0 and lse = -inf
+ *   block_table  an entry outside [0, num_blocks) reads zeros
+ *   workspace    at least fa_decode_fp8_workspace_query() bytes, 256-byte
+ *                aligned; may be NULL where that is 0
+ * Cache slots past a request's length may hold any codes, NaN included.
+ */
+fa_status fa_decode_paged_fp8(const void *q, const void *k_cache, const void *v_cache,
+                              const float *k_scale, const float *v_scale, const int *block_table,
+                              const int *seq_lens, void *o, float *lse, void *workspace,
+                              size_t workspace_bytes, int B, int H, int H_kv, int Sq, int d,
+                              int block_size, int max_blocks, int num_blocks, int max_seq_len,
+                              float scale, int mask_kind, int dtype, fa_stream_t stream);
+
+/*
+ * fa_decode_fp8_workspace_query -- workspace bytes fa_decode_paged_fp8 needs
+ * on the current device and the status it would return for these sizes.
+ * bytes must be non-NULL; it is 0 whenever the status is not FA_OK.
+ */
+fa_status fa_decode_fp8_workspace_query(int B, int H, int H_kv, int Sq, int d, int block_size,
+                                        int max_blocks, int num_blocks, int max_seq_len, int mask_kind,
+                                        int dtype, size_t *bytes);
 
 /*
  * fa_fwd_host -- the forward end to end from host memory: Q, K, V are
