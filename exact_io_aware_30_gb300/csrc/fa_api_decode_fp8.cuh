@@ -21,17 +21,80 @@ fa_status check_dec_fp8_sizes(int B, int H, int Hkv, int Sq, int d, int block_si
         return FA_ERR_INVALID_ARG;
     if ((long long)B * H * Sq > 0x7fffffffLL / 2 || (long long)B * max_blocks > 0x7fffffffLL)
         return FA_ERR_INVALID_ARG;
+    if ((long long)Hkv * (H / Hkv * Sq) > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
     return FA_OK;
 }
 
-template <int D>
-fa_status launch_decode_fp8(const DecFp8Params &p, bool fp16, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(p.B * p.H * p.Sq);
-    if (fp16)
-        fa_decode_fp8_kernel<D, true><<<grid, 128, 0, stream>>>(p);
-    else
-        fa_decode_fp8_kernel<D, false><<<grid, 128, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+// Rows per unit (the kernel's RC) for R rows per K/V head: one chunk of the
+// smallest size that holds them, or equal chunks of at most 32 -- beyond that
+// the parts' columns of S and O no longer fit tensor memory beside each other,
+// and the cache is read once more per chunk (from L2, the chunks being
+// neighbours in the line of tiles).
+constexpr int kDecFp8MaxRows = 32;
+
+struct DecFp8Plan {
+    int rc = 0, chunks = 1, rows_per_chunk = 0, grid = 0;
+    bool cuts = false;  // a unit can lie across CTAs
+    size_t part_lse_off = 0, part_o_off = 0, bytes = 0;
+};
+
+template <int D, bool kFP16>
+int dec_fp8_ctas_per_sm(int rc) {
+    return rc == 1    ? DecFp8Cfg<D, kFP16, 1>::CTAS_PER_SM
+           : rc == 4  ? DecFp8Cfg<D, kFP16, 4>::CTAS_PER_SM
+           : rc == 8  ? DecFp8Cfg<D, kFP16, 8>::CTAS_PER_SM
+           : rc == 16 ? DecFp8Cfg<D, kFP16, 16>::CTAS_PER_SM
+                      : DecFp8Cfg<D, kFP16, 32>::CTAS_PER_SM;
+}
+
+DecFp8Plan plan_decode_fp8(int B, int Hkv, int R, int d, bool fp16, int max_seq_len, int num_sms) {
+    DecFp8Plan pl;
+    pl.chunks = (R + kDecFp8MaxRows - 1) / kDecFp8MaxRows;
+    pl.rows_per_chunk = (R + pl.chunks - 1) / pl.chunks;
+    pl.chunks = (R + pl.rows_per_chunk - 1) / pl.rows_per_chunk;
+    for (int rc : {1, 4, 8, 16, 32})
+        if (pl.rc == 0 && rc >= pl.rows_per_chunk) pl.rc = rc;
+    const int per_sm = d == 64    ? (fp16 ? dec_fp8_ctas_per_sm<64, true>(pl.rc) : dec_fp8_ctas_per_sm<64, false>(pl.rc))
+                       : d == 128 ? (fp16 ? dec_fp8_ctas_per_sm<128, true>(pl.rc) : dec_fp8_ctas_per_sm<128, false>(pl.rc))
+                                  : 1;
+    const long long tiles = (max_seq_len + 127LL) / 128;
+    const long long most = (long long)B * Hkv * pl.chunks * tiles;
+    pl.grid = (int)std::min(most, (long long)num_sms * per_sm);
+    pl.cuts = pl.grid > 1 && tiles > 1;
+    size_t at = (size_t)(4 + 4 * pl.grid) * 4;
+    if (pl.cuts) {
+        pl.part_lse_off = (at + 255) / 256 * 256;
+        pl.part_o_off = (pl.part_lse_off + (size_t)2 * pl.grid * pl.rc * 4 + 255) / 256 * 256;
+        at = pl.part_o_off + (size_t)2 * pl.grid * pl.rc * d * 4;
+    }
+    pl.bytes = at;
+    return pl;
+}
+
+template <int D, bool kFP16, int RC>
+fa_status launch_decode_fp8_rc(const DecFp8Params &p, const DecFp8Plan &pl, DeviceInfo &info, cudaStream_t stream) {
+    using C = DecFp8Cfg<D, kFP16, RC>;
+    constexpr int kind = RC == 1 ? 0 : RC == 4 ? 1 : RC == 8 ? 2 : RC == 16 ? 3 : 4;
+    const int slot = ((D == 256 ? 2 : D == 128 ? 1 : 0) * 2 + (kFP16 ? 1 : 0)) * 5 + kind;
+    if (set_smem(fa_decode_fp8_kernel<C>, C::SMEM_BYTES, info.attr_dec_fp8[slot]) != FA_OK) return FA_ERR_CUDA;
+    fa_decode_fp8_kernel<C><<<(unsigned)pl.grid, C::NUM_THREADS, C::SMEM_BYTES, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (pl.cuts) {
+        fa_decode_fp8_combine_kernel<D, kFP16, RC><<<(unsigned)(pl.grid - 1), 128, 0, stream>>>(p, pl.grid);
+        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+template <int D, bool kFP16>
+fa_status launch_decode_fp8(const DecFp8Params &p, const DecFp8Plan &pl, DeviceInfo &info, cudaStream_t stream) {
+    switch (pl.rc) {
+        case 1: return launch_decode_fp8_rc<D, kFP16, 1>(p, pl, info, stream);
+        case 4: return launch_decode_fp8_rc<D, kFP16, 4>(p, pl, info, stream);
+        case 8: return launch_decode_fp8_rc<D, kFP16, 8>(p, pl, info, stream);
+        case 16: return launch_decode_fp8_rc<D, kFP16, 16>(p, pl, info, stream);
+        default: return launch_decode_fp8_rc<D, kFP16, 32>(p, pl, info, stream);
+    }
 }
 
 fa_status decode_fp8_impl(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
@@ -55,8 +118,10 @@ fa_status decode_fp8_impl(const void *q, const void *k_cache, const void *v_cach
     DeviceInfo *info = nullptr;
     st = device_info(&dev, &info);
     if (st != FA_OK) return st;
-    const size_t need = 0;
-    if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+    const bool fp16 = dtype == FA_DTYPE_FP16;
+    const DecFp8Plan pl = plan_decode_fp8(B, Hkv, H / Hkv * Sq, d, fp16, max_seq_len, info->num_sms);
+    const size_t need = pl.bytes;
+    if (!workspace || workspace_bytes < need) return FA_ERR_INVALID_ARG;
     const size_t rows = (size_t)B * H * Sq, qo = rows * d * 2;
     const size_t cache = (size_t)num_blocks * Hkv * block_size * d, scales = (size_t)num_blocks * Hkv * 4;
     const Extent ins[7] = {{q, qo}, {k_cache, cache}, {v_cache, cache}, {k_scale, scales}, {v_scale, scales},
@@ -64,34 +129,49 @@ fa_status decode_fp8_impl(const void *q, const void *k_cache, const void *v_cach
     const Extent outs[3] = {{o, qo}, {lse, rows * 4}, {workspace, need}};
     if (!outputs_apart(outs, 3, ins, 7, nullptr)) return FA_ERR_INVALID_ARG;
 
-    const bool fp16 = dtype == FA_DTYPE_FP16;
     DecFp8Params p;
     std::memset(&p, 0, sizeof(p));
+    const int row_bytes = std::min(d, 128);
+    if (!make_map8(&p.tm_k, k_cache, d, block_size, Hkv, num_blocks, row_bytes, block_size) ||
+        !make_map8(&p.tm_v, v_cache, d, block_size, Hkv, num_blocks, row_bytes, block_size))
+        return FA_ERR_CUDA;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.q = static_cast<const uint16_t *>(q);
-    p.k_cache = static_cast<const uint8_t *>(k_cache);
-    p.v_cache = static_cast<const uint8_t *>(v_cache);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.block_table = block_table;
     p.seq_lens = seq_lens;
     p.o = o;
     p.lse = lse;
+    p.cuts = reinterpret_cast<int *>(ws);
+    p.part_lse = reinterpret_cast<float *>(ws + pl.part_lse_off);
+    p.part_o = reinterpret_cast<float *>(ws + pl.part_o_off);
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;
     p.Sq = Sq;
+    p.R = H / Hkv * Sq;
+    p.chunks = pl.chunks;
+    p.rows_per_chunk = pl.rows_per_chunk;
     p.bs_log2 = block_size_log2(block_size);
     p.max_blocks = max_blocks;
     p.num_blocks = num_blocks;
     p.max_seq_len = max_seq_len;
     p.mask_kind = mask_kind;
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.wait_limit_ns = fa::kWaitLimitNs;
+    if (const uint64_t ns = debug_stall_ns()) {
+        p.stall_test = 1;
+        p.wait_limit_ns = ns;
+    }
     if (log_enabled())
-        std::fprintf(stderr, "[fa] fa_decode_paged_fp8 d=%d B=%d H=%d Hkv=%d Sq=%d bs=%d max_len=%d\n", d, B, H, Hkv,
-                     Sq, block_size, max_seq_len);
-    return d == 64    ? launch_decode_fp8<64>(p, fp16, stream)
-           : d == 128 ? launch_decode_fp8<128>(p, fp16, stream)
-                      : launch_decode_fp8<256>(p, fp16, stream);
+        std::fprintf(stderr, "[fa] fa_decode_paged_fp8 d=%d B=%d H=%d Hkv=%d Sq=%d bs=%d max_len=%d rows=%d x %d grid=%d\n",
+                     d, B, H, Hkv, Sq, block_size, max_seq_len, pl.rows_per_chunk, pl.chunks, pl.grid);
+    if (d == 64)
+        return fp16 ? launch_decode_fp8<64, true>(p, pl, *info, stream) : launch_decode_fp8<64, false>(p, pl, *info, stream);
+    if (d == 128)
+        return fp16 ? launch_decode_fp8<128, true>(p, pl, *info, stream) : launch_decode_fp8<128, false>(p, pl, *info, stream);
+    return fp16 ? launch_decode_fp8<256, true>(p, pl, *info, stream) : launch_decode_fp8<256, false>(p, pl, *info, stream);
 }
 
 }  // namespace
@@ -118,7 +198,10 @@ fa_status fa_decode_fp8_workspace_query(int B, int H, int H_kv, int Sq, int d, i
     if (st != FA_OK) return st;
     int dev = 0;
     fa::DeviceInfo *info = nullptr;
-    return fa::device_info(&dev, &info);
+    const fa_status dst = fa::device_info(&dev, &info);
+    if (dst != FA_OK) return dst;
+    *bytes = fa::plan_decode_fp8(B, H_kv, H / H_kv * Sq, d, dtype == FA_DTYPE_FP16, max_seq_len, info->num_sms).bytes;
+    return FA_OK;
 }
 
 }  // extern "C"
