@@ -46,7 +46,7 @@ struct DeviceInfo {
     unsigned long long noalloc_ctx = 0;  // id of the context that address belongs to
     bool attr_dec[6] = {false, false, false, false, false, false};
     bool attr_fp8[3] = {false, false, false};  // 8-bit forward, d = 64, 128, 256
-    bool attr_dec_fp8[30] = {};  // 8-bit cache decode: d = 64, 128, 256 x bf16, fp16 x rows
+    bool attr_dec_fp8[36] = {};  // 8-bit cache decode: d = 64, 128, 256 x bf16, fp16 x rows
     bool attr_gemv[12] = {};  // few-row decode: d = 64, 128, 256 x bf16, fp16 x 1, 2 rows
 };
 

@@ -26,11 +26,11 @@ fa_status check_dec_fp8_sizes(int B, int H, int Hkv, int Sq, int d, int block_si
 }
 
 // Rows per unit (the kernel's RC) for R rows per K/V head: one chunk of the
-// smallest size that holds them, or equal chunks of at most 32 -- beyond that
-// the parts' columns of S and O no longer fit tensor memory beside each other,
-// and the cache is read once more per chunk (from L2, the chunks being
-// neighbours in the line of tiles).
-constexpr int kDecFp8MaxRows = 32;
+// smallest size that holds them, or equal chunks of at most 32 (24 for fp16 at
+// d = 256) -- beyond that two buffers each of S's and O's part columns no
+// longer fit tensor memory, and the cache is read once more per chunk (from
+// L2, the chunks being neighbours in the line of tiles).
+constexpr int dec_fp8_max_rows(int d, bool fp16) { return d == 256 && fp16 ? 24 : 32; }
 
 struct DecFp8Plan {
     int rc = 0, chunks = 1, rows_per_chunk = 0, grid = 0;
@@ -44,15 +44,17 @@ int dec_fp8_ctas_per_sm(int rc) {
            : rc == 4  ? DecFp8Cfg<D, kFP16, 4>::CTAS_PER_SM
            : rc == 8  ? DecFp8Cfg<D, kFP16, 8>::CTAS_PER_SM
            : rc == 16 ? DecFp8Cfg<D, kFP16, 16>::CTAS_PER_SM
+           : rc == 24 ? DecFp8Cfg<D, kFP16, 24>::CTAS_PER_SM
                       : DecFp8Cfg<D, kFP16, 32>::CTAS_PER_SM;
 }
 
 DecFp8Plan plan_decode_fp8(int B, int Hkv, int R, int d, bool fp16, int max_seq_len, int num_sms) {
     DecFp8Plan pl;
-    pl.chunks = (R + kDecFp8MaxRows - 1) / kDecFp8MaxRows;
+    const int max_rows = dec_fp8_max_rows(d, fp16);
+    pl.chunks = (R + max_rows - 1) / max_rows;
     pl.rows_per_chunk = (R + pl.chunks - 1) / pl.chunks;
     pl.chunks = (R + pl.rows_per_chunk - 1) / pl.rows_per_chunk;
-    for (int rc : {1, 4, 8, 16, 32})
+    for (int rc : {1, 4, 8, 16, 24, 32})
         if (pl.rc == 0 && rc >= pl.rows_per_chunk) pl.rc = rc;
     const int per_sm = d == 64    ? (fp16 ? dec_fp8_ctas_per_sm<64, true>(pl.rc) : dec_fp8_ctas_per_sm<64, false>(pl.rc))
                        : d == 128 ? (fp16 ? dec_fp8_ctas_per_sm<128, true>(pl.rc) : dec_fp8_ctas_per_sm<128, false>(pl.rc))
@@ -61,7 +63,7 @@ DecFp8Plan plan_decode_fp8(int B, int Hkv, int R, int d, bool fp16, int max_seq_
     const long long most = (long long)B * Hkv * pl.chunks * tiles;
     pl.grid = (int)std::min(most, (long long)num_sms * per_sm);
     pl.cuts = pl.grid > 1 && tiles > 1;
-    size_t at = (size_t)(4 + 4 * pl.grid) * 4;
+    size_t at = (size_t)(4 + 5 * pl.grid) * 4;
     if (pl.cuts) {
         pl.part_lse_off = (at + 255) / 256 * 256;
         pl.part_o_off = (pl.part_lse_off + (size_t)2 * pl.grid * pl.rc * 4 + 255) / 256 * 256;
@@ -74,8 +76,8 @@ DecFp8Plan plan_decode_fp8(int B, int Hkv, int R, int d, bool fp16, int max_seq_
 template <int D, bool kFP16, int RC>
 fa_status launch_decode_fp8_rc(const DecFp8Params &p, const DecFp8Plan &pl, DeviceInfo &info, cudaStream_t stream) {
     using C = DecFp8Cfg<D, kFP16, RC>;
-    constexpr int kind = RC == 1 ? 0 : RC == 4 ? 1 : RC == 8 ? 2 : RC == 16 ? 3 : 4;
-    const int slot = ((D == 256 ? 2 : D == 128 ? 1 : 0) * 2 + (kFP16 ? 1 : 0)) * 5 + kind;
+    constexpr int kind = RC == 1 ? 0 : RC == 4 ? 1 : RC == 8 ? 2 : RC == 16 ? 3 : RC == 24 ? 4 : 5;
+    const int slot = ((D == 256 ? 2 : D == 128 ? 1 : 0) * 2 + (kFP16 ? 1 : 0)) * 6 + kind;
     if (set_smem(fa_decode_fp8_kernel<C>, C::SMEM_BYTES, info.attr_dec_fp8[slot]) != FA_OK) return FA_ERR_CUDA;
     fa_decode_fp8_kernel<C><<<(unsigned)pl.grid, C::NUM_THREADS, C::SMEM_BYTES, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
@@ -93,8 +95,11 @@ fa_status launch_decode_fp8(const DecFp8Params &p, const DecFp8Plan &pl, DeviceI
         case 4: return launch_decode_fp8_rc<D, kFP16, 4>(p, pl, info, stream);
         case 8: return launch_decode_fp8_rc<D, kFP16, 8>(p, pl, info, stream);
         case 16: return launch_decode_fp8_rc<D, kFP16, 16>(p, pl, info, stream);
-        default: return launch_decode_fp8_rc<D, kFP16, 32>(p, pl, info, stream);
+        case 24: return launch_decode_fp8_rc<D, kFP16, 24>(p, pl, info, stream);
+        default: break;
     }
+    if constexpr (dec_fp8_max_rows(D, kFP16) >= 32) return launch_decode_fp8_rc<D, kFP16, 32>(p, pl, info, stream);
+    else return FA_ERR_UNSUPPORTED;  // (the plan keeps chunks within the limit)
 }
 
 fa_status decode_fp8_impl(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,

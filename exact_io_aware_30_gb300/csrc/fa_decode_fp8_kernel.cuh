@@ -37,10 +37,13 @@
 // fa_decode_fp8_combine_kernel (a CTA per cut) merges them in order.
 //
 // One CTA:
-//   warps 0-3: softmax.  Thread = key for S^T (TMEM lane), = column of d for
-//              O^T; O is kept in registers, rescaled per tile;
-//   warp 4:    MMA issuer: S^T of tile t + 1 before O^T of tile t;
-//   warp 5:    TMA, a lane per block of the tile, K and V rings.
+//   softmax warpgroups, one per eight rows of the unit.  Thread = key for S^T
+//     (TMEM lane), = column of d for O^T; O is kept in registers, rescaled per
+//     tile.  (All rows in one warpgroup, 16 or 32 to a thread, left the SM with
+//     eight warps in long dependent chains: 115 and 240 us where 8 rows take 94,
+//     64 requests x 8 K/V heads x 4,096 tokens at d 128.)
+//   an MMA warp: S^T of tile t + 1 before O^T of tile t;
+//   a TMA warp: a lane per block of the tile, K and V rings.
 #pragma once
 
 #include <math.h>
@@ -60,7 +63,7 @@ struct DecFp8Params {
     float *lse;
     float *part_o;           // [2 G, RC, d]: slot 2c: CTA c's unit begun by others; 2c + 1: one it begins and others end
     float *part_lse;         // [2 G, RC], log2 units
-    int *cuts;               // [4 + 4 G]: total tiles (64-bit), then per CTA its first unit: b, head and chunk, tile, tiles
+    int *cuts;               // [4 + 5 G]: total tiles (64-bit), then per CTA its first unit: b, head, chunk, tile, tiles
     int B, H, Hkv, Sq, R;    // R = H / Hkv * Sq rows per K/V head
     int chunks;              // of at most RC rows each
     int rows_per_chunk;
@@ -76,6 +79,9 @@ struct DecFp8Cfg {
     static constexpr int D = D_;
     static constexpr bool kFP16 = kFP16_;
     static constexpr int RC = RC_;                      // query rows per unit
+    static constexpr int RW = RC < 8 ? RC : 8;          // rows of one softmax warpgroup
+    static constexpr int NWG = RC / RW;                 // softmax warpgroups, each with all keys of a tile
+    static_assert(RW * NWG == RC, "whole warpgroups of rows");
     static constexpr int NP = kFP16 ? 3 : 2;            // e4m3 parts of q and of the weights
     static constexpr int N = (RC * NP + 15) / 16 * 16;  // columns: part-major, then rows
     static constexpr int BN = 128;                      // keys per tile
@@ -86,25 +92,29 @@ struct DecFp8Cfg {
     static constexpr int CHUNK_BYTES = BN * ROWB;
     static constexpr int Q_BYTES = N * D;               // one buffer of q's parts
     static constexpr int QCH = N * ROWB;
-    static constexpr int P_BYTES = N * 128;
+    static constexpr int P_BYTES = N * 128;             // one buffer of the weights' parts
     static constexpr uint32_t S_COL = 0;                // two buffers
-    static constexpr uint32_t O_COL = 2 * N;
-    static constexpr int COLS = (2 + NM) * N;
+    static constexpr uint32_t O_COL = 2 * N;            // two buffers of NM M blocks
+    static constexpr int COLS = (2 + 2 * NM) * N;
     static constexpr uint32_t TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    static constexpr int CTAS_PER_SM = (D <= 128 && TMEM_COLS <= 256) ? 2 : 1;
-    static constexpr int NUM_THREADS = 192;
-    static constexpr int MMA_WARP = 4;
-    static constexpr int TMA_WARP = 5;
-    // small arrays, in floats
-    static constexpr int F_RED = 0;                        // [2][4][RC + 1] tile maxima, largest |vs|
-    static constexpr int F_M = F_RED + 2 * 4 * (RC + 1);   // [4][RC] the tile's maxima, a copy per warp
-    static constexpr int F_AB = (F_M + 4 * RC + 1) / 2 * 2;  // [2][4][RC] float2: rescale of O, weight of the tile
-    static constexpr int F_C = F_AB + 2 * 4 * RC * 2;      // [2][RC] score multiplier
-    static constexpr int F_LAST = F_C + 2 * RC;            // [2][RC] last key the row sees (int)
-    static constexpr int F_L = F_LAST + 2 * RC;            // [4][RC] warps' sums
-    static constexpr int F_NUM = F_L + 4 * RC;
-    static constexpr int BUDGET = CTAS_PER_SM == 2 ? 113 * 1024 : 226 * 1024;
-    static constexpr int FIXED = 1024 + 2 * Q_BYTES + P_BYTES + F_NUM * 4 + 512;
+    static constexpr int CTAS_PER_SM = D == 64 && RC <= 4 ? 3 : (D <= 128 && TMEM_COLS <= 256 && NWG <= 2) ? 2 : 1;
+    static constexpr int MMA_WARP = 4 * NWG;
+    static constexpr int TMA_WARP = 4 * NWG + 1;
+    static constexpr int NUM_THREADS = 32 * (TMA_WARP + 1);
+    // small arrays of a warpgroup, in floats, rows padded to a multiple of four
+    static constexpr int RP = (RW + 3) / 4 * 4;
+    static constexpr int F_M = 0;                    // [4 warps] the tile's maxima
+    static constexpr int F_B = F_M + 4 * RP;         // [4 warps] 2^(tile's maximum - running maximum)
+    static constexpr int F_A = F_B + 4 * RP;         // [2][4 warps] rescale of what came before the tile
+    static constexpr int F_V = F_A + 8 * RP;         // [2][4 warps] weight of the tile's O
+    static constexpr int F_C = F_V + 8 * RP;         // [2] score multipliers
+    static constexpr int F_LAST = F_C + 2 * RP;      // [2] last key the row sees (int)
+    static constexpr int F_L = F_LAST + 2 * RP;      // [4 warps] sums
+    static constexpr int F_RED = F_L + 4 * RP;       // [2][4 warps][RW + 1] tile maxima, largest |vs|
+    static constexpr int F_WG = (F_RED + 2 * 4 * (RW + 1) + 3) / 4 * 4;
+    static constexpr int F_NUM = NWG * F_WG;
+    static constexpr int BUDGET = CTAS_PER_SM == 3 ? 75 * 1024 : CTAS_PER_SM == 2 ? 113 * 1024 : 226 * 1024;
+    static constexpr int FIXED = 1024 + 2 * Q_BYTES + 2 * P_BYTES + F_NUM * 4 + 512;
     static constexpr int SLOTS = (BUDGET - FIXED) / TILE;
     static constexpr int KST = SLOTS >= 12 ? 6 : (SLOTS + 1) / 2;
     static constexpr int VST = SLOTS >= 12 ? 6 : SLOTS / 2;
@@ -115,12 +125,12 @@ struct DecFp8Cfg {
     static constexpr int B_QFULL = B_VEMPTY + VST;  // [2]
     static constexpr int B_SFULL = B_QFULL + 2;     // [2]
     static constexpr int B_SFREE = B_SFULL + 2;     // [2]
-    static constexpr int B_PFULL = B_SFREE + 2;
-    static constexpr int B_OFULL = B_PFULL + 1;
-    static constexpr int B_DRAIN = B_OFULL + 1;
+    static constexpr int B_PFULL = B_SFREE + 2;     // [2]
+    static constexpr int B_OFULL = B_PFULL + 2;     // [2]
+    static constexpr int B_DRAIN = B_OFULL + 2;
     static constexpr int B_NEVER = B_DRAIN + 1;     // no arrivals (the stall test's wait)
     static constexpr int NUM_BARS = B_NEVER + 1;
-    static constexpr int SMEM_TILES = 2 * Q_BYTES + P_BYTES + (KST + VST) * TILE;
+    static constexpr int SMEM_TILES = 2 * Q_BYTES + 2 * P_BYTES + (KST + VST) * TILE;
     static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + F_NUM * 4 + NUM_BARS * 8 + 64;
     static_assert(VST >= 2, "rings of at least two tiles");
     static_assert(SMEM_BYTES <= BUDGET && SMEM_BYTES <= 232448, "shared memory overflow");
@@ -145,10 +155,10 @@ struct DecFp8Cfg {
 
 // A CTA's place in the line of tiles, stepped tile by tile.
 struct DecFp8It {
-    int b, hc, tile;  // request, K/V head * chunks + chunk, tile of the unit
-    int L, nt;        // the request's length and tiles
-    int next_len;     // the next request's length, loaded ahead
-    int left;         // tiles left, this one included
+    int b, kvh, chunk, tile;  // request, K/V head, chunk of rows, tile of the unit
+    int L, nt;                // the request's length and tiles
+    int next_len;             // the next request's length, loaded ahead
+    int left;                 // tiles left, this one included
 };
 
 __device__ __forceinline__ int dec_fp8_tiles(int L) { return max((L + 127) >> 7, 1); }
@@ -161,16 +171,28 @@ __device__ __forceinline__ void dec_fp8_step(const DecFp8Params &p, DecFp8It &it
     --it.left;
     if (++it.tile < it.nt) return;
     it.tile = 0;
-    if (++it.hc < p.Hkv * p.chunks) return;
-    it.hc = 0;
+    if (++it.chunk < p.chunks) return;
+    it.chunk = 0;
+    if (++it.kvh < p.Hkv) return;
+    it.kvh = 0;
     ++it.b;
     it.L = it.next_len;
     it.nt = dec_fp8_tiles(it.L);
     it.next_len = dec_fp8_len(p, it.b + 1);
 }
 
+// The first tile of the unit behind this one's.  (Its next_len is not loaded
+// where the step does not need it: no use of the result waits for that.)
+__device__ __forceinline__ DecFp8It dec_fp8_next_unit(const DecFp8Params &p, DecFp8It it) {
+    it.left -= it.nt - 1 - it.tile;
+    it.tile = it.nt - 1;
+    dec_fp8_step(p, it);
+    return it;
+}
+
 // Where this CTA's tiles begin: prefix sums over the requests' tiles, by all
-// threads of the CTA.  `scratch` holds 16 long longs.
+// threads of the CTA.  `scratch` holds THREADS / 32 + 2 long
+// longs.
 template <int THREADS>
 __device__ DecFp8It dec_fp8_begin(const DecFp8Params &p, long long *scratch) {
     constexpr int W = THREADS / 32;
@@ -186,7 +208,7 @@ __device__ DecFp8It dec_fp8_begin(const DecFp8Params &p, long long *scratch) {
     total *= hc;
     const long long G = min((long long)gridDim.x, total), c = blockIdx.x;
     DecFp8It it;
-    it.b = it.hc = it.tile = it.L = it.nt = it.next_len = it.left = 0;
+    it.b = it.kvh = it.chunk = it.tile = it.L = it.nt = it.next_len = it.left = 0;
     if (c == 0 && tid == 0) *reinterpret_cast<long long *>(p.cuts) = total;
     if (c >= G) return it;
     const long long lo = c * total / G, hi = (c + 1) * total / G;
@@ -222,15 +244,18 @@ __device__ DecFp8It dec_fp8_begin(const DecFp8Params &p, long long *scratch) {
     it.nt = dec_fp8_tiles(it.L);
     it.next_len = dec_fp8_len(p, it.b + 1);
     const long long off = lo - scratch[W + 1] * hc;
-    it.hc = (int)(off / it.nt);
-    it.tile = (int)(off - (long long)it.hc * it.nt);
+    const int unit = (int)(off / it.nt);
+    it.tile = (int)(off - (long long)unit * it.nt);
+    it.kvh = unit / p.chunks;
+    it.chunk = unit - it.kvh * p.chunks;
     it.left = (int)(hi - lo);
     if (tid == 0) {
-        int *cut = p.cuts + 4 + 4 * c;
+        int *cut = p.cuts + 4 + 5 * c;
         cut[0] = it.b;
-        cut[1] = it.hc;
-        cut[2] = it.tile;
-        cut[3] = it.nt;
+        cut[1] = it.kvh;
+        cut[2] = it.chunk;
+        cut[3] = it.tile;
+        cut[4] = it.nt;
     }
     return it;
 }
@@ -257,7 +282,7 @@ __device__ void dec_fp8_tma_role(const DecFp8Params &p, DecFp8It it, uint8_t *sK
     bool ok = true;
     int phys = look_up(it);
     for (int t = 0; it.left > 0; ++t) {
-        const int kvh = it.hc / p.chunks;
+        const int kvh = it.kvh;
         dec_fp8_step(p, it);
         const int next = look_up(it);
         const int ks = t % C::KST, vs = t % C::VST;
@@ -342,21 +367,22 @@ __device__ void dec_fp8_mma_role(const DecFp8Params &p, DecFp8It it, uint8_t *sQ
         if (t >= 1) {
             const int tp = t - 1, vs = tp % C::VST;
             if (!wait_warp(bar_addr(bars, C::B_VFULL + vs), (tp / C::VST) & 1, ctl, 76) ||
-                !wait_warp(bar_addr(bars, C::B_PFULL), tp & 1, ctl, 77)) {
+                !wait_warp(bar_addr(bars, C::B_PFULL + (tp & 1)), (tp >> 1) & 1, ctl, 77)) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
             if (leader) {
-                const uint32_t va = ptx::smem_addr(sV + vs * C::TILE), pa = ptx::smem_addr(sP);
+                const uint32_t va = ptx::smem_addr(sV + vs * C::TILE), pa = ptx::smem_addr(sP + (tp & 1) * C::P_BYTES);
+                const uint32_t o_col = tmem + C::O_COL + (tp & 1) * C::NM * C::N;
 #pragma unroll
                 for (int m = 0; m < C::NM; ++m)
 #pragma unroll
                     for (int kk = 0; kk < C::BN / 32; ++kk)
-                        ptx::mma_ss_f8(tmem + C::O_COL + m * C::N,
+                        ptx::mma_ss_f8(o_col + m * C::N,
                                        C::desc_v(va + m * C::CHUNK_BYTES + kk * 32 * C::ROWB),
                                        smem_desc(pa + kk * 32, 16), kIdescO, kk > 0 ? 1u : 0u);
-                ptx::mma_commit(bar_addr(bars, C::B_OFULL));
+                ptx::mma_commit(bar_addr(bars, C::B_OFULL + (tp & 1)));
                 ptx::mma_commit(bar_addr(bars, C::B_VEMPTY + vs));
             }
             __syncwarp();
@@ -386,12 +412,13 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[G]) {
     }
 }
 
-// The sum of the NP part columns of rows [g0, g0 + G) of this lane.
+// The sums of the NP part columns of G rows of this lane, `col` the first part
+// of the first of them.
 template <class C, int G>
-__device__ __forceinline__ void dec_fp8_read(uint32_t col, int g0, float (&x)[G]) {
+__device__ __forceinline__ void dec_fp8_read(uint32_t col, float (&x)[G]) {
     uint32_t part[C::NP][G];
 #pragma unroll
-    for (int j = 0; j < C::NP; ++j) tmem_ld_cols<G>(col + j * C::RC + g0, part[j]);
+    for (int j = 0; j < C::NP; ++j) tmem_ld_cols<G>(col + j * C::RC, part[j]);
     ptx::tmem_wait_ld();
 #pragma unroll
     for (int j = 0; j < C::NP; ++j) ptx::reg_fence<G>(part[j]);
@@ -404,67 +431,130 @@ __device__ __forceinline__ void dec_fp8_read(uint32_t col, int g0, float (&x)[G]
     }
 }
 
-// Two values as NP parts: codes[j] holds part j of a in byte 0, of b in byte 1.
+// Two values (at most 256) as NP parts: codes[j] holds part j of a in byte 0,
+// of b in byte 1.  They are rounded to fp16 first, whose 11 bits three parts
+// hold, and every later step is exact in fp16: what a part leaves is at most
+// half a step of it, 2^-4 of the value before.
 template <int NP>
 __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t (&codes)[NP]) {
+    const __half2 k16 = __half2half2(__ushort_as_half(0x4C00));  // 16
+    const uint32_t w = ptx::pack_f16x2(a, b);
+    __half2 h = *reinterpret_cast<const __half2 *>(&w);
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
         uint16_t two;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(*reinterpret_cast<const uint32_t *>(&h)));
         codes[j] = two;
         if (j + 1 < NP) {
-            const float2 back = unpack_e4m3x2(two);
-            a = (a - back.x) * 16.f;
-            b = (b - back.y) * 16.f;
+            uint32_t back;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(two));
+            h = __hmul2(__hsub2(h, *reinterpret_cast<const __half2 *>(&back)), k16);
         }
     }
 }
 
-__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// The largest of the warp's values (NaN only if all are), in every lane.
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// Rows of unit (b, hc): the packed rows' first index in [B, H, Sq] and count.
-__device__ __forceinline__ size_t dec_fp8_row0(const DecFp8Params &p, int b, int hc, int *rows) {
-    const int kvh = hc / p.chunks, chunk = hc - kvh * p.chunks;
+// r consecutive floats of shared memory (16-byte aligned for r >= 4).
+template <int R>
+__device__ __forceinline__ void lds_row(const float *src, float (&dst)[R]) {
+    if constexpr (R % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < R; i += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src + i);
+            dst[i] = v.x;
+            dst[i + 1] = v.y;
+            dst[i + 2] = v.z;
+            dst[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) dst[i] = src[i];
+    }
+}
+
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
+    // (no memory clobber: the loads of later rows may pass; the proxy fence
+    // behind the last store is a volatile asm as well and stays behind it)
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v));
+}
+
+// Rows of a unit: the packed rows' first index in [B, H, Sq] and count.
+__device__ __forceinline__ size_t dec_fp8_row0(const DecFp8Params &p, int b, int kvh, int chunk, int *rows) {
     *rows = min(p.rows_per_chunk, p.R - chunk * p.rows_per_chunk);
     return ((size_t)b * p.Hkv + kvh) * p.R + (size_t)chunk * p.rows_per_chunk;
 }
 
-// q's parts of a unit into shared memory (K-major, swizzled), its rows' score
-// multipliers and last keys.  Each of the four warps takes every fourth row.
-// A row is scaled by a power of two so that its largest component is in
-// [128, 256); a row with an infinity or NaN becomes NaN codes.
+// A warpgroup's q rows of a unit, 16-bit, each of its four warps every fourth
+// row, a lane D / 32 adjacent components.
 template <class C>
-__device__ void dec_fp8_load_q(const DecFp8Params &p, int b, int hc, int L, uint8_t *sQ, float *mul, int *last) {
-    const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+struct DecFp8Q {
+    static constexpr int PL = C::D / 32;        // components per lane
+    static constexpr int NR = (C::RW + 3) / 4;  // rows per warp
+    uint32_t raw[NR][PL / 2];
+};
+
+template <class C>
+__device__ __forceinline__ void dec_fp8_load_q(const DecFp8Params &p, const DecFp8It &u, DecFp8Q<C> &q) {
+    constexpr int PL = DecFp8Q<C>::PL;
+    const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5 & 3, wg = (int)threadIdx.x >> 7;
     int rows;
-    const size_t row0 = dec_fp8_row0(p, b, hc, &rows);
-    const int r_first = (hc % p.chunks) * p.rows_per_chunk;
-    constexpr int PL = C::D / 32;  // components per lane
-    for (int r = warp; r < C::RC; r += 4) {
+    const size_t row0 = dec_fp8_row0(p, u.b, u.kvh, u.chunk, &rows);
+#pragma unroll
+    for (int i = 0; i < DecFp8Q<C>::NR; ++i) {
+        const int r = wg * C::RW + warp + 4 * i;
+        const uint16_t *src = p.q + (row0 + (r < rows ? r : 0)) * C::D + lane * PL;
+        if constexpr (PL == 8) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(src);
+            q.raw[i][0] = w.x, q.raw[i][1] = w.y, q.raw[i][2] = w.z, q.raw[i][3] = w.w;
+        } else if constexpr (PL == 4) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(src);
+            q.raw[i][0] = w.x, q.raw[i][1] = w.y;
+        } else {
+            q.raw[i][0] = *reinterpret_cast<const uint32_t *>(src);
+        }
+    }
+}
+
+// q's parts into shared memory (K-major, swizzled), its rows' score multipliers
+// and last keys.  A row is scaled by a power of two so that its largest
+// component is in [128, 256); a row with an infinity or NaN becomes NaN codes.
+template <class C>
+__device__ __forceinline__ void dec_fp8_put_q(const DecFp8Params &p, const DecFp8It &u, const DecFp8Q<C> &q, uint8_t *sQ,
+                                              float *mul, int *last) {
+    constexpr int PL = DecFp8Q<C>::PL;
+    const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5 & 3, wg = (int)threadIdx.x >> 7;
+    const int r_first = u.chunk * p.rows_per_chunk, rows = min(p.rows_per_chunk, p.R - r_first);
+#pragma unroll
+    for (int i = 0; i < DecFp8Q<C>::NR; ++i) {
+        const int in_wg = warp + 4 * i, r = wg * C::RW + in_wg;
+        if (in_wg >= C::RW) break;
         float x[PL];
         float top = 0.f;
         bool fine = true;
 #pragma unroll
         for (int e = 0; e < PL; e += 2) {
-            uint32_t w = 0;
-            if (r < rows) w = *reinterpret_cast<const uint32_t *>(p.q + (row0 + r) * C::D + lane * PL + e);
-            const float2 f = unpack16<C::kFP16>(w);
+            const float2 f = unpack16<C::kFP16>(r < rows ? q.raw[i][e / 2] : 0u);
             x[e] = f.x;
             x[e + 1] = f.y;
             fine = fine && isfinite(f.x) && isfinite(f.y);
             top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = warp_max(top);
         fine = __all_sync(0xffffffffu, fine);
-        // 2^(7 - exponent of top); the exponents stay within fp32's normal range for any 16-bit top
-        const int ex = max((int)(__float_as_uint(top) >> 23), 20);  // biased
-        const float up = __uint_as_float((uint32_t)min(261 - ex, 254) << 23);
+        // 2^(7 - exponent of top) and its inverse: with the exponent at least
+        // 2^-107 both are normal for any 16-bit top
+        const uint32_t ex = max(__float_as_uint(top) >> 23, 20u);  // biased
+        const float up = __uint_as_float((261u - min(ex, 254u)) << 23), down = __uint_as_float((min(ex, 254u) - 7u) << 23);
         if (lane == 0) {
-            mul[r] = p.scale_log2 / up;
-            last[r] = p.mask_kind == kMaskCausal ? L - p.Sq + (r_first + r) % p.Sq : L - 1;
+            // positive, so that a hidden key's -inf stays -inf: a zero scale runs as 2^-126
+            mul[in_wg] = fmaxf(p.scale_log2 * down, 1.17549435e-38f);
+            last[in_wg] = p.mask_kind != kMaskCausal ? u.L - 1 : p.Sq == 1 ? u.L - 1 : u.L - p.Sq + (r_first + r) % p.Sq;
         }
 #pragma unroll
         for (int e = 0; e < PL; e += 2) {
@@ -482,168 +572,188 @@ __device__ void dec_fp8_load_q(const DecFp8Params &p, int b, int hc, int L, uint
     }
 }
 
+// acc = acc * alpha + O * weight over a warpgroup's rows, O read from its buffer.
+template <class C>
+__device__ __forceinline__ void dec_fp8_accumulate(uint32_t o_col, const float *alpha, const float *weight,
+                                                   float (&acc)[C::NM][C::RW]) {
+    float a[C::RW], w[C::RW];
+    lds_row<C::RW>(alpha, a);
+    lds_row<C::RW>(weight, w);
+#pragma unroll
+    for (int m = 0; m < C::NM; ++m) {
+        float o[C::RW];
+        dec_fp8_read<C, C::RW>(o_col + m * C::N, o);
+#pragma unroll
+        for (int i = 0; i < C::RW; ++i) acc[m][i] = fmaf(acc[m][i], a[i], o[i] * w[i]);
+    }
+}
+
 template <class C>
 __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t *sQ, uint8_t *sP, uint8_t *sV,
                                      float *sF, uint32_t bars, uint32_t tmem, Ctl *ctl) {
-    constexpr int RC = C::RC, G = RC < 8 ? RC : 8;
-    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t p_addr = ptx::smem_addr(sP);
-    float *sM = sF + C::F_M + warp * RC;
+    constexpr int RW = C::RW, RP = C::RP;
+    const int wg = (int)threadIdx.x >> 7, tid = (int)threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
+    sF += wg * C::F_WG;
+    // this warp's TMEM lanes, from the warpgroup's first column of a part
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16) + wg * RW;
+    // this thread's byte of the warpgroup's row n of the weights: 16-byte chunk (tid >> 4) ^ (n & 7)
+    const uint32_t p_addr = ptx::smem_addr(sP) + (uint32_t)(wg * RW * 128 + tid);
     if (it.left <= 0) return;
 
-    // what this thread's key of a tile needs of its block: entry, then scales,
-    // looked up one and two tiles ahead (`ahead` runs in front of `it`)
-    auto entry = [&](const DecFp8It &i) -> int {
-        const int key = i.tile * C::BN + tid;
-        if (i.left <= 0 || key >= i.L) return -1;
-        const int e = p.block_table[(size_t)i.b * p.max_blocks + (key >> p.bs_log2)];
-        return e >= 0 && e < p.num_blocks ? e : -1;
-    };
+    // What this thread's key of a tile needs of its block: the table's entry,
+    // then the scales, loaded three and two tiles ahead (`ahead` runs in front
+    // of `it`): with the memory busy a load takes more than a tile's time.  The
+    // loads are unconditional, at places clamped into the arrays, and judged
+    // only when they are used, so that none is waited for early.
     DecFp8It ahead = it;
-    int phys = entry(ahead);
-    float ks_next = phys >= 0 ? p.k_scale[(size_t)phys * p.Hkv + ahead.hc / p.chunks] : 0.f;
-    float vs_next = phys >= 0 ? p.v_scale[(size_t)phys * p.Hkv + ahead.hc / p.chunks] : 0.f;
-    if (ahead.left > 0) dec_fp8_step(p, ahead);
-    phys = entry(ahead);
+    int entry;               // of `ahead`'s tile, as loaded
+    bool entry_seen;         // its key exists
+    float ks_next, vs_next, ks_far, vs_far;  // of the next tile and the one behind it, as loaded
+    bool next_seen, far_seen;
+    auto load_entry = [&] {
+        const int key = ahead.tile * C::BN + tid;
+        entry_seen = ahead.left > 0 && key < ahead.L;
+        entry = p.block_table[(size_t)min(ahead.b, p.B - 1) * p.max_blocks + min(key >> p.bs_log2, p.max_blocks - 1)];
+    };
+    auto load_scales = [&] {
+        far_seen = entry_seen && entry >= 0 && entry < p.num_blocks;
+        const size_t bh = (size_t)(far_seen ? entry : 0) * p.Hkv + ahead.kvh;
+        ks_far = p.k_scale[bh];
+        vs_far = p.v_scale[bh];
+        if (ahead.left > 0) dec_fp8_step(p, ahead);
+    };
 
-    // units are numbered from 0 in this CTA; unit u's q sits in buffer u & 1
-    dec_fp8_load_q<C>(p, it.b, it.hc, it.L, sQ, sF + C::F_C, reinterpret_cast<int *>(sF + C::F_LAST));
+    // Units are numbered from 0 in this CTA; unit u's q sits in buffer u & 1.
+    // Its rows are loaded one unit before they are split into parts, and split
+    // one unit before they are used.
+    DecFp8Q<C> q;
+    dec_fp8_load_q<C>(p, it, q);
+    load_entry();
+    load_scales();
+    load_entry();
+    dec_fp8_put_q<C>(p, it, q, sQ, sF + C::F_C, reinterpret_cast<int *>(sF + C::F_LAST));
     ptx::fence_proxy_async_smem();
     ptx::mbar_arrive(bar_addr(bars, C::B_QFULL));
-    ptx::named_bar_sync(3, 128);  // every warp's rows' multipliers and last keys are in place
+    ks_next = ks_far, vs_next = vs_far, next_seen = far_seen;
+    load_scales();
+    load_entry();
+    if (it.left > it.nt - it.tile) dec_fp8_load_q<C>(p, dec_fp8_next_unit(p, it), q);
+    ptx::named_bar_sync(9 + wg, 128);  // every warp's rows' multipliers and last keys are in place
 
-    float acc[C::NM][RC], l[RC];
+    float acc[C::NM][RW], l[RW];
     float m_run = -INFINITY;  // lane r: row r's running maximum
-    float v_prev = 0.f;       // the tile before: its largest scale / 256, the weight of its O
     bool begun_here = it.tile == 0;
     bool first = true, bad = false;
     int unit = 0;
     for (int t = 0;; ++t) {
-        const float *mul = sF + C::F_C + (unit & 1) * RC;
-        const int *last = reinterpret_cast<const int *>(sF + C::F_LAST) + (unit & 1) * RC;
+        const float *mul = sF + C::F_C + (unit & 1) * RP;
+        const int *last = reinterpret_cast<const int *>(sF + C::F_LAST) + (unit & 1) * RP;
         const bool ends = it.tile + 1 == it.nt || it.left == 1;  // the unit, or this CTA's part of it
         if (first) {
 #pragma unroll
-            for (int r = 0; r < RC; ++r) {
+            for (int r = 0; r < RW; ++r) {
                 l[r] = 0.f;
 #pragma unroll
                 for (int m = 0; m < C::NM; ++m) acc[m][r] = 0.f;
             }
             m_run = -INFINITY;
             // the next unit's q, while this unit's first scores are on their way
-            const int to_end = it.nt - it.tile;
-            if (it.left > to_end) {
-                DecFp8It next = it;
-                next.tile = it.nt - 1;
-                dec_fp8_step(p, next);
+            if (it.left > it.nt - it.tile) {
                 const int nb = (unit + 1) & 1;
-                dec_fp8_load_q<C>(p, next.b, next.hc, next.L, sQ + nb * C::Q_BYTES, sF + C::F_C + nb * RC,
-                                  reinterpret_cast<int *>(sF + C::F_LAST) + nb * RC);
+                DecFp8It coming = dec_fp8_next_unit(p, it);
+                dec_fp8_put_q<C>(p, coming, q, sQ + nb * C::Q_BYTES, sF + C::F_C + nb * RP,
+                                 reinterpret_cast<int *>(sF + C::F_LAST) + nb * RP);
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(bar_addr(bars, C::B_QFULL + nb));
+                if (coming.left > coming.nt) dec_fp8_load_q<C>(p, dec_fp8_next_unit(p, coming), q);
             }
         }
-        const float ks = ks_next, vs = vs_next;
-        ks_next = phys >= 0 ? p.k_scale[(size_t)phys * p.Hkv + ahead.hc / p.chunks] : 0.f;
-        vs_next = phys >= 0 ? p.v_scale[(size_t)phys * p.Hkv + ahead.hc / p.chunks] : 0.f;
-        if (ahead.left > 0) dec_fp8_step(p, ahead);
-        phys = entry(ahead);
+        const float ks = next_seen ? ks_next : 0.f, vs = next_seen ? vs_next : 0.f;
+        ks_next = ks_far, vs_next = vs_far, next_seen = far_seen;
+        load_scales();
+        load_entry();
 
         const int b = t & 1, k0 = it.tile * C::BN, key = k0 + tid;
         bad = bad || !wait_warp(bar_addr(bars, p.stall_test && t == 0 ? C::B_NEVER : C::B_SFULL + b), (t >> 1) & 1, ctl, 78);
-        float x[RC];
-        float *red = sF + C::F_RED + b * 4 * (RC + 1) + warp * (RC + 1);
+        float x[RW];  // scores without their row's multiplier
+        float *red = sF + C::F_RED + (b * 4 + warp) * (RW + 1);
         if (!bad) {
             ptx::tc_fence_after();
+            dec_fp8_read<C, RW>(lane_base + C::S_COL + b * C::N, x);
 #pragma unroll
-            for (int g = 0; g < RC; g += G) {
-                float s[G];
-                dec_fp8_read<C, G>(lane_base + C::S_COL + b * C::N, g, s);
-#pragma unroll
-                for (int i = 0; i < G; ++i) x[g + i] = s[i] * (mul[g + i] * ks);
-            }
+            for (int r = 0; r < RW; ++r) x[r] *= ks;
             ptx::tc_fence_before();
             ptx::mbar_arrive(bar_addr(bars, C::B_SFREE + b));
             // hidden keys: past the row's last (a select, so nothing of theirs leaks)
             const int seen_by_all = p.mask_kind == kMaskCausal ? it.L - p.Sq : it.L - 1;
             if (k0 + C::BN - 1 > seen_by_all) {
 #pragma unroll
-                for (int r = 0; r < RC; ++r)
+                for (int r = 0; r < RW; ++r)
                     if (key > last[r]) x[r] = -INFINITY;
             }
             float mine = -INFINITY;
 #pragma unroll
-            for (int r = 0; r < RC; ++r) {
-                float top = x[r];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int r = 0; r < RW; ++r) {
+                const float top = warp_max(x[r]);
                 if (lane == r) mine = top;
             }
-            float vtop = fabsf(vs);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-            if (lane < RC) red[lane] = mine;
-            if (lane == 0) red[RC] = vtop;
+            const float vtop = warp_max(fabsf(vs));
+            if (lane < RW) red[lane] = mine;
+            if (lane == 0) red[RW] = vtop;
         }
-        // (a warp whose wait ran out still comes here, and all leave together)
-        if (ptx::named_bar_any(1, 128, bad)) return;
-        const float *all = sF + C::F_RED + b * 4 * (RC + 1);
-        const float vtop = fmaxf(fmaxf(all[RC], all[2 * RC + 1]), fmaxf(all[3 * RC + 2], all[4 * RC + 3]));
-        float2 *ab = reinterpret_cast<float2 *>(sF + C::F_AB) + (b * 4 + warp) * RC;
-        if (lane < RC) {
-            const float m_tile = fmaxf(fmaxf(all[lane], all[RC + 1 + lane]), fmaxf(all[2 * RC + 2 + lane], all[3 * RC + 3 + lane]));
+        // (a warp whose wait ran out still comes here, and the warpgroup leaves together)
+        if (ptx::named_bar_any(1 + wg, 128, bad)) return;
+        const float *all = sF + C::F_RED + b * 4 * (RW + 1);
+        const float vtop = fmaxf(fmaxf(all[RW], all[2 * RW + 1]), fmaxf(all[3 * RW + 2], all[4 * RW + 3]));
+        float *sM = sF + C::F_M + warp * RP, *sB = sF + C::F_B + warp * RP;
+        float *sA = sF + C::F_A + (b * 4 + warp) * RP, *sW = sF + C::F_V + (b * 4 + warp) * RP;
+        if (lane < RW) {
+            const float top = fmaxf(fmaxf(all[lane], all[RW + 1 + lane]), fmaxf(all[2 * RW + 2 + lane], all[3 * RW + 3 + lane]));
+            const float m_tile = top * mul[lane];
+            const bool none = m_tile == -INFINITY;  // the row sees no key of the tile
             const float m_new = fmaxf(m_run, m_tile), m_use = m_new == -INFINITY ? 0.f : m_new;
-            sM[lane] = m_tile == -INFINITY ? 0.f : m_tile;
-            ab[lane] = make_float2(ptx::ex2_approx(m_run - m_use), m_tile == -INFINITY ? 0.f : ptx::ex2_approx(m_tile - m_use));
+            const float beta = none ? 0.f : ptx::ex2_approx(m_tile - m_use);
+            sM[lane] = none ? 0.f : m_tile;
+            sB[lane] = beta;
+            sA[lane] = ptx::ex2_approx(m_run - m_use);
+            sW[lane] = beta * (vtop * 0.00390625f);  // O holds 256 times its weights over vtop
             m_run = m_new;
         }
         __syncwarp();
-        // O of the tile before (of this unit): P and O are free again after it
-        if (!first) {
-            bad = !wait_warp(bar_addr(bars, C::B_OFULL), (t - 1) & 1, ctl, 79);
-            if (!bad) {
-                ptx::tc_fence_after();
-                const float2 *abp = reinterpret_cast<const float2 *>(sF + C::F_AB) + ((b ^ 1) * 4 + warp) * RC;
-#pragma unroll
-                for (int m = 0; m < C::NM; ++m)
-#pragma unroll
-                    for (int g = 0; g < RC; g += G) {
-                        float o[G];
-                        dec_fp8_read<C, G>(lane_base + C::O_COL + m * C::N, g, o);
-#pragma unroll
-                        for (int i = 0; i < G; ++i) acc[m][g + i] = fmaf(acc[m][g + i], abp[g + i].x, o[i] * (abp[g + i].y * v_prev));
-                    }
-                ptx::tc_fence_before();
-            }
-        }
-        v_prev = vtop * 0.00390625f;
-        if (!bad) {
-            // weights: of the sum in fp32, of V (times the block's scale over
-            // the tile's largest, times 256) as parts
+        // weights: of the sum in fp32, of V (times the block's scale over the
+        // tile's largest, times 256) as parts.  P V of tile t - 2 is done (its
+        // O has been read), so its buffer is free.
+        {
             const float share = vtop > 0.f ? vs / vtop * 256.f : 0.f;
+            const uint32_t buf = p_addr + b * C::P_BYTES;
+            constexpr int S = RW < 4 ? RW : 4;  // rows at a time
 #pragma unroll
-            for (int r = 0; r < RC; r += 2) {
-                const float p0 = ptx::ex2_approx(x[r] - sM[r]);
-                const float2 w0 = ab[r];
-                l[r] = fmaf(l[r], w0.x, p0 * w0.y);
-                float p1 = 0.f;
-                if (r + 1 < RC) {
-                    p1 = ptx::ex2_approx(x[(r + 1) % RC] - sM[(r + 1) % RC]);
-                    const float2 w1 = ab[(r + 1) % RC];
-                    l[(r + 1) % RC] = fmaf(l[(r + 1) % RC], w1.x, p1 * w1.y);
+            for (int g = 0; g < RW; g += S) {
+                float m[S], c[S], a[S], e[S], v[(S + 1) / 2 * 2];
+                lds_row<S>(sM + g, m);
+                lds_row<S>(mul + g, c);
+                lds_row<S>(sA + g, a);
+                lds_row<S>(sB + g, e);
+#pragma unroll
+                for (int r = 0; r < S; ++r) {
+                    const float w = ptx::ex2_approx(fmaf(x[g + r], c[r], -m[r]));
+                    l[g + r] = fmaf(l[g + r], a[r], w * e[r]);
+                    v[r] = w * share;
                 }
-                uint32_t codes[C::NP];
-                split_e4m3<C::NP>(p0 * share, p1 * share, codes);
+                if constexpr (S == 1) v[1] = 0.f;
 #pragma unroll
-                for (int j = 0; j < C::NP; ++j) {
-                    const int n = j * RC + r;
-                    st_shared_u8(p_addr + n * 128 + (((tid >> 4) ^ (n & 7)) << 4) + (tid & 15), codes[j]);
-                    if (r + 1 < RC)
-                        st_shared_u8(p_addr + (n + 1) * 128 + (((tid >> 4) ^ ((n + 1) & 7)) << 4) + (tid & 15), codes[j] >> 8);
+                for (int r = 0; r < S; r += 2) {
+                    uint32_t codes[C::NP];
+                    split_e4m3<C::NP>(v[r], v[r + 1], codes);
+#pragma unroll
+                    for (int j = 0; j < C::NP; ++j) {
+                        const int n = j * C::RC + g + r;  // (the warpgroup's first row is 0 modulo 8)
+                        st_shared_u8((buf ^ (uint32_t)((n & 7) << 4)) + n * 128, codes[j]);
+                        if (r + 1 < S) st_shared_u8((buf ^ (uint32_t)(((n + 1) & 7) << 4)) + (n + 1) * 128, codes[j] >> 8);
+                    }
                 }
             }
-            if (k0 + C::BN > it.L && (it.L & ((1 << p.bs_log2) - 1)) != 0 && key >= it.L) {
+            if (wg == 0 && k0 + C::BN > it.L && (it.L & ((1 << p.bs_log2) - 1)) != 0 && key >= it.L) {
                 // a row of V past the request's keys meets weight 0, but junk (NaN)
                 // in it would not vanish: zero it
                 const int slot = t % C::VST;
@@ -658,51 +768,55 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
             bad = __any_sync(0xffffffffu, bad);
         }
         ptx::fence_proxy_async_smem();
-        if (!bad) ptx::mbar_arrive(bar_addr(bars, C::B_PFULL));
+        ptx::tc_fence_before();
+        if (!bad) ptx::mbar_arrive(bar_addr(bars, C::B_PFULL + b));
+        // O of the tile before (of this unit), while P V of this one runs
+        if (!first) {
+            bad = bad || !wait_warp(bar_addr(bars, C::B_OFULL + (b ^ 1)), ((t - 1) >> 1) & 1, ctl, 79);
+            if (!bad) {
+                ptx::tc_fence_after();
+                dec_fp8_accumulate<C>(lane_base + C::O_COL + (b ^ 1) * C::NM * C::N, sF + C::F_A + ((b ^ 1) * 4 + warp) * RP,
+                                      sF + C::F_V + ((b ^ 1) * 4 + warp) * RP, acc);
+                ptx::tc_fence_before();
+            }
+        }
         first = false;
 
         if (ends) {
             // the unit's last O, its sums, and the rows out
-            bad = bad || !wait_warp(bar_addr(bars, C::B_OFULL), t & 1, ctl, 81);
+            bad = bad || !wait_warp(bar_addr(bars, C::B_OFULL + b), (t >> 1) & 1, ctl, 81);
             if (!bad) {
                 ptx::tc_fence_after();
-#pragma unroll
-                for (int m = 0; m < C::NM; ++m)
-#pragma unroll
-                    for (int g = 0; g < RC; g += G) {
-                        float o[G];
-                        dec_fp8_read<C, G>(lane_base + C::O_COL + m * C::N, g, o);
-#pragma unroll
-                        for (int i = 0; i < G; ++i) acc[m][g + i] = fmaf(acc[m][g + i], ab[g + i].x, o[i] * (ab[g + i].y * v_prev));
-                    }
+                dec_fp8_accumulate<C>(lane_base + C::O_COL + b * C::NM * C::N, sA, sW, acc);
                 ptx::tc_fence_before();
             }
             float mine = 0.f;
 #pragma unroll
-            for (int r = 0; r < RC; ++r) {
+            for (int r = 0; r < RW; ++r) {
                 float s = l[r];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
                 if (lane == r) mine = s;
             }
             float *sL = sF + C::F_L;
-            if (lane < RC) sL[warp * RC + lane] = mine;
-            if (ptx::named_bar_any(2, 128, bad)) return;
+            if (lane < RW) sL[warp * RP + lane] = mine;
+            if (ptx::named_bar_any(5 + wg, 128, bad)) return;
             int rows;
-            const size_t row0 = dec_fp8_row0(p, it.b, it.hc, &rows);
+            const size_t row0 = dec_fp8_row0(p, it.b, it.kvh, it.chunk, &rows);
             const bool whole = begun_here && it.tile + 1 == it.nt;
             const size_t slot = 2 * (size_t)blockIdx.x + (begun_here ? 1 : 0);
-            if (warp == 0 && lane < RC && lane < rows) {
-                const float sum = (sL[lane] + sL[RC + lane]) + (sL[2 * RC + lane] + sL[3 * RC + lane]);
+            rows -= wg * RW;  // (0 or less: the warpgroup has none of them)
+            if (warp == 0 && lane < RW && lane < rows) {
+                const float sum = (sL[lane] + sL[RP + lane]) + (sL[2 * RP + lane] + sL[3 * RP + lane]);
                 // (a NaN sum is no empty row)
                 const float lse2 = sum == 0.f ? -INFINITY : m_run + __log2f(sum);
-                if (whole) p.lse[row0 + lane] = lse2 * kLn2;
-                else p.part_lse[slot * RC + lane] = lse2;
+                if (whole) p.lse[row0 + wg * RW + lane] = lse2 * kLn2;
+                else p.part_lse[slot * C::RC + wg * RW + lane] = lse2;
             }
 #pragma unroll
-            for (int r = 0; r < RC; ++r) {
+            for (int r = 0; r < RW; ++r) {
                 if (r >= rows) break;
-                const float sum = (sL[r] + sL[RC + r]) + (sL[2 * RC + r] + sL[3 * RC + r]);
+                const float sum = (sL[r] + sL[RP + r]) + (sL[2 * RP + r] + sL[3 * RP + r]);
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
                 for (int m = 0; m < C::NM; ++m) {
@@ -710,9 +824,9 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
                     if (c >= C::D) continue;
                     const float o = acc[m][r] * inv;
                     if (whole)
-                        static_cast<uint16_t *>(p.o)[(row0 + r) * C::D + c] = (uint16_t)pack2b<C::kFP16>(o, 0.f);
+                        static_cast<uint16_t *>(p.o)[(row0 + wg * RW + r) * C::D + c] = (uint16_t)pack2b<C::kFP16>(o, 0.f);
                     else
-                        p.part_o[(slot * RC + r) * C::D + c] = o;
+                        p.part_o[(slot * C::RC + wg * RW + r) * C::D + c] = o;
                 }
             }
             if (it.left == 1) return;
@@ -735,10 +849,10 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     uint8_t *sV = sK + C::KST * C::TILE;
     uint8_t *sQ = sV + C::VST * C::TILE;
     uint8_t *sP = sQ + 2 * C::Q_BYTES;
-    uint64_t *bar_mem = reinterpret_cast<uint64_t *>(sP + C::P_BYTES);
+    uint64_t *bar_mem = reinterpret_cast<uint64_t *>(sP + 2 * C::P_BYTES);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bar_mem + C::NUM_BARS);
     Ctl *ctl = reinterpret_cast<Ctl *>(tmem_holder + 2);
-    float *sF = reinterpret_cast<float *>(ctl + 2);
+    float *sF = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ctl + 1) + 15) & ~static_cast<uintptr_t>(15));
     const uint32_t bars = ptx::smem_addr(bar_mem);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
 
@@ -752,12 +866,12 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
             ptx::mbar_init(bar_addr(bars, C::B_VEMPTY + s), 1);
         }
         for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(bar_addr(bars, C::B_QFULL + b), 128);
+            ptx::mbar_init(bar_addr(bars, C::B_QFULL + b), 128 * C::NWG);
             ptx::mbar_init(bar_addr(bars, C::B_SFULL + b), 1);
-            ptx::mbar_init(bar_addr(bars, C::B_SFREE + b), 128);
+            ptx::mbar_init(bar_addr(bars, C::B_SFREE + b), 128 * C::NWG);
+            ptx::mbar_init(bar_addr(bars, C::B_PFULL + b), 128 * C::NWG);
+            ptx::mbar_init(bar_addr(bars, C::B_OFULL + b), 1);
         }
-        ptx::mbar_init(bar_addr(bars, C::B_PFULL), 128);
-        ptx::mbar_init(bar_addr(bars, C::B_OFULL), 1);
         ptx::mbar_init(bar_addr(bars, C::B_DRAIN), 1);
         ptx::mbar_init(bar_addr(bars, C::B_NEVER), 1);
         ctl->abort = 0;
@@ -780,7 +894,7 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
-    if (warp < 4) {
+    if (warp < 4 * C::NWG) {
         dec_fp8_softmax_role<C>(p, it, sQ, sP, sV, sF, bars, tmem, ctl);
     } else if (warp == C::MMA_WARP) {
         dec_fp8_mma_role<C>(p, it, sQ, sP, sK, sV, bars, tmem, ctl);
@@ -806,14 +920,14 @@ __global__ void __launch_bounds__(128) fa_decode_fp8_combine_kernel(const __grid
     const long long total = *reinterpret_cast<const long long *>(p.cuts);
     const long long G = min((long long)grid, total);
     if (c >= G) return;
-    const int *cut = p.cuts + 4 + 4 * c;
-    if (cut[2] == 0) return;  // between two units
-    const long long begin = c * total / G - cut[2], end = begin + cut[3];
+    const int *cut = p.cuts + 4 + 5 * c;
+    if (cut[3] == 0) return;  // between two units
+    const long long begin = c * total / G - cut[3], end = begin + cut[4];
     if ((c - 1) * total / G > begin) return;  // an earlier boundary merges this unit
     int n = 1;                                // partials behind the first
     while (c + n < G && (c + n) * total / G < end) ++n;
     int rows;
-    const size_t row0 = dec_fp8_row0(p, cut[0], cut[1], &rows);
+    const size_t row0 = dec_fp8_row0(p, cut[0], cut[1], cut[2], &rows);
     constexpr int PER = D / 32;
     for (int r = warp; r < rows; r += 4) {
         float top = -INFINITY;
