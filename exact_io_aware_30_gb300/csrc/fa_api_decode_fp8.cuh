@@ -82,8 +82,19 @@ fa_status launch_decode_fp8_rc(const DecFp8Params &p, const DecFp8Plan &pl, Devi
     fa_decode_fp8_kernel<C><<<(unsigned)pl.grid, C::NUM_THREADS, C::SMEM_BYTES, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     if (pl.cuts) {
-        fa_decode_fp8_combine_kernel<D, kFP16, RC><<<(unsigned)(pl.grid - 1), 128, 0, stream>>>(p, pl.grid);
-        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(pl.grid - 1));
+        cfg.blockDim = dim3(128);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, kFP16, RC>, p, pl.grid) != cudaSuccess) {
+            cudaGetLastError();
+            return FA_ERR_CUDA;
+        }
     }
     return FA_OK;
 }

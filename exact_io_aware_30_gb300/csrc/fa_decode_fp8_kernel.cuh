@@ -92,12 +92,13 @@ struct DecFp8Cfg {
     static constexpr int CHUNK_BYTES = BN * ROWB;
     static constexpr int Q_BYTES = N * D;               // one buffer of q's parts
     static constexpr int QCH = N * ROWB;
-    static constexpr int P_BYTES = N * 128;             // one buffer of the weights' parts
-    static constexpr uint32_t S_COL = 0;                // two buffers
-    static constexpr uint32_t O_COL = 2 * N;            // two buffers of NM M blocks
-    static constexpr int COLS = (2 + 2 * NM) * N;
-    static constexpr uint32_t TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    static constexpr int CTAS_PER_SM = D == 64 && RC <= 4 ? 3 : (D <= 128 && TMEM_COLS <= 256 && NWG <= 2) ? 2 : 1;
+    static constexpr int P_BYTES = N * 128;             // the weights' parts of a tile
+    // Tensor memory: two S buffers of KPT tiles, two O buffers of NM M blocks.
+    static constexpr int cols(int kpt) { return (2 * kpt + 2 * NM) * N; }
+    static constexpr int ctas(int kpt) {
+        return D == 64 && RC <= 4 ? 3 : D <= 128 && NWG == 1 ? 2 : 1;
+    }
+    static constexpr int budget(int kpt) { return ctas(kpt) == 3 ? 75 * 1024 : ctas(kpt) == 2 ? 113 * 1024 : 226 * 1024; }
     static constexpr int MMA_WARP = 4 * NWG;
     static constexpr int TMA_WARP = 4 * NWG + 1;
     static constexpr int NUM_THREADS = 32 * (TMA_WARP + 1);
@@ -113,11 +114,23 @@ struct DecFp8Cfg {
     static constexpr int F_RED = F_L + 4 * RP;       // [2][4 warps][RW + 1] tile maxima, largest |vs|
     static constexpr int F_WG = (F_RED + 2 * 4 * (RW + 1) + 3) / 4 * 4;
     static constexpr int F_NUM = NWG * F_WG;
-    static constexpr int BUDGET = CTAS_PER_SM == 3 ? 75 * 1024 : CTAS_PER_SM == 2 ? 113 * 1024 : 226 * 1024;
-    static constexpr int FIXED = 1024 + 2 * Q_BYTES + 2 * P_BYTES + F_NUM * 4 + 512;
-    static constexpr int SLOTS = (BUDGET - FIXED) / TILE;
-    static constexpr int KST = SLOTS >= 12 ? 6 : (SLOTS + 1) / 2;
-    static constexpr int VST = SLOTS >= 12 ? 6 : SLOTS / 2;
+    static constexpr int slots(int kpt) {
+        return (budget(kpt) - (1024 + 2 * Q_BYTES + 2 * kpt * P_BYTES + F_NUM * 4 + 512)) / TILE;
+    }
+    // Tiles per step of the softmax: two where tensor memory holds them and the
+    // rings keep two steps.  Most of a step's time is a chain of waits,
+    // exchanges and short loads that does not grow with its keys (d 64, 8 rows:
+    // 84 -> 66 us; d 128, 24 rows: 193 -> 145 us); with shorter rings the
+    // second step's copies start late (d 128, 1 row: 92 -> 107 us).
+    static constexpr int KPT = cols(2) <= 512 / ctas(2) && slots(2) >= 8 ? 2 : 1;
+    static constexpr int COLS = cols(KPT);
+    static constexpr int CTAS_PER_SM = ctas(KPT);
+    static constexpr uint32_t TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static constexpr uint32_t S_COL = 0;
+    static constexpr uint32_t O_COL = 2 * KPT * N;
+    static constexpr int SLOTS = slots(KPT) < 12 ? slots(KPT) : 12;
+    static constexpr int VST = (SLOTS + 1) / 2;
+    static constexpr int KST = SLOTS / 2;
     static constexpr int B_KFULL = 0;
     static constexpr int B_KEMPTY = B_KFULL + KST;
     static constexpr int B_VFULL = B_KEMPTY + KST;
@@ -130,10 +143,10 @@ struct DecFp8Cfg {
     static constexpr int B_DRAIN = B_OFULL + 2;
     static constexpr int B_NEVER = B_DRAIN + 1;     // no arrivals (the stall test's wait)
     static constexpr int NUM_BARS = B_NEVER + 1;
-    static constexpr int SMEM_TILES = 2 * Q_BYTES + 2 * P_BYTES + (KST + VST) * TILE;
+    static constexpr int SMEM_TILES = 2 * Q_BYTES + 2 * KPT * P_BYTES + (KST + VST) * TILE;
     static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + F_NUM * 4 + NUM_BARS * 8 + 64;
-    static_assert(VST >= 2, "rings of at least two tiles");
-    static_assert(SMEM_BYTES <= BUDGET && SMEM_BYTES <= 232448, "shared memory overflow");
+    static_assert(KST >= 2 && VST >= 2, "rings of at least two tiles");
+    static_assert(SMEM_BYTES <= budget(KPT) && SMEM_BYTES <= 232448, "shared memory overflow");
     static_assert(NUM_BARS * 8 + 64 <= 512 && COLS <= 512 && N <= 256, "layout");
     static_assert(QCH % 1024 == 0 || ROWB == 64, "swizzle atoms");
 
@@ -181,6 +194,19 @@ __device__ __forceinline__ void dec_fp8_step(const DecFp8Params &p, DecFp8It &it
     it.next_len = dec_fp8_len(p, it.b + 1);
 }
 
+// Tiles of one step of the softmax: KPT, or what is left of the unit or the CTA's share.
+template <class C>
+__device__ __forceinline__ int dec_fp8_span(const DecFp8It &it) {
+    return C::KPT == 1 ? 1 : min(C::KPT, min(it.nt - it.tile, it.left));
+}
+
+template <class C>
+__device__ __forceinline__ void dec_fp8_steps(const DecFp8Params &p, DecFp8It &it, int span) {
+    it.tile += span - 1;
+    it.left -= span - 1;
+    dec_fp8_step(p, it);
+}
+
 // The first tile of the unit behind this one's.  (Its next_len is not loaded
 // where the step does not need it: no use of the result waits for that.)
 __device__ __forceinline__ DecFp8It dec_fp8_next_unit(const DecFp8Params &p, DecFp8It it) {
@@ -191,38 +217,37 @@ __device__ __forceinline__ DecFp8It dec_fp8_next_unit(const DecFp8Params &p, Dec
 }
 
 // Where this CTA's tiles begin: prefix sums over the requests' tiles, by all
-// threads of the CTA.  `scratch` holds THREADS / 32 + 2 long
-// longs.
+// threads of the CTA.  `scratch` holds THREADS / 32 + 5 long longs.  Up to
+// THREADS requests take one load each and two barriers.
 template <int THREADS>
 __device__ DecFp8It dec_fp8_begin(const DecFp8Params &p, long long *scratch) {
     constexpr int W = THREADS / 32;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long hc = (long long)p.Hkv * p.chunks;
-    int sum = 0;
-    for (int b = tid; b < p.B; b += THREADS) sum += dec_fp8_tiles(dec_fp8_len(p, b));
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == 0) scratch[warp] = sum;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < W; ++w) total += scratch[w];
-    total *= hc;
-    const long long G = min((long long)gridDim.x, total), c = blockIdx.x;
+    const long long hc = (long long)p.Hkv * p.chunks, c = blockIdx.x;
     DecFp8It it;
     it.b = it.kvh = it.chunk = it.tile = it.L = it.nt = it.next_len = it.left = 0;
-    if (c == 0 && tid == 0) *reinterpret_cast<long long *>(p.cuts) = total;
-    if (c >= G) return it;
-    const long long lo = c * total / G, hi = (c + 1) * total / G;
+    long long total = -1, G = 0, lo = 0, hi = 0;
+    if (p.B > THREADS) {  // the sum first; then the requests are gone through again
+        int sum = 0;
+        for (int b = tid; b < p.B; b += THREADS) sum += dec_fp8_tiles(dec_fp8_len(p, b));
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0) scratch[warp] = sum;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < W; ++w) total += scratch[w];
+        total *= hc;
+        __syncthreads();
+    }
     long long before = 0;  // tiles of the requests before this group of THREADS, per K/V head and chunk
     for (int b0 = 0;; b0 += THREADS) {
-        const int b = b0 + tid;
-        const int n = b < p.B ? dec_fp8_tiles(dec_fp8_len(p, b)) : 0;
+        const int b = b0 + tid, L = dec_fp8_len(p, b);
+        const int n = b < p.B ? dec_fp8_tiles(L) : 0;
         int inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
-        __syncthreads();
         if (tid == 0) scratch[W] = -1;
         if (lane == 31) scratch[warp] = inc;
         __syncthreads();
@@ -231,18 +256,29 @@ __device__ DecFp8It dec_fp8_begin(const DecFp8Params &p, long long *scratch) {
             if (w < warp) at += scratch[w];
             all += scratch[w];
         }
+        if (total < 0) total = all * hc;
+        if (b0 == 0) {
+            G = min((long long)gridDim.x, total);
+            if (c == 0 && tid == 0) *reinterpret_cast<long long *>(p.cuts) = total;
+            if (c >= G) return it;
+            lo = c * total / G;
+            hi = (c + 1) * total / G;
+        }
         if (n > 0 && at * hc <= lo && lo < (at + n) * hc) {
-            scratch[W + 1] = at;
             scratch[W] = b;
+            scratch[W + 1] = at;
+            scratch[W + 2] = L;
+            scratch[W + 3] = dec_fp8_len(p, b + 1);
         }
         __syncthreads();
         if (scratch[W] >= 0) break;  // (lo lies in some request)
         before += all;
+        __syncthreads();
     }
     it.b = (int)scratch[W];
-    it.L = dec_fp8_len(p, it.b);
+    it.L = (int)scratch[W + 2];
     it.nt = dec_fp8_tiles(it.L);
-    it.next_len = dec_fp8_len(p, it.b + 1);
+    it.next_len = (int)scratch[W + 3];
     const long long off = lo - scratch[W + 1] * hc;
     const int unit = (int)(off / it.nt);
     it.tile = (int)(off - (long long)unit * it.nt);
@@ -328,65 +364,77 @@ __device__ void dec_fp8_mma_role(const DecFp8Params &p, DecFp8It it, uint8_t *sQ
     constexpr uint32_t kIdescS = make_idesc(128, C::N, true, false);
     constexpr uint32_t kIdescO = make_idesc(128, C::N, true, false) | (1u << 15);
     const bool leader = ptx::lane_id() == 0;
-    const int n = it.left;
-    int unit = 0;
+    int unit = 0, t = 0;  // t: tiles of this CTA so far, as the rings count them
+    int span_before = 0, t_before = 0;
     bool ok = true;
-    for (int t = 0; ok && t <= n; ++t) {
-        if (t < n) {
-            const int ks = t % C::KST, b = t & 1;
-            if (t > 0) {
-                dec_fp8_step(p, it);
-                if (it.tile == 0) ++unit;
-            }
-            if ((t == 0 || it.tile == 0) &&
+    for (int step = 0; ok; ++step) {
+        const int b = step & 1, span = it.left > 0 ? dec_fp8_span<C>(it) : 0;
+        if (span > 0) {
+            if ((step == 0 || it.tile == 0) &&
                 !wait_warp(bar_addr(bars, C::B_QFULL + (unit & 1)), (unit >> 1) & 1, ctl, 73)) {
                 ok = false;
                 break;
             }
-            if (!wait_warp(bar_addr(bars, C::B_KFULL + ks), (t / C::KST) & 1, ctl, 74) ||
-                // the softmax has read S of tile t-2 out of this buffer
-                (t >= 2 && !wait_warp(bar_addr(bars, C::B_SFREE + b), ((t >> 1) - 1) & 1, ctl, 75))) {
+            // the softmax has read S of step - 2 out of this buffer
+            if (step >= 2 && !wait_warp(bar_addr(bars, C::B_SFREE + b), ((step >> 1) - 1) & 1, ctl, 75)) {
                 ok = false;
                 break;
             }
-            ptx::tc_fence_after();
-            if (leader) {
-                const uint32_t ka = ptx::smem_addr(sK + ks * C::TILE);
-                const uint32_t qa = ptx::smem_addr(sQ + (unit & 1) * C::Q_BYTES);
+            for (int j = 0; j < span; ++j) {
+                const int ks = (t + j) % C::KST;
+                ok = wait_warp(bar_addr(bars, C::B_KFULL + ks), ((t + j) / C::KST) & 1, ctl, 74);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (leader) {
+                    const uint32_t ka = ptx::smem_addr(sK + ks * C::TILE);
+                    const uint32_t qa = ptx::smem_addr(sQ + (unit & 1) * C::Q_BYTES);
 #pragma unroll
-                for (int kk = 0; kk < C::D / 32; ++kk) {
-                    const int ch = (kk * 32) / C::ROWB, in = (kk * 32) % C::ROWB;
-                    ptx::mma_ss_f8(tmem + C::S_COL + b * C::N, C::desc(ka + ch * C::CHUNK_BYTES + in),
-                                   C::desc(qa + ch * C::QCH + in), kIdescS, kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < C::D / 32; ++kk) {
+                        const int ch = (kk * 32) / C::ROWB, in = (kk * 32) % C::ROWB;
+                        ptx::mma_ss_f8(tmem + C::S_COL + (b * C::KPT + j) * C::N, C::desc(ka + ch * C::CHUNK_BYTES + in),
+                                       C::desc(qa + ch * C::QCH + in), kIdescS, kk > 0 ? 1u : 0u);
+                    }
+                    if (j + 1 == span) ptx::mma_commit(bar_addr(bars, C::B_SFULL + b));
+                    ptx::mma_commit(bar_addr(bars, C::B_KEMPTY + ks));
                 }
-                ptx::mma_commit(bar_addr(bars, C::B_SFULL + b));
-                ptx::mma_commit(bar_addr(bars, C::B_KEMPTY + ks));
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
         }
-        if (t >= 1) {
-            const int tp = t - 1, vs = tp % C::VST;
-            if (!wait_warp(bar_addr(bars, C::B_VFULL + vs), (tp / C::VST) & 1, ctl, 76) ||
-                !wait_warp(bar_addr(bars, C::B_PFULL + (tp & 1)), (tp >> 1) & 1, ctl, 77)) {
+        if (step >= 1) {
+            const int pb = b ^ 1;  // the step before
+            if (!wait_warp(bar_addr(bars, C::B_PFULL + pb), ((step - 1) >> 1) & 1, ctl, 77)) {
                 ok = false;
                 break;
             }
-            ptx::tc_fence_after();
-            if (leader) {
-                const uint32_t va = ptx::smem_addr(sV + vs * C::TILE), pa = ptx::smem_addr(sP + (tp & 1) * C::P_BYTES);
-                const uint32_t o_col = tmem + C::O_COL + (tp & 1) * C::NM * C::N;
+            for (int j = 0; j < span_before; ++j) {
+                const int vs = (t_before + j) % C::VST;
+                ok = wait_warp(bar_addr(bars, C::B_VFULL + vs), ((t_before + j) / C::VST) & 1, ctl, 76);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (leader) {
+                    const uint32_t va = ptx::smem_addr(sV + vs * C::TILE);
+                    const uint32_t pa = ptx::smem_addr(sP + (pb * C::KPT + j) * C::P_BYTES);
+                    const uint32_t o_col = tmem + C::O_COL + pb * C::NM * C::N;
 #pragma unroll
-                for (int m = 0; m < C::NM; ++m)
+                    for (int m = 0; m < C::NM; ++m)
 #pragma unroll
-                    for (int kk = 0; kk < C::BN / 32; ++kk)
-                        ptx::mma_ss_f8(o_col + m * C::N,
-                                       C::desc_v(va + m * C::CHUNK_BYTES + kk * 32 * C::ROWB),
-                                       smem_desc(pa + kk * 32, 16), kIdescO, kk > 0 ? 1u : 0u);
-                ptx::mma_commit(bar_addr(bars, C::B_OFULL + (tp & 1)));
-                ptx::mma_commit(bar_addr(bars, C::B_VEMPTY + vs));
+                        for (int kk = 0; kk < C::BN / 32; ++kk)
+                            ptx::mma_ss_f8(o_col + m * C::N, C::desc_v(va + m * C::CHUNK_BYTES + kk * 32 * C::ROWB),
+                                           smem_desc(pa + kk * 32, 16), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+                    if (j + 1 == span_before) ptx::mma_commit(bar_addr(bars, C::B_OFULL + pb));
+                    ptx::mma_commit(bar_addr(bars, C::B_VEMPTY + vs));
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
         }
+        if (span == 0) break;
+        t_before = t;
+        span_before = span;
+        t += span;
+        dec_fp8_steps<C>(p, it, span);
+        if (it.tile == 0) ++unit;  // (one more than there are behind the last)
     }
     if (leader) ptx::mma_commit(bar_addr(bars, C::B_DRAIN));
     __syncwarp();
@@ -606,21 +654,34 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
     // loads are unconditional, at places clamped into the arrays, and judged
     // only when they are used, so that none is waited for early.
     DecFp8It ahead = it;
-    int entry;               // of `ahead`'s tile, as loaded
-    bool entry_seen;         // its key exists
-    float ks_next, vs_next, ks_far, vs_far;  // of the next tile and the one behind it, as loaded
-    bool next_seen, far_seen;
+    constexpr int KPT = C::KPT;   // keys of this thread in a step
+    int entry[KPT];               // of `ahead`'s step, as loaded
+    bool entry_seen[KPT];         // its key exists
+    float ks_next[KPT], vs_next[KPT], ks_far[KPT], vs_far[KPT];  // of the next step and the one behind it, as loaded
+    bool next_seen[KPT], far_seen[KPT];
     auto load_entry = [&] {
-        const int key = ahead.tile * C::BN + tid;
-        entry_seen = ahead.left > 0 && key < ahead.L;
-        entry = p.block_table[(size_t)min(ahead.b, p.B - 1) * p.max_blocks + min(key >> p.bs_log2, p.max_blocks - 1)];
+        const int span = dec_fp8_span<C>(ahead);
+        const int *row = p.block_table + (size_t)min(ahead.b, p.B - 1) * p.max_blocks;
+#pragma unroll
+        for (int j = 0; j < KPT; ++j) {
+            const int key = (ahead.tile + j) * C::BN + tid;
+            entry_seen[j] = ahead.left > 0 && j < span && key < ahead.L;
+            entry[j] = row[min(key >> p.bs_log2, p.max_blocks - 1)];
+        }
     };
     auto load_scales = [&] {
-        far_seen = entry_seen && entry >= 0 && entry < p.num_blocks;
-        const size_t bh = (size_t)(far_seen ? entry : 0) * p.Hkv + ahead.kvh;
-        ks_far = p.k_scale[bh];
-        vs_far = p.v_scale[bh];
-        if (ahead.left > 0) dec_fp8_step(p, ahead);
+#pragma unroll
+        for (int j = 0; j < KPT; ++j) {
+            far_seen[j] = entry_seen[j] && entry[j] >= 0 && entry[j] < p.num_blocks;
+            const int bh = (far_seen[j] ? entry[j] : 0) * p.Hkv + ahead.kvh;  // (below 2^31: the host checks)
+            ks_far[j] = p.k_scale[bh];
+            vs_far[j] = p.v_scale[bh];
+        }
+        if (ahead.left > 0) dec_fp8_steps<C>(p, ahead, dec_fp8_span<C>(ahead));
+    };
+    auto shift_scales = [&] {
+#pragma unroll
+        for (int j = 0; j < KPT; ++j) ks_next[j] = ks_far[j], vs_next[j] = vs_far[j], next_seen[j] = far_seen[j];
     };
 
     // Units are numbered from 0 in this CTA; unit u's q sits in buffer u & 1.
@@ -634,7 +695,7 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
     dec_fp8_put_q<C>(p, it, q, sQ, sF + C::F_C, reinterpret_cast<int *>(sF + C::F_LAST));
     ptx::fence_proxy_async_smem();
     ptx::mbar_arrive(bar_addr(bars, C::B_QFULL));
-    ks_next = ks_far, vs_next = vs_far, next_seen = far_seen;
+    shift_scales();
     load_scales();
     load_entry();
     if (it.left > it.nt - it.tile) dec_fp8_load_q<C>(p, dec_fp8_next_unit(p, it), q);
@@ -644,11 +705,12 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
     float m_run = -INFINITY;  // lane r: row r's running maximum
     bool begun_here = it.tile == 0;
     bool first = true, bad = false;
-    int unit = 0;
-    for (int t = 0;; ++t) {
+    int unit = 0, t = 0;  // t: tiles of this CTA so far
+    for (int step = 0;; ++step) {
+        const int span = dec_fp8_span<C>(it);
         const float *mul = sF + C::F_C + (unit & 1) * RP;
         const int *last = reinterpret_cast<const int *>(sF + C::F_LAST) + (unit & 1) * RP;
-        const bool ends = it.tile + 1 == it.nt || it.left == 1;  // the unit, or this CTA's part of it
+        const bool ends = it.tile + span == it.nt || it.left == span;  // the unit, or this CTA's part of it
         if (first) {
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
@@ -668,36 +730,53 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
                 if (coming.left > coming.nt) dec_fp8_load_q<C>(p, dec_fp8_next_unit(p, coming), q);
             }
         }
-        const float ks = next_seen ? ks_next : 0.f, vs = next_seen ? vs_next : 0.f;
-        ks_next = ks_far, vs_next = vs_far, next_seen = far_seen;
+        float ks[KPT], vs[KPT];
+#pragma unroll
+        for (int j = 0; j < KPT; ++j) ks[j] = next_seen[j] ? ks_next[j] : 0.f, vs[j] = next_seen[j] ? vs_next[j] : 0.f;
+        shift_scales();
         load_scales();
         load_entry();
 
-        const int b = t & 1, k0 = it.tile * C::BN, key = k0 + tid;
-        bad = bad || !wait_warp(bar_addr(bars, p.stall_test && t == 0 ? C::B_NEVER : C::B_SFULL + b), (t >> 1) & 1, ctl, 78);
-        float x[RW];  // scores without their row's multiplier
+        const int b = step & 1, k0 = it.tile * C::BN;
+        bad = bad || !wait_warp(bar_addr(bars, p.stall_test && step == 0 ? C::B_NEVER : C::B_SFULL + b), (step >> 1) & 1, ctl, 78);
+        float x[KPT][RW];  // scores without their row's multiplier
         float *red = sF + C::F_RED + (b * 4 + warp) * (RW + 1);
         if (!bad) {
             ptx::tc_fence_after();
-            dec_fp8_read<C, RW>(lane_base + C::S_COL + b * C::N, x);
 #pragma unroll
-            for (int r = 0; r < RW; ++r) x[r] *= ks;
+            for (int j = 0; j < KPT; ++j) {
+                dec_fp8_read<C, RW>(lane_base + C::S_COL + (b * KPT + j) * C::N, x[j]);
+#pragma unroll
+                for (int r = 0; r < RW; ++r) x[j][r] *= ks[j];
+            }
             ptx::tc_fence_before();
             ptx::mbar_arrive(bar_addr(bars, C::B_SFREE + b));
             // hidden keys: past the row's last (a select, so nothing of theirs leaks)
             const int seen_by_all = p.mask_kind == kMaskCausal ? it.L - p.Sq : it.L - 1;
-            if (k0 + C::BN - 1 > seen_by_all) {
+            if (k0 + KPT * C::BN - 1 > seen_by_all) {
 #pragma unroll
-                for (int r = 0; r < RW; ++r)
-                    if (key > last[r]) x[r] = -INFINITY;
+                for (int j = 0; j < KPT; ++j) {
+                    const int key = k0 + j * C::BN + tid;
+#pragma unroll
+                    for (int r = 0; r < RW; ++r)
+                        if (key > last[r] || j >= span) x[j][r] = -INFINITY;
+                }
+            } else if (KPT > 1 && span < KPT) {
+                // (the rest of the unit is another CTA's: S holds nothing of this step there)
+#pragma unroll
+                for (int r = 0; r < RW; ++r) x[KPT - 1][r] = -INFINITY;
             }
             float mine = -INFINITY;
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
-                const float top = warp_max(x[r]);
+                float both = x[0][r];
+                if constexpr (KPT == 2) both = fmaxf(both, x[KPT - 1][r]);
+                const float top = warp_max(both);
                 if (lane == r) mine = top;
             }
-            const float vtop = warp_max(fabsf(vs));
+            float both = fabsf(vs[0]);
+            if constexpr (KPT == 2) both = fmaxf(both, fabsf(vs[KPT - 1]));
+            const float vtop = warp_max(both);
             if (lane < RW) red[lane] = mine;
             if (lane == 0) red[RW] = vtop;
         }
@@ -721,43 +800,57 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
         }
         __syncwarp();
         // weights: of the sum in fp32, of V (times the block's scale over the
-        // tile's largest, times 256) as parts.  P V of tile t - 2 is done (its
-        // O has been read), so its buffer is free.
+        // step's largest, times 256) as parts.  P V of two steps before is done
+        // (its O has been read), so its buffer is free.
         {
-            const float share = vtop > 0.f ? vs / vtop * 256.f : 0.f;
-            const uint32_t buf = p_addr + b * C::P_BYTES;
+            float share[KPT];
+#pragma unroll
+            for (int j = 0; j < KPT; ++j) share[j] = vtop > 0.f ? vs[j] / vtop * 256.f : 0.f;
+            const uint32_t buf = p_addr + b * KPT * C::P_BYTES;
             constexpr int S = RW < 4 ? RW : 4;  // rows at a time
 #pragma unroll
             for (int g = 0; g < RW; g += S) {
-                float m[S], c[S], a[S], e[S], v[(S + 1) / 2 * 2];
+                float m[S], c[S], a[S], e[S], v[KPT][(S + 1) / 2 * 2];
                 lds_row<S>(sM + g, m);
                 lds_row<S>(mul + g, c);
                 lds_row<S>(sA + g, a);
                 lds_row<S>(sB + g, e);
 #pragma unroll
                 for (int r = 0; r < S; ++r) {
-                    const float w = ptx::ex2_approx(fmaf(x[g + r], c[r], -m[r]));
-                    l[g + r] = fmaf(l[g + r], a[r], w * e[r]);
-                    v[r] = w * share;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < KPT; ++j) {
+                        const float w = ptx::ex2_approx(fmaf(x[j][g + r], c[r], -m[r]));
+                        sum += w;
+                        v[j][r] = w * share[j];
+                    }
+                    l[g + r] = fmaf(l[g + r], a[r], sum * e[r]);
                 }
-                if constexpr (S == 1) v[1] = 0.f;
 #pragma unroll
-                for (int r = 0; r < S; r += 2) {
-                    uint32_t codes[C::NP];
-                    split_e4m3<C::NP>(v[r], v[r + 1], codes);
+                for (int j = 0; j < KPT; ++j) {
+                    if constexpr (S == 1) v[j][1] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < C::NP; ++j) {
-                        const int n = j * C::RC + g + r;  // (the warpgroup's first row is 0 modulo 8)
-                        st_shared_u8((buf ^ (uint32_t)((n & 7) << 4)) + n * 128, codes[j]);
-                        if (r + 1 < S) st_shared_u8((buf ^ (uint32_t)(((n + 1) & 7) << 4)) + (n + 1) * 128, codes[j] >> 8);
+                    for (int r = 0; r < S; r += 2) {
+                        uint32_t codes[C::NP];
+                        split_e4m3<C::NP>(v[j][r], v[j][r + 1], codes);
+#pragma unroll
+                        for (int i = 0; i < C::NP; ++i) {
+                            const int n = i * C::RC + g + r;  // (the warpgroup's first row is 0 modulo 8)
+                            st_shared_u8((buf ^ (uint32_t)((n & 7) << 4)) + j * C::P_BYTES + n * 128, codes[i]);
+                            if (r + 1 < S)
+                                st_shared_u8((buf ^ (uint32_t)(((n + 1) & 7) << 4)) + j * C::P_BYTES + (n + 1) * 128,
+                                             codes[i] >> 8);
+                        }
                     }
                 }
             }
-            if (wg == 0 && k0 + C::BN > it.L && (it.L & ((1 << p.bs_log2) - 1)) != 0 && key >= it.L) {
-                // a row of V past the request's keys meets weight 0, but junk (NaN)
-                // in it would not vanish: zero it
-                const int slot = t % C::VST;
-                bad = !wait_bar(bar_addr(bars, C::B_VFULL + slot), (t / C::VST) & 1, ctl, 80);
+            // a row of V past the request's keys (they end in the step's last
+            // tile) meets weight 0, but junk (NaN) in it would not vanish: zero it
+            const int last_tile = it.tile + span - 1;
+            if (wg == 0 && (last_tile + 1) * C::BN > it.L && (it.L & ((1 << p.bs_log2) - 1)) != 0 &&
+                last_tile * C::BN + tid >= it.L) {
+                const int slot = (t + span - 1) % C::VST;
+                bad = !wait_bar(bar_addr(bars, C::B_VFULL + slot), ((t + span - 1) / C::VST) & 1, ctl, 80);
 #pragma unroll
                 for (int ch = 0; ch < C::NCH; ++ch)
 #pragma unroll
@@ -772,7 +865,7 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
         if (!bad) ptx::mbar_arrive(bar_addr(bars, C::B_PFULL + b));
         // O of the tile before (of this unit), while P V of this one runs
         if (!first) {
-            bad = bad || !wait_warp(bar_addr(bars, C::B_OFULL + (b ^ 1)), ((t - 1) >> 1) & 1, ctl, 79);
+            bad = bad || !wait_warp(bar_addr(bars, C::B_OFULL + (b ^ 1)), ((step - 1) >> 1) & 1, ctl, 79);
             if (!bad) {
                 ptx::tc_fence_after();
                 dec_fp8_accumulate<C>(lane_base + C::O_COL + (b ^ 1) * C::NM * C::N, sF + C::F_A + ((b ^ 1) * 4 + warp) * RP,
@@ -784,7 +877,7 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
 
         if (ends) {
             // the unit's last O, its sums, and the rows out
-            bad = bad || !wait_warp(bar_addr(bars, C::B_OFULL + b), (t >> 1) & 1, ctl, 81);
+            bad = bad || !wait_warp(bar_addr(bars, C::B_OFULL + b), (step >> 1) & 1, ctl, 81);
             if (!bad) {
                 ptx::tc_fence_after();
                 dec_fp8_accumulate<C>(lane_base + C::O_COL + b * C::NM * C::N, sA, sW, acc);
@@ -803,7 +896,7 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
             if (ptx::named_bar_any(5 + wg, 128, bad)) return;
             int rows;
             const size_t row0 = dec_fp8_row0(p, it.b, it.kvh, it.chunk, &rows);
-            const bool whole = begun_here && it.tile + 1 == it.nt;
+            const bool whole = begun_here && it.tile + span == it.nt;
             const size_t slot = 2 * (size_t)blockIdx.x + (begun_here ? 1 : 0);
             rows -= wg * RW;  // (0 or less: the warpgroup has none of them)
             if (warp == 0 && lane < RW && lane < rows) {
@@ -829,13 +922,14 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
                         p.part_o[(slot * C::RC + wg * RW + r) * C::D + c] = o;
                 }
             }
-            if (it.left == 1) return;
+            if (it.left == span) return;
             first = true;
             begun_here = true;
             ++unit;
             // sL is written again only behind the next tile's barrier
         }
-        dec_fp8_step(p, it);
+        t += span;
+        dec_fp8_steps<C>(p, it, span);
     }
 }
 
@@ -849,7 +943,7 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     uint8_t *sV = sK + C::KST * C::TILE;
     uint8_t *sQ = sV + C::VST * C::TILE;
     uint8_t *sP = sQ + 2 * C::Q_BYTES;
-    uint64_t *bar_mem = reinterpret_cast<uint64_t *>(sP + 2 * C::P_BYTES);
+    uint64_t *bar_mem = reinterpret_cast<uint64_t *>(sP + 2 * C::KPT * C::P_BYTES);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bar_mem + C::NUM_BARS);
     Ctl *ctl = reinterpret_cast<Ctl *>(tmem_holder + 2);
     float *sF = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ctl + 1) + 15) & ~static_cast<uintptr_t>(15));
@@ -893,6 +987,8 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
+    // the merge may be set up now; it waits for this grid's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp < 4 * C::NWG) {
         dec_fp8_softmax_role<C>(p, it, sQ, sP, sV, sF, bars, tmem, ctl);
@@ -917,6 +1013,7 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
 template <int D, bool kFP16, int RC>
 __global__ void __launch_bounds__(128) fa_decode_fp8_combine_kernel(const __grid_constant__ DecFp8Params p, int grid) {
     const int c = (int)blockIdx.x + 1, lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the attention still runs
     const long long total = *reinterpret_cast<const long long *>(p.cuts);
     const long long G = min((long long)grid, total);
     if (c >= G) return;

@@ -531,39 +531,33 @@ def forward_host(q, k, v, scale: float | None = None, mask="none", window: int =
 
 # --------------------------------------------------- rotary positions and the 8-bit paged cache
 
-class _Scope:
-    """Runs a call on the tensors' own device and on ``stream``.
+def _enter(dev, stream):
+    """Makes a call run on the tensors' own device and on ``stream``.
 
-    Outputs and workspaces made inside are allocated for that stream, so the
+    Returns (raw stream pointer, scope to leave afterwards or None).  Outputs
+    and workspaces made inside the scope are allocated for that stream, so the
     allocator cannot hand their memory to work of another stream too early.
-    Entering gives the raw stream pointer.
     """
-    __slots__ = ("_scope", "_device", "_stream")
+    import torch
+    if stream is None:
+        if torch._C._cuda_getDevice() == dev.index:
+            return torch._C._cuda_getCurrentRawStream(dev.index), None
+        scope = torch.cuda.device(dev)
+        scope.__enter__()
+        return torch._C._cuda_getCurrentRawStream(dev.index), scope
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else \
+            torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        raise FAError(FA_ERR_INVALID_ARG, f"the stream is on {stream.device}, the tensors on {dev}")
+    scope = torch.cuda.stream(stream)
+    scope.__enter__()
+    return stream.cuda_stream, scope
 
-    def __init__(self, device, stream):
-        self._device, self._stream, self._scope = device, stream, None
 
-    def __enter__(self):
-        import torch
-        dev, stream = self._device, self._stream
-        if stream is None:
-            if torch.cuda.current_device() != dev.index:
-                self._scope = torch.cuda.device(dev)
-                self._scope.__enter__()
-            return torch.cuda.current_stream(dev).cuda_stream
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else \
-                torch.cuda.default_stream(dev)
-        if stream.device != dev:
-            raise FAError(FA_ERR_INVALID_ARG, f"the stream is on {stream.device}, the tensors on {dev}")
-        self._scope = torch.cuda.stream(stream)
-        self._scope.__enter__()
-        return stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._scope is not None:
-            self._scope.__exit__(*exc)
-        return False
+def _leave(scope):
+    if scope is not None:
+        scope.__exit__(None, None, None)
 
 
 @functools.lru_cache(maxsize=256)
@@ -574,14 +568,15 @@ def _longs(values):
 
 def _need_tensor(name, t, device, dtype, shape, contiguous=True):
     """Checks one tensor argument against what the call needs of it."""
+    if t.device == device and t.dtype == dtype and t.shape == shape and (not contiguous or t.is_contiguous()):
+        return
     if t.device != device:
         raise FAError(FA_ERR_INVALID_ARG, f"{name} must be on {device}, it is on {t.device}")
     if t.dtype != dtype:
         raise FAError(FA_ERR_INVALID_ARG, f"{name} must be {dtype}, it is {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise FAError(FA_ERR_INVALID_ARG, f"{name} must have shape {tuple(shape)}, it has {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise FAError(FA_ERR_INVALID_ARG, f"{name} must be contiguous")
+    raise FAError(FA_ERR_INVALID_ARG, f"{name} must be contiguous")
 
 
 RopePlan = collections.namedtuple("RopePlan", "rot_dim freq amplitude")
@@ -649,12 +644,12 @@ def _rope(q, k, plan, positions, offset, layout, out_q, out_k, stream, direction
         _need_tensor("k", k, dev, q.dtype, k.shape, contiguous=False)
     elif out_k is not None:
         raise FAError(FA_ERR_INVALID_ARG, "out_k without k")
-    for name, t, like in (("q", q, q), ("k", k, k), ("out_q", out_q, q), ("out_k", out_k, k)):
-        if t is None:
-            continue
-        if t is not like:
-            _need_tensor(name, t, dev, q.dtype, like.shape, contiguous=False)
-        if t.stride(3) != 1 and t.numel():
+    if out_q is not None:
+        _need_tensor("out_q", out_q, dev, q.dtype, q.shape, contiguous=False)
+    if out_k is not None:
+        _need_tensor("out_k", out_k, dev, q.dtype, k.shape, contiguous=False)
+    for name, t in (("q", q), ("k", k), ("out_q", out_q), ("out_k", out_k)):
+        if t is not None and t.stride(3) != 1 and t.numel():
             raise FAError(FA_ERR_INVALID_ARG, f"{name}: the last dimension must be contiguous")
     if plan.freq.device != dev:
         raise FAError(FA_ERR_INVALID_ARG, f"the plan is on {plan.freq.device}, the tensors on {dev}")
@@ -662,26 +657,29 @@ def _rope(q, k, plan, positions, offset, layout, out_q, out_k, stream, direction
     if positions is not None:
         if positions.dtype != torch.int32 or positions.device != dev:
             raise FAError(FA_ERR_INVALID_ARG, f"positions must be int32 on {dev}")
-        if tuple(positions.shape) == (B, S):
+        if positions.shape == (B, S):
             pos_stride = positions.stride(0) if B > 1 else 0
-        elif tuple(positions.shape) != (S,):
+        elif positions.shape != (S,):
             raise FAError(FA_ERR_INVALID_ARG, "positions must be [B,S] or [S]")
         if S > 1 and positions.stride(-1) != 1:
             raise FAError(FA_ERR_INVALID_ARG, "positions: the last dimension must be contiguous")
         pos_ptr = positions.data_ptr()
-    with _Scope(dev, stream) as sp:
+    sp, scope = _enter(dev, stream)
+    try:
         if out_q is None:
             out_q = torch.empty((B, H, S, d), dtype=q.dtype, device=dev)
         if k is not None and out_k is None:
             out_k = torch.empty((B, Hkv, S, d), dtype=q.dtype, device=dev)
         if q.numel() == 0 and (k is None or k.numel() == 0):
             return out_q if k is None else (out_q, out_k)
-        st = load().fa_rope(
-            q.data_ptr(), _longs(q.stride()[:3]), out_q.data_ptr(), _longs(out_q.stride()[:3]),
-            k.data_ptr() if Hkv else None, _longs(k.stride()[:3]) if Hkv else None,
-            out_k.data_ptr() if Hkv else None, _longs(out_k.stride()[:3]) if Hkv else None,
+        st = (_lib or load()).fa_rope(
+            q.data_ptr(), _longs(q.stride()), out_q.data_ptr(), _longs(out_q.stride()),
+            k.data_ptr() if Hkv else None, _longs(k.stride()) if Hkv else None,
+            out_k.data_ptr() if Hkv else None, _longs(out_k.stride()) if Hkv else None,
             pos_ptr, pos_stride, int(offset), plan.freq.data_ptr(), plan.amplitude, B, H, Hkv, S, d,
             plan.rot_dim, ROPE_LAYOUTS[layout], direction, dt, sp)
+    finally:
+        _leave(scope)
     _check(st, "fa_rope")
     return out_q if k is None else (out_q, out_k)
 
@@ -737,7 +735,8 @@ def paged_update(seq_lens, delta, block_table, free_ring, ring_state, block_size
     _need_tensor("block_table", block_table, dev, i32, (B, mb))
     _need_tensor("free_ring", free_ring, dev, i32, free_ring.shape)
     _need_tensor("ring_state", ring_state, dev, i32, (2,))
-    with _Scope(dev, stream) as sp:
+    sp, scope = _enter(dev, stream)
+    try:
         outs = []
         for name, t, n in (("seq_lens_out", seq_lens_out, B), ("ring_state_out", ring_state_out, 2),
                            ("slot_map", slot_map, max_tokens), ("positions", positions, max_tokens),
@@ -747,11 +746,13 @@ def paged_update(seq_lens, delta, block_table, free_ring, ring_state, block_size
             else:
                 _need_tensor(name, t, dev, i32, (n,))
             outs.append(t)
-        st = load().fa_paged_update(
+        st = (_lib or load()).fa_paged_update(
             seq_lens.data_ptr(), delta.data_ptr(), block_table.data_ptr(), free_ring.data_ptr(),
             ring_state.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
             outs[3].data_ptr(), outs[4].data_ptr(), B, mb, free_ring.shape[0], int(block_size),
             int(max_tokens), sp)
+    finally:
+        _leave(scope)
     _check(st, "fa_paged_update")
     return PagedStep(*outs)
 
@@ -790,11 +791,14 @@ def cache_append_fp8(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=
         raise FAError(FA_ERR_INVALID_ARG, "k and v: the last dimension must be contiguous")
     _need_tensor("slot_map", slot_map, dev, torch.int32, (T,))
     _need_fp8_cache(k_cache, v_cache, k_scale, v_scale, dev)
-    with _Scope(dev, stream) as sp:
-        st = load().fa_cache_append_fp8(
+    sp, scope = _enter(dev, stream)
+    try:
+        st = (_lib or load()).fa_cache_append_fp8(
             k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
             slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), T, Hkv, d, bs, nb, dt, sp)
+    finally:
+        _leave(scope)
     _check(st, "fa_cache_append_fp8")
 
 
@@ -806,6 +810,14 @@ def decode_fp8_workspace_query(B, H, H_kv, Sq, d, block_size, max_blocks, num_bl
                                               int(max_blocks), int(num_blocks), int(max_seq_len),
                                               mask_code(mask), int(dtype), ctypes.byref(n))
     return st, n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_fp8_workspace(device_index, *sizes):
+    """Workspace bytes for these sizes on this device (the current one); refusals are not kept."""
+    n = ctypes.c_size_t(0)
+    _check(load().fa_decode_fp8_workspace_query(*sizes, ctypes.byref(n)), "fa_decode_fp8_workspace_query")
+    return n.value
 
 
 def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, max_seq_len: int,
@@ -833,10 +845,11 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     mk = mask_code(mask)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _Scope(dev, stream) as sp:
-        st, ws_bytes = decode_fp8_workspace_query(B, H, Hkv, Sq, d, bs, mb, nb, max_seq_len, mk, dt)
-        _check(st, "fa_decode_fp8_workspace_query")
+    max_seq_len = int(max_seq_len)
+    sp, scope = _enter(dev, stream)
+    try:
         if workspace is None:
+            ws_bytes = _decode_fp8_workspace(dev.index, B, H, Hkv, Sq, d, bs, mb, nb, max_seq_len, mk, dt)
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         else:
             _need_tensor("workspace", workspace, dev, torch.uint8, workspace.shape)
@@ -848,10 +861,12 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
             lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
         else:
             _need_tensor("lse", lse, dev, torch.float32, (B, H, Sq))
-        st = load().fa_decode_paged_fp8(
+        st = (_lib or load()).fa_decode_paged_fp8(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), B, H, Hkv, Sq, d, bs, mb, nb, int(max_seq_len),
+            workspace.data_ptr(), workspace.numel(), B, H, Hkv, Sq, d, bs, mb, nb, max_seq_len,
             float(scale), mk, dt, sp)
+    finally:
+        _leave(scope)
     _check(st, "fa_decode_paged_fp8")
     return out, lse
