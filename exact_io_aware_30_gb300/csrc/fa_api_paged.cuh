@@ -32,8 +32,8 @@ bool outputs_apart(const Extent *outs, int n_out, const Extent *ins, int n_in, c
     return true;
 }
 
-// Rows of slot_map that one CTA of the update serves before a second CTA of
-// the cluster pays for its own scan of the requests.
+// Rows of slot_map that one CTA of the update serves before a second CTA pays
+// for its own scan of the requests.
 constexpr int kUpdateRowsPerCta = 2048;
 
 fa_status paged_update_impl(const int *seq_lens, const int *delta, int *block_table, int *free_ring,
@@ -80,23 +80,30 @@ fa_status paged_update_impl(const int *seq_lens, const int *delta, int *block_ta
     p.ring_size = ring_size;
     p.bs_log2 = bs_log2;
     p.max_tokens = max_tokens;
+    // In place, the CTAs have to meet: one cluster of a portable size.
+    const bool in_place = seq_lens_out == seq_lens || ring_state_out == ring_state;
+    const int most = in_place ? 8 : 32;
     int ranks = 1;
-    while (ranks < 8 && max_tokens > ranks * kUpdateRowsPerCta) ranks *= 2;
+    while (ranks < most && max_tokens > ranks * kUpdateRowsPerCta) ranks *= 2;
+    p.meet = in_place && ranks > 1;
     if (log_enabled())
         std::fprintf(stderr, "[fa] fa_paged_update B=%d max_blocks=%d bs=%d rows=%d ctas=%d\n", B, max_blocks,
                      block_size, max_tokens, ranks);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ranks);
-    cfg.blockDim = dim3(kPagedThreads);
+    // few requests and rows: a small CTA, whose barriers cost less
+    const bool small = B <= 128 && max_tokens <= 512;
+    cfg.blockDim = dim3(small ? 128 : 1024);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)ranks;
+    attr.val.clusterDim.x = p.meet ? (unsigned)ranks : 1;
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fa_paged_update_kernel, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, small ? fa_paged_update_kernel<128> : fa_paged_update_kernel<1024>, p) !=
+        cudaSuccess) {
         cudaGetLastError();
         return FA_ERR_CUDA;
     }
@@ -157,31 +164,36 @@ fa_status cache_append_impl(const void *k, const void *v, long long k_token_stri
     p.slot_map = slot_map;
     p.T = T;
     p.Hkv = Hkv;
-    p.d = d;
+    p.d_log2 = d == 64 ? 6 : d == 128 ? 7 : 8;
     p.bs_log2 = block_size_log2(block_size);
     p.slots = (long long)num_blocks * block_size;
-    // Rows per CTA: one while the grid stays within a few waves (a decode
-    // step: every row leads a block of its own), else up to a block's worth
-    // (a prompt: one leader per block, and a CTA whose rows hold none only
-    // reads their slots).
+    // Warps per pair: a lane holds eight vectors of eight values.
+    const int block_log2 = p.d_log2 + p.bs_log2;
+    p.wpu_log2 = std::min(std::max(block_log2 - 11, 0), 3);
+    const bool big = block_log2 > 14;  // 32,768 values: sixteen vectors a lane
+    // Two pairs per group, and rows until the grid is about two waves (four
+    // CTAs per SM), at most a block's: in a decode step every row leads a block
+    // of its own; in a prompt one row of a block does, and the others only read
+    // their slot.
+    const int groups = kAppendThreads / (32 << p.wpu_log2);
+    const int y = std::max(1, (2 * Hkv + 2 * groups - 1) / (2 * groups));
     p.rows_per_cta = 1;
-    while (p.rows_per_cta < block_size && (long long)((T + p.rows_per_cta - 1) / p.rows_per_cta) * Hkv * 2 >
-                                              64LL * info->num_sms)
+    while (p.rows_per_cta < block_size &&
+           (long long)((T + p.rows_per_cta - 1) / p.rows_per_cta) * y > 8LL * info->num_sms)
         p.rows_per_cta *= 2;
-    const dim3 grid((unsigned)((T + p.rows_per_cta - 1) / p.rows_per_cta), (unsigned)Hkv, 2);
+    const dim3 grid((unsigned)((T + p.rows_per_cta - 1) / p.rows_per_cta), (unsigned)y);
     long long bits = (long long)(kp | vp);
     if (T > 1) bits |= (k_token_stride | v_token_stride) * 2;
     if (Hkv > 1) bits |= (k_head_stride | v_head_stride) * 2;
     const bool vec = (bits & 15) == 0, fp16 = dtype == FA_DTYPE_FP16;
     if (log_enabled())
-        std::fprintf(stderr, "[fa] fa_cache_append_fp8 rows=%d Hkv=%d d=%d bs=%d vec=%d rows_per_cta=%d\n", T, Hkv, d,
-                     block_size, vec ? 1 : 0, p.rows_per_cta);
-    if (fp16)
-        vec ? fa_cache_append_kernel<true, true><<<grid, kAppendThreads, 0, stream>>>(p)
-            : fa_cache_append_kernel<true, false><<<grid, kAppendThreads, 0, stream>>>(p);
-    else
-        vec ? fa_cache_append_kernel<false, true><<<grid, kAppendThreads, 0, stream>>>(p)
-            : fa_cache_append_kernel<false, false><<<grid, kAppendThreads, 0, stream>>>(p);
+        std::fprintf(stderr, "[fa] fa_cache_append_fp8 rows=%d Hkv=%d d=%d bs=%d vec=%d rows_per_cta=%d grid=%d x %d\n", T,
+                     Hkv, d, block_size, vec ? 1 : 0, p.rows_per_cta, (int)grid.x, (int)grid.y);
+    auto kern = big ? (fp16 ? (vec ? fa_cache_append_kernel<true, true, 16> : fa_cache_append_kernel<true, false, 16>)
+                            : (vec ? fa_cache_append_kernel<false, true, 16> : fa_cache_append_kernel<false, false, 16>))
+                    : (fp16 ? (vec ? fa_cache_append_kernel<true, true, 8> : fa_cache_append_kernel<true, false, 8>)
+                            : (vec ? fa_cache_append_kernel<false, true, 8> : fa_cache_append_kernel<false, false, 8>));
+    kern<<<grid, kAppendThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -189,16 +189,17 @@ fa_status rope_impl(const void *q, const long long *q_strides, void *q_out, cons
     p.S = S;
     p.d = d;
     p.rot = rot_dim;
-    p.slots = half / V + (d - rot_dim) / V;
+    p.slots = half / V + ((d - rot_dim) / V + 1) / 2;
     p.units = (long long)B * S * p.slots;
     const long long blocks = (p.units + 255) / 256;
     if (blocks > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-    // Heads per thread: as many as leave about eight CTAs of 256 threads per
-    // SM, since the sines are shared by them; at least one.
-    const long long want = 8LL * info->num_sms;
-    long long chunks = (want + blocks - 1) / blocks;
-    chunks = std::max(1LL, std::min(chunks, (long long)p.heads));
-    p.heads_per_chunk = (int)((p.heads + chunks - 1) / chunks);
+    // Heads per thread share the sines: eight, as long as that leaves a wave of
+    // CTAs (four per SM), else fewer (one in a decode step: latency).  268 MB in
+    // fp16: eight heads 48 us, four 49, one 90.
+    const long long wave = 4LL * info->num_sms;
+    p.heads_per_chunk = 8;
+    while (p.heads_per_chunk > 1 && blocks * ((p.heads + p.heads_per_chunk - 1) / p.heads_per_chunk) < wave)
+        p.heads_per_chunk /= 2;
     const dim3 grid((unsigned)blocks, (unsigned)((p.heads + p.heads_per_chunk - 1) / p.heads_per_chunk));
     if (log_enabled())
         std::fprintf(stderr, "[fa] fa_rope B=%d H=%d Hkv=%d S=%d d=%d rot=%d %s vector=%d heads_per_thread=%d\n", B,

@@ -16,10 +16,9 @@
 // Products and sums are fp32, each output rounded once.
 //
 // What bounds it: every element is read and written once, 3 flops each, so
-// HBM.  A thread owns one 16-byte vector of each pair half of one token (two
-// vectors, in either layout) and walks a chunk of the heads with the same
-// sines and cosines in registers; the vectors of four heads are in flight at
-// once.  q and k go in one launch.  Strides are free, so the rows can be read
+// HBM.  A thread owns two 16-byte vectors of one token (in either layout, of
+// the turning or of the other components) and walks eight heads with the same
+// sines and cosines in registers.  q and k go in one launch.  Strides are free, so the rows can be read
 // straight out of a packed projection and written as the contiguous
 // [B, H, S, d] the attention takes.
 #pragma once
@@ -47,7 +46,7 @@ struct RopeParams {
     int H, heads, heads_per_chunk;
     int S, d, rot;
     long long units;         // B * S * slots
-    int slots;               // per token: rot / 2 / V rotating, then (d - rot) / V copying
+    int slots;               // per token: rot / 2 / V turning, then half of (d - rot) / V passing through
 };
 
 template <typename T>
@@ -75,7 +74,7 @@ struct alignas(sizeof(T) * V) RopeVec {
 
 // V elements per vector; each thread rotates V pairs (two vectors).
 template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(256) fa_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(256, 4) fa_rope_kernel(const __grid_constant__ RopeParams p) {
     using Vec = RopeVec<T, V>;
     using C = RopeType<T>;
     const long long unit = (long long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -83,82 +82,84 @@ __global__ void __launch_bounds__(256) fa_rope_kernel(const __grid_constant__ Ro
     const long long token = unit / p.slots;
     const int slot = (int)(unit - token * p.slots);
     const int b = (int)(token / p.S), s = (int)(token - (long long)b * p.S);
-    const int half = p.rot >> 1, turning = half / V;
+    const int half = p.rot >> 1, turning = half / V, passing = (p.d - p.rot) / V;
     const int h0 = (int)blockIdx.y * p.heads_per_chunk;
     const int h1 = min(h0 + p.heads_per_chunk, p.heads);
 
-    if (slot >= turning) {  // components past rot
-        const int e = p.rot + (slot - turning) * V;
-        for (int h = h0; h < h1; ++h) {
-            const RopeView &t = p.t[h >= p.H];
-            const int hh = h >= p.H ? h - p.H : h;
-            if (!t.copy) continue;
-            const T *in = reinterpret_cast<const T *>(t.in) + b * t.is[0] + hh * t.is[1] + s * t.is[2] + e;
-            T *out = reinterpret_cast<T *>(t.out) + b * t.os[0] + hh * t.os[1] + s * t.os[2] + e;
-            *reinterpret_cast<Vec *>(out) = *reinterpret_cast<const Vec *>(in);
-        }
-        return;
-    }
-
-    // Vectors at components e0 and e0 + half.  Half layout: they are the two
-    // sides of V pairs.  Interleaved: V / 2 whole pairs each (V = 1: one pair,
-    // components 2 slot and 2 slot + 1).
-    const int e0 = (kInterleaved && V == 1) ? 2 * slot : slot * V;
-    const int e1 = (kInterleaved && V == 1) ? e0 + 1 : e0 + half;
-    const long long n = (p.positions ? (long long)p.positions[b * p.pos_stride + s] : (long long)s) + p.offset;
-    float cs[V], sn[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        int pair = slot * V + i;
-        if (kInterleaved && V > 1) pair = i < V / 2 ? e0 / 2 + i : e1 / 2 + i - V / 2;
-        const unsigned long long phase = (unsigned long long)n * p.freq[pair];
-        const float x = (float)(int)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
-        float si, co;
-        sincospif(x, &si, &co);
-        cs[i] = co * p.amplitude;
-        sn[i] = si * p.amplitude * p.sin_sign;
-    }
-
-    constexpr int U = 4;  // heads in flight
-    for (int h = h0; h < h1; h += U) {
-        Vec x0[U], x1[U];
+    // Two vectors per thread.  A turning slot: at components e0 and e0 + half;
+    // half layout: they are the two sides of V pairs; interleaved: V / 2 whole
+    // pairs each (V = 1: one pair, components 2 slot and 2 slot + 1).  A slot
+    // past those: two vectors of the components that pass through.
+    const bool turns = slot < turning;
+    const int pass0 = slot - turning, pass_step = (passing + 1) / 2;
+    const bool two = turns || pass0 + pass_step < passing;
+    const int e0 = !turns ? p.rot + pass0 * V : (kInterleaved && V == 1) ? 2 * slot : slot * V;
+    const int e1 = !turns ? (two ? e0 + pass_step * V : e0) : (kInterleaved && V == 1) ? e0 + 1 : e0 + half;
+    // Heads in flight.  Four CTAs of 64 registers a thread hide the memory's
+    // latency; more heads per thread only spill (interleaved, half of d 128
+    // turning, bf16, 134 MB: one 31 us, two 37, four 57; half layout, fp16, 268 MB:
+    // one 54 us, two 48, four 48).
+    constexpr int U = kInterleaved && V > 1 ? 1 : 2;
+    Vec x0[U], x1[U];
+    auto load = [&](int h) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (h + u < h1) {
-                const bool k = h + u >= p.H;
-                const RopeView &t = p.t[k];
+            const bool k = h + u >= p.H;
+            const RopeView &t = p.t[k];
+            if (h + u < h1 && (turns || t.copy)) {
                 const T *in = reinterpret_cast<const T *>(t.in) + b * t.is[0] +
                               (h + u - (k ? p.H : 0)) * t.is[1] + s * t.is[2];
                 x0[u] = *reinterpret_cast<const Vec *>(in + e0);
                 x1[u] = *reinterpret_cast<const Vec *>(in + e1);
             }
         }
+    };
+    float cs[V], sn[V];
+    if (turns) {
+        const long long n = (p.positions ? (long long)p.positions[b * p.pos_stride + s] : (long long)s) + p.offset;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            int pair = slot * V + i;
+            if (kInterleaved && V > 1) pair = i < V / 2 ? e0 / 2 + i : e1 / 2 + i - V / 2;
+            const unsigned long long phase = (unsigned long long)n * p.freq[pair];
+            const float x = (float)(int)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
+            float si, co;
+            sincospif(x, &si, &co);
+            cs[i] = co * p.amplitude;
+            sn[i] = si * p.amplitude * p.sin_sign;
+        }
+    }
+
+    for (int h = h0; h < h1; h += U) {
+        load(h);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (h + u < h1) {
-                Vec y0, y1;
+            const bool k = h + u >= p.H;
+            const RopeView &t = p.t[k];
+            if (h + u < h1 && (turns || t.copy)) {
+                Vec y0 = x0[u], y1 = x1[u];
+                if (turns) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (!kInterleaved || V == 1) {
-                        const float a = C::up(x0[u].e[i]), c = C::up(x1[u].e[i]);
-                        y0.e[i] = C::down(a * cs[i] - c * sn[i]);
-                        y1.e[i] = C::down(a * sn[i] + c * cs[i]);
-                    } else if (i < V / 2) {
-                        const float a = C::up(x0[u].e[(2 * i) % V]), c = C::up(x0[u].e[(2 * i + 1) % V]);
-                        y0.e[(2 * i) % V] = C::down(a * cs[i] - c * sn[i]);
-                        y0.e[(2 * i + 1) % V] = C::down(a * sn[i] + c * cs[i]);
-                        const int j = i + V / 2;
-                        const float f = C::up(x1[u].e[(2 * i) % V]), g = C::up(x1[u].e[(2 * i + 1) % V]);
-                        y1.e[(2 * i) % V] = C::down(f * cs[j] - g * sn[j]);
-                        y1.e[(2 * i + 1) % V] = C::down(f * sn[j] + g * cs[j]);
+                    for (int i = 0; i < V; ++i) {
+                        if (!kInterleaved || V == 1) {
+                            const float a = C::up(x0[u].e[i]), c = C::up(x1[u].e[i]);
+                            y0.e[i] = C::down(a * cs[i] - c * sn[i]);
+                            y1.e[i] = C::down(a * sn[i] + c * cs[i]);
+                        } else if (i < V / 2) {
+                            const float a = C::up(x0[u].e[(2 * i) % V]), c = C::up(x0[u].e[(2 * i + 1) % V]);
+                            y0.e[(2 * i) % V] = C::down(a * cs[i] - c * sn[i]);
+                            y0.e[(2 * i + 1) % V] = C::down(a * sn[i] + c * cs[i]);
+                            const int j = i + V / 2;
+                            const float f = C::up(x1[u].e[(2 * i) % V]), g = C::up(x1[u].e[(2 * i + 1) % V]);
+                            y1.e[(2 * i) % V] = C::down(f * cs[j] - g * sn[j]);
+                            y1.e[(2 * i + 1) % V] = C::down(f * sn[j] + g * cs[j]);
+                        }
                     }
                 }
-                const bool k = h + u >= p.H;
-                const RopeView &t = p.t[k];
                 T *out = reinterpret_cast<T *>(t.out) + b * t.os[0] +
                          (h + u - (k ? p.H : 0)) * t.os[1] + s * t.os[2];
                 *reinterpret_cast<Vec *>(out + e0) = y0;
-                *reinterpret_cast<Vec *>(out + e1) = y1;
+                if (two) *reinterpret_cast<Vec *>(out + e1) = y1;
             }
         }
     }
