@@ -629,58 +629,68 @@ def _rope_dtype(t) -> int:
 
 def _rope(q, k, plan, positions, offset, layout, out_q, out_k, stream, direction):
     import torch
-    if layout not in ROPE_LAYOUTS:
+    lay = ROPE_LAYOUTS.get(layout)
+    if lay is None:
         raise FAError(FA_ERR_UNSUPPORTED, f"layout {layout!r}: one of {list(ROPE_LAYOUTS)}")
     dt = _rope_dtype(q)
+    dev, dtype = q.device, q.dtype
     if not q.is_cuda or q.dim() != 4:
         raise FAError(FA_ERR_INVALID_ARG, "q must be a 4-D CUDA tensor [B,H,S,d]")
-    dev = q.device
-    B, H, S, d = q.shape
+    B, H, S, d = q_shape = q.shape
     Hkv = 0
     if k is not None:
-        if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, S, d):
+        k_shape = k.shape
+        if len(k_shape) != 4 or k_shape[0] != B or k_shape[2] != S or k_shape[3] != d:
             raise FAError(FA_ERR_INVALID_ARG, "k must be [B,H_kv,S,d] matching q")
-        Hkv = k.shape[1]
-        _need_tensor("k", k, dev, q.dtype, k.shape, contiguous=False)
+        Hkv = k_shape[1]
+        _need_tensor("k", k, dev, dtype, k_shape, contiguous=False)
     elif out_k is not None:
         raise FAError(FA_ERR_INVALID_ARG, "out_k without k")
     if out_q is not None:
-        _need_tensor("out_q", out_q, dev, q.dtype, q.shape, contiguous=False)
+        _need_tensor("out_q", out_q, dev, dtype, q_shape, contiguous=False)
     if out_k is not None:
-        _need_tensor("out_k", out_k, dev, q.dtype, k.shape, contiguous=False)
-    for name, t in (("q", q), ("k", k), ("out_q", out_q), ("out_k", out_k)):
-        if t is not None and t.stride(3) != 1 and t.numel():
-            raise FAError(FA_ERR_INVALID_ARG, f"{name}: the last dimension must be contiguous")
-    if plan.freq.device != dev:
-        raise FAError(FA_ERR_INVALID_ARG, f"the plan is on {plan.freq.device}, the tensors on {dev}")
+        _need_tensor("out_k", out_k, dev, dtype, k_shape, contiguous=False)
+    rot_dim, freq, amplitude = plan
+    if freq.device != dev:
+        raise FAError(FA_ERR_INVALID_ARG, f"the plan is on {freq.device}, the tensors on {dev}")
     pos_ptr, pos_stride = None, 0
     if positions is not None:
         if positions.dtype != torch.int32 or positions.device != dev:
             raise FAError(FA_ERR_INVALID_ARG, f"positions must be int32 on {dev}")
+        steps = positions.stride()
         if positions.shape == (B, S):
-            pos_stride = positions.stride(0) if B > 1 else 0
+            pos_stride = steps[0] if B > 1 else 0
         elif positions.shape != (S,):
             raise FAError(FA_ERR_INVALID_ARG, "positions must be [B,S] or [S]")
-        if S > 1 and positions.stride(-1) != 1:
+        if S > 1 and steps[-1] != 1:
             raise FAError(FA_ERR_INVALID_ARG, "positions: the last dimension must be contiguous")
         pos_ptr = positions.data_ptr()
     sp, scope = _enter(dev, stream)
     try:
         if out_q is None:
-            out_q = torch.empty((B, H, S, d), dtype=q.dtype, device=dev)
+            out_q = torch.empty(q_shape, dtype=dtype, device=dev)
         if k is not None and out_k is None:
-            out_k = torch.empty((B, Hkv, S, d), dtype=q.dtype, device=dev)
-        if q.numel() == 0 and (k is None or k.numel() == 0):
-            return out_q if k is None else (out_q, out_k)
+            out_k = torch.empty(k_shape, dtype=dtype, device=dev)
+        if B == 0 or S == 0 or d == 0 or H == 0:
+            if k is None or k.numel() == 0:
+                return out_q if k is None else (out_q, out_k)
+            raise FAError(FA_ERR_INVALID_ARG, "q has no heads, k has some")
+        q_steps, oq_steps, k_steps, ok_steps = q.stride(), out_q.stride(), None, None
+        if Hkv:
+            k_steps, ok_steps = k.stride(), out_k.stride()
+        for steps in (q_steps, oq_steps, k_steps, ok_steps):
+            if steps is not None and steps[3] != 1:
+                raise FAError(FA_ERR_INVALID_ARG, "q, k and the outputs: the last dimension must be contiguous")
         st = (_lib or load()).fa_rope(
-            q.data_ptr(), _longs(q.stride()), out_q.data_ptr(), _longs(out_q.stride()),
-            k.data_ptr() if Hkv else None, _longs(k.stride()) if Hkv else None,
-            out_k.data_ptr() if Hkv else None, _longs(out_k.stride()) if Hkv else None,
-            pos_ptr, pos_stride, int(offset), plan.freq.data_ptr(), plan.amplitude, B, H, Hkv, S, d,
-            plan.rot_dim, ROPE_LAYOUTS[layout], direction, dt, sp)
+            q.data_ptr(), _longs(q_steps), out_q.data_ptr(), _longs(oq_steps),
+            k.data_ptr() if Hkv else None, _longs(k_steps) if Hkv else None,
+            out_k.data_ptr() if Hkv else None, _longs(ok_steps) if Hkv else None,
+            pos_ptr, pos_stride, int(offset), freq.data_ptr(), amplitude, B, H, Hkv, S, d,
+            rot_dim, lay, direction, dt, sp)
     finally:
         _leave(scope)
-    _check(st, "fa_rope")
+    if st:
+        _check(st, "fa_rope")
     return out_q if k is None else (out_q, out_k)
 
 
@@ -759,13 +769,15 @@ def paged_update(seq_lens, delta, block_table, free_ring, ring_state, block_size
 
 def _need_fp8_cache(k_cache, v_cache, k_scale, v_scale, dev):
     import torch
-    if k_cache.dim() != 4 or k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn):
+    dtype, shape = k_cache.dtype, k_cache.shape
+    if len(shape) != 4 or dtype not in (torch.uint8, torch.float8_e4m3fn):
         raise FAError(FA_ERR_INVALID_ARG,
                       "k_cache must be [num_blocks,H_kv,block_size,d], uint8 codes or float8_e4m3fn")
-    _need_tensor("k_cache", k_cache, dev, k_cache.dtype, k_cache.shape)
-    _need_tensor("v_cache", v_cache, dev, k_cache.dtype, k_cache.shape)
-    _need_tensor("k_scale", k_scale, dev, torch.float32, k_cache.shape[:2])
-    _need_tensor("v_scale", v_scale, dev, torch.float32, k_cache.shape[:2])
+    heads = shape[:2]
+    _need_tensor("k_cache", k_cache, dev, dtype, shape)
+    _need_tensor("v_cache", v_cache, dev, dtype, shape)
+    _need_tensor("k_scale", k_scale, dev, torch.float32, heads)
+    _need_tensor("v_scale", v_scale, dev, torch.float32, heads)
 
 
 def cache_append_fp8(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
@@ -830,21 +842,22 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     allowed: the row's output is 0 and its lse -inf).  Returns (o, lse).
     """
     import torch
-    if not q.is_cuda or q.dim() != 4 or not q.is_contiguous() or k_cache.dim() != 4:
+    q_shape, c_shape, t_shape = q.shape, k_cache.shape, block_table.shape
+    if not q.is_cuda or len(q_shape) != 4 or not q.is_contiguous() or len(c_shape) != 4:
         raise FAError(FA_ERR_INVALID_ARG, "q must be a contiguous CUDA tensor [B,H,Sq,d], the caches 4-D")
     dev = q.device
     dt = _dtype_code(q)
-    B, H, Sq, d = q.shape
-    nb, Hkv, bs, dc = k_cache.shape
-    if dc != d or block_table.dim() != 2:
+    B, H, Sq, d = q_shape
+    nb, Hkv, bs, dc = c_shape
+    if dc != d or len(t_shape) != 2:
         raise FAError(FA_ERR_INVALID_ARG, "the caches' last dimension must be q's; block_table [B,max_blocks]")
-    mb = block_table.shape[1]
+    mb = t_shape[1]
     _need_tensor("block_table", block_table, dev, torch.int32, (B, mb))
     _need_tensor("seq_lens", seq_lens, dev, torch.int32, (B,))
     _need_fp8_cache(k_cache, v_cache, k_scale, v_scale, dev)
     mk = mask_code(mask)
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
+        scale = d ** -0.5
     max_seq_len = int(max_seq_len)
     sp, scope = _enter(dev, stream)
     try:
@@ -853,10 +866,11 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         else:
             _need_tensor("workspace", workspace, dev, torch.uint8, workspace.shape)
+            ws_bytes = workspace.numel()
         if out is None:
             out = torch.empty_like(q)
         else:
-            _need_tensor("out", out, dev, q.dtype, q.shape)
+            _need_tensor("out", out, dev, q.dtype, q_shape)
         if lse is None:
             lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
         else:
@@ -864,9 +878,9 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
         st = (_lib or load()).fa_decode_paged_fp8(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), B, H, Hkv, Sq, d, bs, mb, nb, max_seq_len,
-            float(scale), mk, dt, sp)
+            workspace.data_ptr(), ws_bytes, B, H, Hkv, Sq, d, bs, mb, nb, max_seq_len, scale, mk, dt, sp)
     finally:
         _leave(scope)
-    _check(st, "fa_decode_paged_fp8")
+    if st:
+        _check(st, "fa_decode_paged_fp8")
     return out, lse
