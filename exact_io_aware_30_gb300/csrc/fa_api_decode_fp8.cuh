@@ -26,11 +26,11 @@ fa_status check_dec_fp8_sizes(int B, int H, int Hkv, int Sq, int d, int block_si
 }
 
 // Rows per unit (the kernel's RC) for R rows per K/V head: one chunk of the
-// smallest size that holds them, or equal chunks of at most 32 (24 for fp16 at
-// d = 256) -- beyond that two buffers each of S's and O's part columns no
-// longer fit tensor memory, and the cache is read once more per chunk (from
-// L2, the chunks being neighbours in the line of tiles).
-constexpr int dec_fp8_max_rows(int d, bool fp16) { return d == 256 && fp16 ? 24 : 32; }
+// smallest size that holds them, or equal chunks of at most 32 (24 at d = 256),
+// the cache being read once more per chunk.  Beyond that tensor memory does not
+// hold S's and O's part columns twice (fp16, d 256) or the registers O's rows
+// (32 rows at d 256: 360 us in one chunk, 334 in two; at d 128 201 against 211).
+constexpr int dec_fp8_max_rows(int d) { return d == 256 ? 24 : 32; }
 
 struct DecFp8Plan {
     int rc = 0, chunks = 1, rows_per_chunk = 0, grid = 0;
@@ -50,7 +50,7 @@ int dec_fp8_ctas_per_sm(int rc) {
 
 DecFp8Plan plan_decode_fp8(int B, int Hkv, int R, int d, bool fp16, int max_seq_len, int num_sms) {
     DecFp8Plan pl;
-    const int max_rows = dec_fp8_max_rows(d, fp16);
+    const int max_rows = dec_fp8_max_rows(d);
     pl.chunks = (R + max_rows - 1) / max_rows;
     pl.rows_per_chunk = (R + pl.chunks - 1) / pl.chunks;
     pl.chunks = (R + pl.rows_per_chunk - 1) / pl.rows_per_chunk;
@@ -84,7 +84,7 @@ fa_status launch_decode_fp8_rc(const DecFp8Params &p, const DecFp8Plan &pl, Devi
     if (pl.cuts) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(pl.grid - 1));
-        cfg.blockDim = dim3(128);
+        cfg.blockDim = dim3(kDecFp8MergeThreads<RC>);
         cfg.stream = stream;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -109,7 +109,7 @@ fa_status launch_decode_fp8(const DecFp8Params &p, const DecFp8Plan &pl, DeviceI
         case 24: return launch_decode_fp8_rc<D, kFP16, 24>(p, pl, info, stream);
         default: break;
     }
-    if constexpr (dec_fp8_max_rows(D, kFP16) >= 32) return launch_decode_fp8_rc<D, kFP16, 32>(p, pl, info, stream);
+    if constexpr (dec_fp8_max_rows(D) >= 32) return launch_decode_fp8_rc<D, kFP16, 32>(p, pl, info, stream);
     else return FA_ERR_UNSUPPORTED;  // (the plan keeps chunks within the limit)
 }
 

@@ -1009,57 +1009,66 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
 // Merges the units that a boundary between two CTAs cuts.  CTA x stands for
 // the boundary in front of CTA c = x + 1 of the attention; the first boundary
 // inside a unit merges it: the partial of CTA c - 1 (slot 2c - 1), then those of
-// c, c + 1, ... (slots 2c, 2c + 2, ...) up to the unit's end.  A warp per row.
+// c, c + 1, ... (slots 2c, 2c + 2, ...) up to the unit's end, in that order.  A
+// warp per row (all rows at once: it is a chain of three loads); lane i holds
+// the weight of partial i of 32 at a time.
+template <int RC>
+constexpr int kDecFp8MergeThreads = 32 * (RC < 4 ? 4 : RC);
+
 template <int D, bool kFP16, int RC>
-__global__ void __launch_bounds__(128) fa_decode_fp8_combine_kernel(const __grid_constant__ DecFp8Params p, int grid) {
-    const int c = (int)blockIdx.x + 1, lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+__global__ void __launch_bounds__(kDecFp8MergeThreads<RC>)
+    fa_decode_fp8_combine_kernel(const __grid_constant__ DecFp8Params p, int grid) {
+    const int c = (int)blockIdx.x + 1, lane = (int)threadIdx.x & 31, r = (int)threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the attention still runs
     const long long total = *reinterpret_cast<const long long *>(p.cuts);
+    const int *cut = p.cuts + 4 + 5 * c;
     const long long G = min((long long)grid, total);
     if (c >= G) return;
-    const int *cut = p.cuts + 4 + 5 * c;
-    if (cut[3] == 0) return;  // between two units
-    const long long begin = c * total / G - cut[3], end = begin + cut[4];
+    const int cb = cut[0], ckvh = cut[1], cchunk = cut[2], ctile = cut[3], cnt = cut[4];
+    if (ctile == 0) return;  // between two units
+    const long long begin = c * total / G - ctile, end = begin + cnt;
     if ((c - 1) * total / G > begin) return;  // an earlier boundary merges this unit
-    int n = 1;                                // partials behind the first
-    while (c + n < G && (c + n) * total / G < end) ++n;
+    // Partials of the unit: CTA c - 1's and one for each CTA from c on that
+    // begins before its end.  CTA k begins at k T / G, which is below `end` for
+    // k < end G / T: the largest such k gives the last.
+    const long long last = min((end * G - 1) / total, G - 1);
+    const int n = (int)(last - c) + 2;
     int rows;
-    const size_t row0 = dec_fp8_row0(p, cut[0], cut[1], cut[2], &rows);
+    const size_t row0 = dec_fp8_row0(p, cb, ckvh, cchunk, &rows);
+    if (r >= rows) return;
+    auto slot_row = [&](int i) { return (size_t)(i == 0 ? 2 * c - 1 : 2 * (c + i - 1)) * RC + r; };
     constexpr int PER = D / 32;
-    for (int r = warp; r < rows; r += 4) {
-        float top = -INFINITY;
-        bool nan = false;
-        for (int i = lane; i <= n; i += 32) {
-            const float v = p.part_lse[(size_t)(i == 0 ? 2 * c - 1 : 2 * (c + i - 1)) * RC + r];
-            top = fmaxf(top, v);
-            nan = nan || isnan(v);
-        }
+    float acc[PER], sum = 0.f, top = -INFINITY;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (__any_sync(0xffffffffu, nan)) top = NAN;
-        float acc[PER], sum = 0.f;
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const float mine = i0 + lane < n ? p.part_lse[slot_row(i0 + lane)] : -INFINITY;
+        const bool nan = __any_sync(0xffffffffu, isnan(mine));
+        const float high = nan ? NAN : fmaxf(top, warp_max(mine));
+        const float use = high == -INFINITY ? 0.f : high;
+        const float rescale = ptx::ex2_approx(top - use), weight = ptx::ex2_approx(mine - use);
+        top = nan || isnan(top) ? NAN : high;
+        sum *= rescale;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-        if (top != -INFINITY) {
-            for (int i = 0; i <= n; ++i) {
-                const size_t slot = (size_t)(i == 0 ? 2 * c - 1 : 2 * (c + i - 1)) * RC + r;
-                const float w = ptx::ex2_approx(p.part_lse[slot] - top);
-                sum += w;
-                const float *src = p.part_o + slot * D + lane * PER;
+        for (int e = 0; e < PER; ++e) acc[e] *= rescale;
+#pragma unroll 4
+        for (int i = 0; i < min(32, n - i0); ++i) {
+            const float w = __shfl_sync(0xffffffffu, weight, i);
+            const float *src = p.part_o + slot_row(i0 + i) * D + lane * PER;
+            sum += w;
 #pragma unroll
-                for (int e = 0; e < PER; e += 2) {
-                    const float2 v = *reinterpret_cast<const float2 *>(src + e);
-                    acc[e] = fmaf(w, v.x, acc[e]);
-                    acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
-                }
+            for (int e = 0; e < PER; e += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(src + e);
+                acc[e] = fmaf(w, v.x, acc[e]);
+                acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
             }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + (row0 + r) * D + lane * PER);
-#pragma unroll
-        for (int e = 0; e < PER; e += 2) dst[e / 2] = pack2b<kFP16>(acc[e] * inv, acc[e + 1] * inv);
-        if (lane == 0) p.lse[row0 + r] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + (row0 + r) * D + lane * PER);
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) dst[e / 2] = pack2b<kFP16>(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) p.lse[row0 + r] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
 }  // namespace fa

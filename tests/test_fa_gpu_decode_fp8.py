@@ -301,6 +301,34 @@ def test_a_cache_of_over_32_bits():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("H,Hkv,Sq,d", [(4, 4, 1, 64), (8, 2, 1, 128), (32, 1, 1, 128), (20, 1, 1, 256)])
+def test_a_wait_that_runs_out_is_reported_and_the_context_recovers(H, Hkv, Sq, d):
+    # one, four, thirty-two and twenty rows per K/V head: the warpgroup shapes
+    p = _problem(3, H, Hkv, Sq, d, 16, [700, 3, 129], inputs.BF16, seed=51)
+    dev = _device(p)
+    assert fa.device_error() == fa.FA_OK
+    fa.set_debug_stall_ms(50)
+    try:
+        fa.decode_paged_fp8(*dev, 700, mask="causal")
+        torch.cuda.synchronize()
+    finally:
+        fa.set_debug_stall_ms(0)
+    assert fa.device_error() == fa.FA_ERR_DEVICE_TIMEOUT
+    assert fa.device_error() == fa.FA_OK
+    o, lse = fa.decode_paged_fp8(*dev, 700, mask="causal")
+    _check(p, o, lse, "causal", 700)
+
+
+@pytest.mark.parametrize("B", [193, 700])
+def test_more_requests_than_threads_with_uneven_lengths(B):
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 200, B)
+    lens[rng.integers(0, B)] = 3000
+    p = _problem(B, 2, 1, 1, 64, 16, lens, inputs.BF16, seed=52)
+    o, lse = fa.decode_paged_fp8(*_device(p), 3000)
+    _check(p, o, lse, "none", 3000)
+
+
 # ------------------------------------------------------------------ the step as it is used
 
 @pytest.mark.parametrize("dtype,H,Hkv,d,bs", [(torch.bfloat16, 8, 2, 128, 16), (torch.float16, 4, 4, 64, 32),
