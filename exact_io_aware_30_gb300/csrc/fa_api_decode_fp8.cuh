@@ -19,6 +19,7 @@ fa_status check_dec_fp8_sizes(int B, int H, int Hkv, int Sq, int d, int block_si
     if ((long long)(H / Hkv) * Sq > 128) return FA_ERR_UNSUPPORTED;  // rows of one K/V head
     if (max_blocks < 1 || max_seq_len < 1 || (long long)max_seq_len > (long long)max_blocks * block_size)
         return FA_ERR_INVALID_ARG;
+    if (max_seq_len > 0x7fffffff - 512) return FA_ERR_INVALID_ARG;  // key numbers of a whole step stay below 2^31
     if ((long long)B * H * Sq > 0x7fffffffLL / 2 || (long long)B * max_blocks > 0x7fffffffLL)
         return FA_ERR_INVALID_ARG;
     if ((long long)Hkv * (H / Hkv * Sq) > 0x7fffffffLL) return FA_ERR_INVALID_ARG;

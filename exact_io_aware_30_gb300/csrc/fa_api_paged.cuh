@@ -127,7 +127,7 @@ fa_status cache_append_impl(const void *k, const void *v, long long k_token_stri
     if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) return FA_ERR_UNSUPPORTED;
     const fa_status sizes = check_fp8_cache(num_blocks, Hkv, block_size, d);
     if (sizes != FA_OK) return sizes;
-    if (T < 0 || Hkv > 65535) return FA_ERR_INVALID_ARG;
+    if (T < 0 || T > (1 << 30) || Hkv > 65535) return FA_ERR_INVALID_ARG;
     if (T == 0) return FA_OK;
     if (!k || !v || !slot_map || !k_cache || !v_cache || !k_scale || !v_scale) return FA_ERR_INVALID_ARG;
     const long long strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};

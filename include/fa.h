@@ -399,7 +399,7 @@ fa_status fa_paged_update(const int *seq_lens, const int *delta, int *block_tabl
  * NaN).  A stored scale that is no positive finite number counts as none.
  *
  *   k, v        [T, H_kv, d] 16-bit by element strides (token, head); values
- *               of a head adjacent; the strides are >= 0
+ *               of a head adjacent; the strides are >= 0; T <= 2^30
  *   slot_map    device int32 [T], as fa_paged_update writes it: row t goes to
  *               slot s = block * block_size + place; rows whose slot is outside
  *               [0, num_blocks * block_size) are skipped.  Rows of one block
@@ -440,7 +440,9 @@ fa_status fa_cache_append_fp8(const void *k, const void *v, long long k_token_st
  *                gets O = 0 and lse = -inf
  *   block_table  an entry outside [0, num_blocks) reads zeros
  *   workspace    at least fa_decode_fp8_workspace_query() bytes, 256-byte
- *                aligned; may be NULL where that is 0
+ *                aligned; calls that may overlap in time (other streams, graphs
+ *                replayed beside each other) need one each
+ *   max_seq_len  at most 2^31 - 513
  * Cache slots past a request's length may hold any codes, NaN included.
  */
 fa_status fa_decode_paged_fp8(const void *q, const void *k_cache, const void *v_cache,

@@ -159,6 +159,7 @@ def _append(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=fa.DTYPE_FP32), fa.FA_ERR_UNSUPPORTED), (dict(d=96), fa.FA_ERR_UNSUPPORTED),
     (dict(bs=24), fa.FA_ERR_UNSUPPORTED), (dict(Hkv=0), fa.FA_ERR_INVALID_ARG), (dict(T=-1), fa.FA_ERR_INVALID_ARG),
+    (dict(T=(1 << 30) + 1), fa.FA_ERR_INVALID_ARG),
     (dict(blocks=0), fa.FA_ERR_INVALID_ARG), (dict(blocks=1 << 27), fa.FA_ERR_INVALID_ARG),
     (dict(Hkv=65536), fa.FA_ERR_INVALID_ARG), (dict(v=None), fa.FA_ERR_INVALID_ARG),
     (dict(kt=-1), fa.FA_ERR_INVALID_ARG), (dict(k=FAKE + 1), fa.FA_ERR_MISALIGNED),
@@ -192,7 +193,8 @@ def _decode(**kw):
     (dict(bs=256), fa.FA_ERR_UNSUPPORTED), (dict(mask=fa.MASK_SLIDING_WINDOW), fa.FA_ERR_UNSUPPORTED),
     (dict(H=9), fa.FA_ERR_INVALID_ARG), (dict(Hkv=0), fa.FA_ERR_INVALID_ARG), (dict(Sq=0), fa.FA_ERR_INVALID_ARG),
     (dict(Sq=33), fa.FA_ERR_UNSUPPORTED), (dict(max_len=0), fa.FA_ERR_INVALID_ARG),
-    (dict(max_len=129), fa.FA_ERR_INVALID_ARG), (dict(blocks=0), fa.FA_ERR_INVALID_ARG),
+    (dict(max_len=129), fa.FA_ERR_INVALID_ARG),
+    (dict(B=1, max_blocks=1 << 27, max_len=0x7fffffff - 511), fa.FA_ERR_INVALID_ARG), (dict(blocks=0), fa.FA_ERR_INVALID_ARG),
     (dict(scale=float("nan")), fa.FA_ERR_INVALID_ARG), (dict(scale=-0.1), fa.FA_ERR_INVALID_ARG),
     (dict(ks=None), fa.FA_ERR_INVALID_ARG), (dict(kc=FAKE + GB + 8), fa.FA_ERR_MISALIGNED),
     (dict(vs=FAKE + 4 * GB + 1), fa.FA_ERR_MISALIGNED), (dict(ws=FAKE + 9 * GB + 16), fa.FA_ERR_MISALIGNED)])
