@@ -299,6 +299,32 @@ fa_status set_smem(K kern, int bytes, bool &done) {
     return FA_OK;
 }
 
+// Launches a kernel that begins with ptx::wait_for_previous_kernel(), so that
+// its launch and set-up overlap the end of the work in front of it.
+template <typename... Args>
+fa_status launch_overlapped(void (*kern)(Args...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                            cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
 // Every CTA of the two backward kernels allocates all 512 tensor-memory
 // columns, so they request enough shared memory to run one CTA per SM.
 constexpr int kBwdMinSmem = 120 * 1024;

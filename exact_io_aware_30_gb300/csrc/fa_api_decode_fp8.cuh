@@ -80,24 +80,11 @@ fa_status launch_decode_fp8_rc(const DecFp8Params &p, const DecFp8Plan &pl, Devi
     constexpr int kind = RC == 1 ? 0 : RC == 4 ? 1 : RC == 8 ? 2 : RC == 16 ? 3 : RC == 24 ? 4 : 5;
     const int slot = ((D == 256 ? 2 : D == 128 ? 1 : 0) * 2 + (kFP16 ? 1 : 0)) * 6 + kind;
     if (set_smem(fa_decode_fp8_kernel<C>, C::SMEM_BYTES, info.attr_dec_fp8[slot]) != FA_OK) return FA_ERR_CUDA;
-    fa_decode_fp8_kernel<C><<<(unsigned)pl.grid, C::NUM_THREADS, C::SMEM_BYTES, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    if (pl.cuts) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(pl.grid - 1));
-        cfg.blockDim = dim3(kDecFp8MergeThreads<RC>);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, kFP16, RC>, p, pl.grid) != cudaSuccess) {
-            cudaGetLastError();
-            return FA_ERR_CUDA;
-        }
-    }
-    return FA_OK;
+    const fa_status st = launch_overlapped(fa_decode_fp8_kernel<C>, dim3((unsigned)pl.grid), C::NUM_THREADS,
+                                           C::SMEM_BYTES, 1, stream, p);
+    if (st != FA_OK || !pl.cuts) return st;
+    return launch_overlapped(fa_decode_fp8_combine_kernel<D, kFP16, RC>, dim3((unsigned)(pl.grid - 1)),
+                             kDecFp8MergeThreads<RC>, 0, 1, stream, p, pl.grid);
 }
 
 template <int D, bool kFP16>

@@ -65,6 +65,7 @@ fa_status paged_update_impl(const int *seq_lens, const int *delta, int *block_ta
     if (st != FA_OK) return st;
 
     PagedUpdateParams p;
+    std::memset(&p, 0, sizeof(p));
     p.seq_lens = seq_lens;
     p.delta = delta;
     p.ring_state = ring_state;
@@ -89,25 +90,10 @@ fa_status paged_update_impl(const int *seq_lens, const int *delta, int *block_ta
     if (log_enabled())
         std::fprintf(stderr, "[fa] fa_paged_update B=%d max_blocks=%d bs=%d rows=%d ctas=%d\n", B, max_blocks,
                      block_size, max_tokens, ranks);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ranks);
     // few requests and rows: a small CTA, whose barriers cost less
     const bool small = B <= 128 && max_tokens <= 512;
-    cfg.blockDim = dim3(small ? 128 : 1024);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = p.meet ? (unsigned)ranks : 1;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, small ? fa_paged_update_kernel<128> : fa_paged_update_kernel<1024>, p) !=
-        cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_CUDA;
-    }
-    return FA_OK;
+    return launch_overlapped(small ? fa_paged_update_kernel<128> : fa_paged_update_kernel<1024>, dim3((unsigned)ranks),
+                             small ? 128 : 1024, 0, p.meet ? (unsigned)ranks : 1u, stream, p);
 }
 
 // Sizes of an 8-bit cache shared by the append and the decode.
@@ -151,6 +137,7 @@ fa_status cache_append_impl(const void *k, const void *v, long long k_token_stri
     if (st != FA_OK) return st;
 
     AppendParams p;
+    std::memset(&p, 0, sizeof(p));
     p.x[0] = static_cast<const uint8_t *>(k);
     p.x[1] = static_cast<const uint8_t *>(v);
     p.token_stride[0] = k_token_stride;
@@ -193,8 +180,7 @@ fa_status cache_append_impl(const void *k, const void *v, long long k_token_stri
                             : (vec ? fa_cache_append_kernel<false, true, 16> : fa_cache_append_kernel<false, false, 16>))
                     : (fp16 ? (vec ? fa_cache_append_kernel<true, true, 8> : fa_cache_append_kernel<true, false, 8>)
                             : (vec ? fa_cache_append_kernel<false, true, 8> : fa_cache_append_kernel<false, false, 8>));
-    kern<<<grid, kAppendThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return launch_overlapped(kern, grid, kAppendThreads, 0, 1, stream, p);
 }
 
 }  // namespace

@@ -86,11 +86,8 @@ bool same_view(const StridedView &a, const StridedView &b) {
 
 template <typename T, int V>
 fa_status launch_rope(const RopeParams &p, int layout, dim3 grid, cudaStream_t stream) {
-    if (layout == FA_ROPE_INTERLEAVED)
-        fa_rope_kernel<T, V, true><<<grid, 256, 0, stream>>>(p);
-    else
-        fa_rope_kernel<T, V, false><<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return launch_overlapped(layout == FA_ROPE_INTERLEAVED ? fa_rope_kernel<T, V, true> : fa_rope_kernel<T, V, false>,
+                             grid, 256, 0, 1, stream, p);
 }
 
 fa_status rope_impl(const void *q, const long long *q_strides, void *q_out, const long long *q_out_strides,

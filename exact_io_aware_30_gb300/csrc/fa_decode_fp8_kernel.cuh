@@ -981,6 +981,7 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
         ptx::prefetch_tensormap(&p.tm_k);
         ptx::prefetch_tensormap(&p.tm_v);
     }
+    ptx::wait_for_previous_kernel();
     // (the small arrays are not yet in use: the prefix sums borrow their first bytes)
     const DecFp8It it = dec_fp8_begin<C::NUM_THREADS>(p, reinterpret_cast<long long *>(sF));
     ptx::tc_fence_before();
@@ -988,7 +989,7 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     // the merge may be set up now; it waits for this grid's end before it reads
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    ptx::let_next_kernel_begin();
 
     if (warp < 4 * C::NWG) {
         dec_fp8_softmax_role<C>(p, it, sQ, sP, sV, sF, bars, tmem, ctl);
@@ -1019,7 +1020,7 @@ template <int D, bool kFP16, int RC>
 __global__ void __launch_bounds__(kDecFp8MergeThreads<RC>)
     fa_decode_fp8_combine_kernel(const __grid_constant__ DecFp8Params p, int grid) {
     const int c = (int)blockIdx.x + 1, lane = (int)threadIdx.x & 31, r = (int)threadIdx.x >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the attention still runs
+    ptx::wait_for_previous_kernel();  // (launched while the attention still runs)
     const long long total = *reinterpret_cast<const long long *>(p.cuts);
     const int *cut = p.cuts + 4 + 5 * c;
     const long long G = min((long long)grid, total);

@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
     __shared__ int s_ok[kPagedThreads];
     const int tid = (int)threadIdx.x, bs = 1 << p.bs_log2;
     const int rank = (int)blockIdx.x, ranks = (int)gridDim.x;
+    ptx::wait_for_previous_kernel();
     const long long head = min(max(p.ring_state[0], 0), p.ring_size - 1);
     const long long count = min(max(p.ring_state[1], 0), p.ring_size);
     const long long most = (long long)p.max_blocks << p.bs_log2;
@@ -295,7 +296,9 @@ __global__ void __launch_bounds__(kAppendThreads, HOLD == 8 ? 4 : 2) fa_cache_ap
         return s >= 0 && s < p.slots ? s : -1;
     };
     const int first = row0 - BACK;
+    ptx::wait_for_previous_kernel();
     for (int j = tid; j < BACK + p.rows_per_cta + BACK; j += kAppendThreads) win[j] = slot_of(first + j);
+    if (tid < bs) owner[tid] = -1;
     // this thread's group, its place in it, and the pairs it takes
     const int gsize = 32 << p.wpu_log2, group = tid / gsize, in_group = tid & (gsize - 1);
     const int groups = kAppendThreads / gsize, pairs = 2 * p.Hkv;
@@ -322,148 +325,158 @@ __global__ void __launch_bounds__(kAppendThreads, HOLD == 8 ? 4 : 2) fa_cache_ap
             if (seen >= 0) prev = p.slot_map[seen] >> p.bs_log2;
         }
     }
-    for (int row = row0; row < row1; ++row) {
-        const int j0 = row - first;
-        const int slot = win[j0];
-        if (slot < 0) continue;  // a skipped row
-        const int block = slot >> p.bs_log2;
-        if (block == prev) continue;  // an earlier row leads this block
-        prev = block;
+    // The leaders among the CTA's rows, 32 at a time (every warp for itself): a
+    // live row whose last live row before it is of another block.
+    bool used = false;  // owner holds an earlier leader's rows
+    for (int seg = row0; seg < row1; seg += 32) {
+        const int here = seg + lane < row1 ? win[seg + lane - first] : -1;
+        const uint32_t live = __ballot_sync(0xffffffffu, here >= 0), before = live & ((1u << lane) - 1);
+        const int at_before = __shfl_sync(0xffffffffu, here, before ? 31 - __clz(before) : 0);
+        const int block_before = before ? at_before >> p.bs_log2 : prev;
+        uint32_t leaders = __ballot_sync(0xffffffffu, here >= 0 && here >> p.bs_log2 != block_before);
+        if (live) prev = __shfl_sync(0xffffffffu, here, 31 - __clz(live)) >> p.bs_log2;
+        for (; leaders; leaders &= leaders - 1) {
+            const int row = seg + __ffs(leaders) - 1, j0 = row - first;
+            const int block = win[j0] >> p.bs_log2;
 
-        // its rows: up to the first live row of another block
-        __syncthreads();
-        if (tid < bs) owner[tid] = -1;
-        __syncthreads();
-        int end = BACK;
-#pragma unroll
-        for (int k = BACK / 32 - 1; k >= 0; --k) {
-            const int s = win[j0 + k * 32 + lane];
-            const uint32_t other = __ballot_sync(0xffffffffu, s >= 0 && s >> p.bs_log2 != block);
-            if (other) end = k * 32 + __ffs(other) - 1;
-        }
-        if (tid < end) {  // a slot named twice: the later row
-            const int s = win[j0 + tid];
-            if (s >= 0) atomicMax(&owner[s & (bs - 1)], row + tid);
-        }
-        if (end == BACK) {  // (rows past the first look)
-            int stop = p.T;
-            for (int r0 = row + BACK; r0 < stop; r0 += kAppendThreads) {
+            // its rows: up to the first live row of another block
+            if (used) {
                 __syncthreads();
-                if (tid == 0) s_row = stop;
+                if (tid < bs) owner[tid] = -1;
                 __syncthreads();
-                const int s = slot_of(r0 + tid);
-                if (s >= 0 && s >> p.bs_log2 != block) atomicMin(&s_row, r0 + tid);
-                __syncthreads();
-                stop = s_row;
-                if (s >= 0 && r0 + tid < stop) atomicMax(&owner[s & (bs - 1)], r0 + tid);
             }
-        }
-        __syncthreads();
-
-        const bool begun = owner[0] >= 0;
-        for (int pair = (int)blockIdx.y * groups + group; pair < pairs; pair += (int)gridDim.y * groups) {
-            const int kv = pair >= p.Hkv, head = pair - (kv ? p.Hkv : 0);
-            const uint16_t *x = reinterpret_cast<const uint16_t *>(p.x[kv]) + head * p.head_stride[kv];
-            const size_t bh = (size_t)block * p.Hkv + head;
-            uint8_t *codes = p.cache[kv] + (bh << (p.d_log2 + p.bs_log2));
-            const float old = p.scale[kv][bh];
-            auto source = [&](int u, int r) {
-                return x + r * p.token_stride[kv] + ((u & ((1 << vec_log2) - 1)) << 3);
-            };
-            // Only what every call does is unrolled (registers cannot be indexed
-            // otherwise); infinities, scales that are no powers of two and growth
-            // of the scale take the short loops, which read again: the whole in
-            // line was several times the code, and fetching it cost a decode step
-            // more than its data (128 rows x 40 heads: 19 us against 12; 8,203 rows
-            // of prompts x 8 heads: 45 against 24).
-            uint4 held[HOLD];
-            uint32_t mine = 0;  // which of this lane's vectors are written
+            used = true;
+            int end = BACK;
 #pragma unroll
-            for (int i = 0; i < HOLD; ++i) {
-                const int u = in_group + i * gsize;
-                const int r = u < units ? owner[u >> vec_log2] : -1;
-                held[i] = make_uint4(0, 0, 0, 0);
-                if (r >= 0) {
-                    mine |= 1u << i;
-                    held[i] = load8_16<kVec>(source(u, r));
+            for (int k = BACK / 32 - 1; k >= 0; --k) {
+                const int s = win[j0 + k * 32 + lane];
+                const uint32_t other = __ballot_sync(0xffffffffu, s >= 0 && s >> p.bs_log2 != block);
+                if (other) end = k * 32 + __ffs(other) - 1;
+            }
+            if (tid < end) {  // a slot named twice: the later row
+                const int s = win[j0 + tid];
+                if (s >= 0) atomicMax(&owner[s & (bs - 1)], row + tid);
+            }
+            if (end == BACK) {  // (rows past the first look)
+                int stop = p.T;
+                for (int r0 = row + BACK; r0 < stop; r0 += kAppendThreads) {
+                    __syncthreads();
+                    if (tid == 0) s_row = stop;
+                    __syncthreads();
+                    const int s = slot_of(r0 + tid);
+                    if (s >= 0 && s >> p.bs_log2 != block) atomicMin(&s_row, r0 + tid);
+                    __syncthreads();
+                    stop = s_row;
+                    if (s >= 0 && r0 + tid < stop) atomicMax(&owner[s & (bs - 1)], r0 + tid);
                 }
             }
-            // 16-bit magnitudes are ordered as whole numbers
-            uint32_t top2 = 0;
-#pragma unroll
-            for (int i = 0; i < HOLD; ++i) {
-                top2 = __vmaxu2(top2, __vmaxu2(held[i].x & 0x7fff7fffu, held[i].y & 0x7fff7fffu));
-                top2 = __vmaxu2(top2, __vmaxu2(held[i].z & 0x7fff7fffu, held[i].w & 0x7fff7fffu));
-            }
-            constexpr uint32_t kInf = kFP16 ? 0x7c00u : 0x7f80u;
-            uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-            if (top >= kInf) {  // the largest finite one
-                top = 0;
-                for (int u = in_group; u < units; u += gsize) {
-                    const int r = owner[u >> vec_log2];
-                    for (int j = 0; r >= 0 && j < 8; ++j) {
-                        const uint32_t v = source(u, r)[j] & 0x7fffu;
-                        top = max(top, v < kInf ? v : 0u);
-                    }
-                }
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (p.wpu_log2 > 0) {
-                if ((tid & 31) == 0) s_max[tid >> 5] = top;
-                ptx::named_bar_sync(1 + group, gsize);  // also: the group has read the old scale
-                for (int w = 0; w < gsize / 32; ++w) top = max(top, s_max[group * (gsize / 32) + w]);
-                ptx::named_bar_sync(1 + group, gsize);
-            }
-            __syncwarp();
-            const float need = scale_for(unpack16<kFP16>(top).x);
-            // (an old scale that is no positive finite number counts as none)
-            const float now = begun || !(old > need) || isinf(old) ? need : old;
-            const bool grew = !begun && old > 0.f && now > old;
-            const uint32_t nb = __float_as_uint(now);
-            if ((nb & 0x7fffffu) == 0 && (nb >> 23) < 254) {  // x / now by its exact inverse
-                const float inv = __uint_as_float((254u - (nb >> 23)) << 23);
+            __syncthreads();
+
+            const bool begun = owner[0] >= 0;
+            for (int pair = (int)blockIdx.y * groups + group; pair < pairs; pair += (int)gridDim.y * groups) {
+                const int kv = pair >= p.Hkv, head = pair - (kv ? p.Hkv : 0);
+                const uint16_t *x = reinterpret_cast<const uint16_t *>(p.x[kv]) + head * p.head_stride[kv];
+                const size_t bh = (size_t)block * p.Hkv + head;
+                uint8_t *codes = p.cache[kv] + (bh << (p.d_log2 + p.bs_log2));
+                const float old = p.scale[kv][bh];
+                auto source = [&](int u, int r) {
+                    return x + r * p.token_stride[kv] + ((u & ((1 << vec_log2) - 1)) << 3);
+                };
+                // Only what every call does is unrolled (registers cannot be indexed
+                // otherwise); infinities, scales that are no powers of two and growth
+                // of the scale take the short loops, which read again: the whole in
+                // line was several times the code, and fetching it cost a decode step
+                // more than its data (128 rows x 40 heads: 19 us against 12; 8,203 rows
+                // of prompts x 8 heads: 45 against 24).
+                uint4 held[HOLD];
+                uint32_t mine = 0;  // which of this lane's vectors are written
 #pragma unroll
                 for (int i = 0; i < HOLD; ++i) {
-                    if (!(mine >> i & 1)) continue;
-                    const uint32_t ws[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
-                    float f[8];
+                    const int u = in_group + i * gsize;
+                    const int r = u < units ? owner[u >> vec_log2] : -1;
+                    held[i] = make_uint4(0, 0, 0, 0);
+                    if (r >= 0) {
+                        mine |= 1u << i;
+                        held[i] = load8_16<kVec>(source(u, r));
+                    }
+                }
+                // 16-bit magnitudes are ordered as whole numbers
+                uint32_t top2 = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 y = unpack16<kFP16>(ws[j]);
-                        f[2 * j] = y.x * inv;
-                        f[2 * j + 1] = y.y * inv;
+                for (int i = 0; i < HOLD; ++i) {
+                    top2 = __vmaxu2(top2, __vmaxu2(held[i].x & 0x7fff7fffu, held[i].y & 0x7fff7fffu));
+                    top2 = __vmaxu2(top2, __vmaxu2(held[i].z & 0x7fff7fffu, held[i].w & 0x7fff7fffu));
+                }
+                constexpr uint32_t kInf = kFP16 ? 0x7c00u : 0x7f80u;
+                uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+                if (top >= kInf) {  // the largest finite one
+                    top = 0;
+                    for (int u = in_group; u < units; u += gsize) {
+                        const int r = owner[u >> vec_log2];
+                        for (int j = 0; r >= 0 && j < 8; ++j) {
+                            const uint32_t v = source(u, r)[j] & 0x7fffu;
+                            top = max(top, v < kInf ? v : 0u);
+                        }
                     }
-                    *reinterpret_cast<uint2 *>(codes + (size_t)(in_group + i * gsize) * 8) =
-                        make_uint2(ptx::pack_e4m3x4(f[0], f[1], f[2], f[3]), ptx::pack_e4m3x4(f[4], f[5], f[6], f[7]));
                 }
-            } else {
-#pragma unroll 1
-                for (int u = in_group; u < units; u += gsize) {
-                    const int r = owner[u >> vec_log2];
-#pragma unroll 1
-                    for (int j = 0; r >= 0 && j < 8; ++j)
-                        codes[(size_t)u * 8 + j] =
-                            (uint8_t)ptx::pack_e4m3x4(__fdiv_rn(unpack16<kFP16>(source(u, r)[j]).x, now), 0.f, 0.f, 0.f);
+                top = __reduce_max_sync(0xffffffffu, top);
+                if (p.wpu_log2 > 0) {
+                    if ((tid & 31) == 0) s_max[tid >> 5] = top;
+                    ptx::named_bar_sync(1 + group, gsize);  // also: the group has read the old scale
+                    for (int w = 0; w < gsize / 32; ++w) top = max(top, s_max[group * (gsize / 32) + w]);
+                    ptx::named_bar_sync(1 + group, gsize);
                 }
-            }
-            if (grew) {
-#pragma unroll 1
-                for (int u = in_group; u < units; u += gsize) {
-                    if (owner[u >> vec_log2] >= 0) continue;
-                    uint2 *dst = reinterpret_cast<uint2 *>(codes + (size_t)u * 8);
-                    const uint2 w = *dst;
-                    uint32_t out[2] = {0, 0};
-#pragma unroll 1
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 y = unpack_e4m3x2((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
-                        const uint32_t two = ptx::pack_e4m3x4(__fdiv_rn(y.x * old, now), __fdiv_rn(y.y * old, now), 0.f, 0.f);
-                        if (j < 2) out[0] |= two << (16 * j);
-                        else out[1] |= two << (16 * (j - 2));
+                __syncwarp();
+                const float need = scale_for(unpack16<kFP16>(top).x);
+                // (an old scale that is no positive finite number counts as none)
+                const float now = begun || !(old > need) || isinf(old) ? need : old;
+                const bool grew = !begun && old > 0.f && now > old;
+                const uint32_t nb = __float_as_uint(now);
+                if ((nb & 0x7fffffu) == 0 && (nb >> 23) < 254) {  // x / now by its exact inverse
+                    const float inv = __uint_as_float((254u - (nb >> 23)) << 23);
+#pragma unroll
+                    for (int i = 0; i < HOLD; ++i) {
+                        if (!(mine >> i & 1)) continue;
+                        const uint32_t ws[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
+                        float f[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 y = unpack16<kFP16>(ws[j]);
+                            f[2 * j] = y.x * inv;
+                            f[2 * j + 1] = y.y * inv;
+                        }
+                        *reinterpret_cast<uint2 *>(codes + (size_t)(in_group + i * gsize) * 8) =
+                            make_uint2(ptx::pack_e4m3x4(f[0], f[1], f[2], f[3]), ptx::pack_e4m3x4(f[4], f[5], f[6], f[7]));
                     }
-                    *dst = make_uint2(out[0], out[1]);
+                } else {
+#pragma unroll 1
+                    for (int u = in_group; u < units; u += gsize) {
+                        const int r = owner[u >> vec_log2];
+#pragma unroll 1
+                        for (int j = 0; r >= 0 && j < 8; ++j)
+                            codes[(size_t)u * 8 + j] =
+                                (uint8_t)ptx::pack_e4m3x4(__fdiv_rn(unpack16<kFP16>(source(u, r)[j]).x, now), 0.f, 0.f, 0.f);
+                    }
                 }
+                if (grew) {
+#pragma unroll 1
+                    for (int u = in_group; u < units; u += gsize) {
+                        if (owner[u >> vec_log2] >= 0) continue;
+                        uint2 *dst = reinterpret_cast<uint2 *>(codes + (size_t)u * 8);
+                        const uint2 w = *dst;
+                        uint32_t out[2] = {0, 0};
+#pragma unroll 1
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 y = unpack_e4m3x2((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
+                            const uint32_t two = ptx::pack_e4m3x4(__fdiv_rn(y.x * old, now), __fdiv_rn(y.y * old, now), 0.f, 0.f);
+                            if (j < 2) out[0] |= two << (16 * j);
+                            else out[1] |= two << (16 * (j - 2));
+                        }
+                        *dst = make_uint2(out[0], out[1]);
+                    }
+                }
+                if (in_group == 0) p.scale[kv][bh] = now;
             }
-            if (in_group == 0) p.scale[kv][bh] = now;
         }
     }
 }

@@ -27,6 +27,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "sm103_ptx.cuh"
+
 namespace fa {
 
 struct RopeView {
@@ -77,6 +79,7 @@ template <typename T, int V, bool kInterleaved>
 __global__ void __launch_bounds__(256, 4) fa_rope_kernel(const __grid_constant__ RopeParams p) {
     using Vec = RopeVec<T, V>;
     using C = RopeType<T>;
+    ptx::wait_for_previous_kernel();
     const long long unit = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (unit >= p.units) return;
     const long long token = unit / p.slots;

@@ -431,6 +431,19 @@ __device__ __forceinline__ void setmaxnreg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ------------------------------------------------------ programmatic launch
+// A kernel launched with the programmatic attribute may begin before the one in
+// front of it in the stream has ended; this waits for that end and for its
+// writes.  Everything before it must touch no memory that other kernels use.
+__device__ __forceinline__ void wait_for_previous_kernel() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Lets the kernel behind this one begin once every CTA has come here (or ended).
+__device__ __forceinline__ void let_next_kernel_begin() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------ named barriers
 // Barrier `id` over `n` threads (a multiple of 32); orders shared memory like
 // __syncthreads among the participants.
