@@ -30,7 +30,7 @@ fa_status check_dec_fp8_sizes(int B, int H, int Hkv, int Sq, int d, int block_si
 // smallest size that holds them, or equal chunks of at most 32 (24 at d = 256),
 // the cache being read once more per chunk.  Beyond that tensor memory does not
 // hold S's and O's part columns twice (fp16, d 256) or the registers O's rows
-// (32 rows at d 256: 360 us in one chunk, 334 in two; at d 128 201 against 211).
+// (32 rows at d 256: 360 us in one chunk, 334 in two; at d 128 164 against 211).
 constexpr int dec_fp8_max_rows(int d) { return d == 256 ? 24 : 32; }
 
 struct DecFp8Plan {

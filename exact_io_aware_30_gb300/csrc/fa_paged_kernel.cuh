@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
 // among its rows which row writes which slot of the block, and then gives each
 // pair's block to a group of WPU warps: enough that a lane holds its whole
 // share, eight 16-byte vectors (sixteen for blocks of 32,768 values), between
-// finding the maximum and writing the codes.  So a row is read once.  HBM bound
-// for prompts (6 bytes per value), latency for a decode step.
+// finding the maximum and writing the codes.  So a row is read once.  Bound by
+// latency, slots then rows and scale then stores: 128 rows x 40 heads 8.8 us, 8,203
+// rows x 8 heads (50 MB) 14.3 us, where the copy rate would take 0.6 and 7.4.
 
 struct AppendParams {
     const uint8_t *x[2];        // new K and V rows, 16-bit
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kAppendThreads, HOLD == 8 ? 4 : 2) fa_cache_ap
     const int tid = (int)threadIdx.x, lane = tid & 31, bs = 1 << p.bs_log2;
     const int row0 = (int)blockIdx.x * p.rows_per_cta;
     const int row1 = min(row0 + p.rows_per_cta, p.T);
-    auto slot_of = [&](int row) -> int {
+    auto slot_of = [&](int row) -> int {  // -1: skipped
         const int s = row >= 0 && row < p.T ? p.slot_map[row] : -1;
         return s >= 0 && s < p.slots ? s : -1;
     };

@@ -16,11 +16,12 @@
 // Products and sums are fp32, each output rounded once.
 //
 // What bounds it: every element is read and written once, 3 flops each, so
-// HBM (268 MB in 45 us, 87 % of copy).  A thread owns two 16-byte vectors of one token (in either layout, of
-// the turning or of the other components) and walks eight heads with the same
-// sines and cosines in registers.  q and k go in one launch.  Strides are free, so the rows can be read
-// straight out of a packed projection and written as the contiguous
-// [B, H, S, d] the attention takes.
+// HBM (268 MB in 45 us, 87 % of a copy).  A thread owns two 16-byte vectors of
+// one token (in either layout, of the turning or of the other components) and
+// walks eight heads with the same sines and cosines in registers.  q and k go in
+// one launch.  Strides are free, so the rows can be read straight out of a
+// packed projection and written as the contiguous [B, H, S, d] the attention
+// takes.
 #pragma once
 
 #include <cuda_bf16.h>

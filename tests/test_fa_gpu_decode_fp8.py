@@ -64,9 +64,11 @@ def _device(p):
 
 
 def _check(p, o, lse, mask, max_len, scale=None):
-    """A weight is rounded by at most a half step u of the 16-bit type (8 or 11 bits) and, below 2^-14
-    of its 128 keys' largest, by 2^-22 of that (2^-26 for fp16), which over 128 keys of values up to 448
-    scales is 2^-15 (2^-19) of 448 times the largest scale.  The products and sums are fp32: 2^-16 of
+    """A weight is rounded to fp16 (2^-11 of it) and then, for bf16, to two e4m3 parts: what the first
+    leaves is at most 2^-4 of the weight, what the second leaves 2^-4 of that, 2^-8 in all (three parts
+    hold fp16's 11 bits).  Below 2^-14 of the largest of the 256 keys of a step a part's rounding is a
+    fixed 2^-22 of that largest (2^-26 with three parts), which over 256 keys of values up to 448 scales
+    is 2^-14 (2^-18) of 448 times the largest scale.  The products and sums are fp32: 2^-16 of
     sum p |v| over the lengths here.  O is rounded once.  Scores: a dot of at most 256 exact products
     summed in fp32, 2^-18 of the sum of their sizes, and the exponent's and the logarithm's few steps."""
     d = p["q"].shape[-1]
@@ -81,8 +83,9 @@ def _check(p, o, lse, mask, max_len, scale=None):
     tol = 2.0 ** -18 * reach + 2.0 ** -20 * (1 + np.abs(np.where(none, 0, want_lse)))
     assert np.all(np.abs(np.where(none, 0, lse) - np.where(none, 0, want_lse)) <= tol)
     vmax = 448.0 * np.nanmax(np.where(np.isfinite(p["vs"]), np.abs(p["vs"]), 0))
-    bound = (u + 2.0 ** -16 + 2 * tol[..., None]) * spread + u * np.abs(want) + \
-        (2.0 ** -15 if p["dtype"] == inputs.BF16 else 2.0 ** -19) * vmax + 2.0 ** -24
+    weight = 2.0 ** -11 + (2.0 ** -8 if p["dtype"] == inputs.BF16 else 0.0)
+    bound = (weight + 2.0 ** -16 + 2 * tol[..., None]) * spread + u * np.abs(want) + \
+        (2.0 ** -14 if p["dtype"] == inputs.BF16 else 2.0 ** -18) * vmax + 2.0 ** -24
     err = np.abs(o - want)
     assert np.all(err <= bound), float((err / bound).max())
     return float((err / bound).max())
