@@ -1023,8 +1023,8 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
 // the boundary in front of CTA c = x + 1 of the attention; the first boundary
 // inside a unit merges it: the partial of CTA c - 1 (slot 2c - 1), then those of
 // c, c + 1, ... (slots 2c, 2c + 2, ...) up to the unit's end, in that order.  A
-// warp per row (all rows at once: it is a chain of three loads); lane i holds
-// the weight of partial i of 32 at a time.
+// warp per row, all at once; lane i holds the weight of partial i of 32 at a
+// time.
 template <int RC>
 constexpr int kDecFp8MergeThreads = 32 * (RC < 4 ? 4 : RC);
 
@@ -1033,11 +1033,28 @@ __global__ void __launch_bounds__(kDecFp8MergeThreads<RC>)
     fa_decode_fp8_combine_kernel(const __grid_constant__ DecFp8Params p, int grid) {
     const int c = (int)blockIdx.x + 1, lane = (int)threadIdx.x & 31, r = (int)threadIdx.x >> 5;
     ptx::wait_for_previous_kernel();  // (launched while the attention still runs)
+    // One round of loads: the cut, the first 32 partials' lse and the first two
+    // partial rows, which every unit that is merged has.
     const long long total = *reinterpret_cast<const long long *>(p.cuts);
     const int *cut = p.cuts + 4 + 5 * c;
+    const int cb = cut[0], ckvh = cut[1], cchunk = cut[2], ctile = cut[3], cnt = cut[4];
+    auto slot_row = [&](int i) { return (size_t)(i == 0 ? 2 * c - 1 : 2 * (c + i - 1)) * RC + r; };
+    constexpr int PER = D / 32;
+    const bool held = r < RC;
+    float lse0 = held && c + lane - 1 < grid ? p.part_lse[slot_row(lane)] : -INFINITY;
+    float row0_v[PER], row1_v[PER];
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) {
+        float2 v0 = make_float2(0.f, 0.f), v1 = v0;
+        if (held) {
+            v0 = *reinterpret_cast<const float2 *>(p.part_o + slot_row(0) * D + lane * PER + e);
+            v1 = *reinterpret_cast<const float2 *>(p.part_o + slot_row(1) * D + lane * PER + e);
+        }
+        row0_v[e] = v0.x, row0_v[e + 1] = v0.y;
+        row1_v[e] = v1.x, row1_v[e + 1] = v1.y;
+    }
     const long long G = min((long long)grid, total);
     if (c >= G) return;
-    const int cb = cut[0], ckvh = cut[1], cchunk = cut[2], ctile = cut[3], cnt = cut[4];
     if (ctile == 0) return;  // between two units
     const long long begin = c * total / G - ctile, end = begin + cnt;
     if ((c - 1) * total / G > begin) return;  // an earlier boundary merges this unit
@@ -1049,13 +1066,11 @@ __global__ void __launch_bounds__(kDecFp8MergeThreads<RC>)
     int rows;
     const size_t row0 = dec_fp8_row0(p, cb, ckvh, cchunk, &rows);
     if (r >= rows) return;
-    auto slot_row = [&](int i) { return (size_t)(i == 0 ? 2 * c - 1 : 2 * (c + i - 1)) * RC + r; };
-    constexpr int PER = D / 32;
     float acc[PER], sum = 0.f, top = -INFINITY;
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
     for (int i0 = 0; i0 < n; i0 += 32) {
-        const float mine = i0 + lane < n ? p.part_lse[slot_row(i0 + lane)] : -INFINITY;
+        const float mine = i0 + lane >= n ? -INFINITY : i0 == 0 ? lse0 : p.part_lse[slot_row(i0 + lane)];
         const bool nan = __any_sync(0xffffffffu, isnan(mine));
         const float high = nan ? NAN : fmaxf(top, warp_max(mine));
         const float use = high == -INFINITY ? 0.f : high;
@@ -1064,8 +1079,16 @@ __global__ void __launch_bounds__(kDecFp8MergeThreads<RC>)
         sum *= rescale;
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] *= rescale;
+        int i = 0;
+        if (i0 == 0) {
+            const float w0 = __shfl_sync(0xffffffffu, weight, 0), w1 = __shfl_sync(0xffffffffu, weight, 1);
+            sum = w0 + w1;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w1, row1_v[e], w0 * row0_v[e]);
+            i = 2;
+        }
 #pragma unroll 4
-        for (int i = 0; i < min(32, n - i0); ++i) {
+        for (; i < min(32, n - i0); ++i) {
             const float w = __shfl_sync(0xffffffffu, weight, i);
             const float *src = p.part_o + slot_row(i0 + i) * D + lane * PER;
             sum += w;
