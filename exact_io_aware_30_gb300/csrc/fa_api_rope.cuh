@@ -86,8 +86,13 @@ bool same_view(const StridedView &a, const StridedView &b) {
 
 template <typename T, int V>
 fa_status launch_rope(const RopeParams &p, int layout, dim3 grid, cudaStream_t stream) {
-    return launch_overlapped(layout == FA_ROPE_INTERLEAVED ? fa_rope_kernel<T, V, true> : fa_rope_kernel<T, V, false>,
-                             grid, 256, 0, 1, stream, p);
+    // Two heads in flight; one for interleaved pairs of part of the head (bf16,
+    // half of d 128, 134 MB: one 29 us, two 31, four 47; all of it, fp16, 268 MB:
+    // one 55 us, two 48, four 47; half layout: one 54 us, two 48, four 49).
+    auto kern = layout != FA_ROPE_INTERLEAVED ? fa_rope_kernel<T, V, false, 2>
+                : p.rot < p.d                 ? fa_rope_kernel<T, V, true, 1>
+                                              : fa_rope_kernel<T, V, true, 2>;
+    return launch_overlapped(kern, grid, 256, 0, 1, stream, p);
 }
 
 fa_status rope_impl(const void *q, const long long *q_strides, void *q_out, const long long *q_out_strides,

@@ -75,18 +75,35 @@ struct alignas(sizeof(T) * V) RopeVec {
     T e[V];
 };
 
-// V elements per vector; each thread rotates V pairs (two vectors).
-template <typename T, int V, bool kInterleaved>
+// V elements per vector; each thread rotates V pairs (two vectors).  U heads are
+// in flight at once: four CTAs of 64 registers a thread hide the memory's
+// latency, and more heads per thread spill.
+template <typename T, int V, bool kInterleaved, int U>
 __global__ void __launch_bounds__(256, 4) fa_rope_kernel(const __grid_constant__ RopeParams p) {
     using Vec = RopeVec<T, V>;
     using C = RopeType<T>;
     ptx::wait_for_previous_kernel();
     const long long unit = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (unit >= p.units) return;
-    const long long token = unit / p.slots;
-    const int slot = (int)(unit - token * p.slots);
-    const int b = (int)(token / p.S), s = (int)(token - (long long)b * p.S);
     const int half = p.rot >> 1, turning = half / V, passing = (p.d - p.rot) / V;
+    long long token;
+    int slot;
+    if (passing == 0) {
+        token = unit / p.slots;
+        slot = (int)(unit - token * p.slots);
+    } else {
+        // 32 tokens at a time, their turning slots first: a warp turns or copies,
+        // and no lane waits for its neighbours' sines (31 -> 29 us for half of d 128)
+        const long long group = unit / (32 * p.slots);
+        const int in_group = (int)min(32LL, p.units / p.slots - group * 32);
+        int at = (int)(unit - group * (32 * p.slots));
+        const bool copies = at >= in_group * turning;
+        if (copies) at -= in_group * turning;
+        const int per = copies ? p.slots - turning : turning, in = at / per;
+        slot = at - in * per + (copies ? turning : 0);
+        token = group * 32 + in;
+    }
+    const int b = (int)(token / p.S), s = (int)(token - (long long)b * p.S);
     const int h0 = (int)blockIdx.y * p.heads_per_chunk;
     const int h1 = min(h0 + p.heads_per_chunk, p.heads);
 
@@ -99,11 +116,6 @@ __global__ void __launch_bounds__(256, 4) fa_rope_kernel(const __grid_constant__
     const bool two = turns || pass0 + pass_step < passing;
     const int e0 = !turns ? p.rot + pass0 * V : (kInterleaved && V == 1) ? 2 * slot : slot * V;
     const int e1 = !turns ? (two ? e0 + pass_step * V : e0) : (kInterleaved && V == 1) ? e0 + 1 : e0 + half;
-    // Heads in flight.  Four CTAs of 64 registers a thread hide the memory's
-    // latency; more heads per thread only spill (interleaved, half of d 128
-    // turning, bf16, 134 MB: one 31 us, two 37, four 57; half layout, fp16, 268 MB:
-    // one 54 us, two 48, four 48).
-    constexpr int U = kInterleaved && V > 1 ? 1 : 2;
     Vec x0[U], x1[U];
     auto load = [&](int h) {
 #pragma unroll
