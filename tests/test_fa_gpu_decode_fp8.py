@@ -332,6 +332,65 @@ def test_more_requests_than_threads_with_uneven_lengths(B):
     _check(p, o, lse, "none", 3000)
 
 
+def test_a_bound_far_above_the_lengths_and_a_wide_table():
+    # the grid is sized by the bound; most of its CTAs find no tile
+    p = _problem(3, 8, 2, 2, 128, 16, [5, 300, 0], inputs.BF16, seed=53)
+    wide = np.full((3, 9000), -1, np.int32)
+    wide[:, :p["table"].shape[1]] = p["table"]
+    p["table"] = wide
+    narrow = fa.decode_paged_fp8(*_device(p), 300, mask="causal")
+    o, lse = fa.decode_paged_fp8(*_device(p), 9000 * 16, mask="causal")
+    _check(p, o, lse, "causal", 9000 * 16)
+    _check(p, *narrow, "causal", 300)
+
+
+def test_two_host_threads_at_once():
+    import threading
+    ps = [_problem(3, 8, 2, 1, d, 16, [700, 33, 1200], inputs.FP16, seed=54 + d) for d in (64, 128)]
+    devs = [_device(p) for p in ps]
+    want = [fa.decode_paged_fp8(*d, 1200) for d in devs]
+    torch.cuda.synchronize()
+    got, failed = [None, None], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(30):
+                got[i] = fa.decode_paged_fp8(*devs[i], 1200, stream=stream)
+            stream.synchronize()
+        except Exception as e:  # (an assertion in a thread would be lost)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_the_results_of_the_kernel_in_front_are_seen():
+    # the kernels begin before the one in front of them ends: each must still wait for its results
+    p = _problem(2, 8, 2, 1, 128, 16, [3000, 1500], inputs.BF16, seed=55)
+    dev = _device(p)
+    want = fa.decode_paged_fp8(*dev, 3000)
+    plan, x = fa.rope_plan(128), torch.randn(1, 64, 8192, 128, device="cuda").bfloat16()
+    big, q, lens = torch.empty_like(x), torch.zeros_like(dev[0]), torch.zeros_like(dev[6])
+    for _ in range(5):
+        q.zero_()
+        lens.zero_()
+        torch.cuda.synchronize()
+        fa.rope(x, None, plan, out_q=big)  # long enough for the next launches to queue behind it
+        fa.rope(dev[0], None, fa.RopePlan(2, plan.freq, 1.0), offset=0, out_q=q)  # position 0: a copy
+        fa.paged_update(lens, dev[6], dev[5].clone(), torch.zeros(400, dtype=torch.int32, device="cuda"),
+                        torch.tensor([0, 400], dtype=torch.int32, device="cuda"), 16, max_tokens=4500, seq_lens_out=lens)
+        got = fa.decode_paged_fp8(q, *dev[1:6], lens, 3000)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ------------------------------------------------------------------ the step as it is used
 
 @pytest.mark.parametrize("dtype,H,Hkv,d,bs", [(torch.bfloat16, 8, 2, 128, 16), (torch.float16, 4, 4, 64, 32),
