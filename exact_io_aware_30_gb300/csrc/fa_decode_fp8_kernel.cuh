@@ -451,13 +451,11 @@ template <int G>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[G]) {
     if constexpr (G == 1) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
-    } else if constexpr (G == 2) {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
     } else if constexpr (G == 4) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
     } else {
-        static_assert(G == 8, "1, 2, 4 or 8 columns");
+        static_assert(G == 8, "1, 4 or 8 columns");
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                      : "r"(taddr));
@@ -819,7 +817,8 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
 #pragma unroll
             for (int j = 0; j < KPT; ++j) share[j] = vtop > 0.f ? vs[j] / vtop * 256.f : 0.f;
             const uint32_t buf = p_addr + b * KPT * C::P_BYTES;
-            constexpr int S = RW < 4 ? RW : 4;  // rows at a time
+            constexpr int S = RW < 4 ? 1 : 4;  // rows at a time
+            static_assert(RW == 1 || RW % 4 == 0, "one row, or whole fours");
 #pragma unroll
             for (int g = 0; g < RW; g += S) {
                 float m[S], c[S], a[S], e[S], v[KPT][(S + 1) / 2 * 2];

@@ -10,6 +10,7 @@
 
 #include <type_traits>
 
+#include "fa.h"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -109,7 +110,11 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
         const long long before = paged_scan<W>(need << 32 | gone, warp_sums, &both);
         const long long start = needed + (before >> 32), freed_before = freed + (before & 0xffffffffLL);
         const bool short_of = need > 0 && start + need > count;
-        const int status = add == 0 ? 0 : too_long ? 2 : no_rows ? 3 : short_of ? 1 : 0;
+        const int status = add == 0   ? FA_PAGED_OK
+                           : too_long ? FA_PAGED_TOO_LONG
+                           : no_rows  ? FA_PAGED_NO_ROWS
+                           : short_of ? FA_PAGED_NO_BLOCKS
+                                      : FA_PAGED_OK;
         const int given = __reduce_add_sync(0xffffffffu, (int)(short_of ? 0 : need));
         if ((tid & 31) == 0 && given) atomicAdd(&s_used, (unsigned long long)given);
 
@@ -117,7 +122,7 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
         s_old[tid] = (int)old;
         s_start[tid] = (int)min(start, 0x7fffffffLL);
         s_gone[tid] = (int)gone;
-        s_ok[tid] = status == 0;
+        s_ok[tid] = status == FA_PAGED_OK;
         __syncthreads();
 
         // rows of this chunk's tokens
@@ -196,7 +201,7 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
         freed += both & 0xffffffffLL;
         if (p.meet) cluster_meet();
         if (rank == 0 && real) {
-            p.seq_lens_out[b] = (int)(status == 0 ? (delta < 0 ? left : old + add) : old);
+            p.seq_lens_out[b] = (int)(status == FA_PAGED_OK ? (delta < 0 ? left : old + add) : old);
             p.status[b] = status;
         }
         __syncthreads();
