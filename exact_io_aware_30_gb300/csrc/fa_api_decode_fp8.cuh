@@ -33,9 +33,16 @@ fa_status check_dec_fp8_sizes(int B, int H, int Hkv, int Sq, int d, int block_si
 // (32 rows at d 256: 360 us in one chunk, 334 in two; at d 128 164 against 211).
 constexpr int dec_fp8_max_rows(int d) { return d == 256 ? 24 : 32; }
 
+// Tiles per unit up to which units are not cut: a CTA then takes whole ones, and
+// the merge with its launch and its workspace is left out.  Whole against cut, us:
+// 400 tokens, 1 request x 8 heads 8.0 / 8.0, 64 x 8 15.5 / 18.1, 16 x 4 of 40 rows
+// at d 256 12.9 / 19.8; 1,000 tokens, 1 x 8 11.9 / 8.6, 64 x 8 25.9 / 27.6, but
+// with lengths that differ the longest share would set the time.
+constexpr int kDecFp8WholeTiles = 4;
+
 struct DecFp8Plan {
     int rc = 0, chunks = 1, rows_per_chunk = 0, grid = 0;
-    bool cuts = false;  // a unit can lie across CTAs
+    bool cuts = false;  // units may lie across CTAs
     size_t part_lse_off = 0, part_o_off = 0, bytes = 0;
 };
 
@@ -61,11 +68,12 @@ DecFp8Plan plan_decode_fp8(int B, int Hkv, int R, int d, bool fp16, int max_seq_
                        : d == 128 ? (fp16 ? dec_fp8_ctas_per_sm<128, true>(pl.rc) : dec_fp8_ctas_per_sm<128, false>(pl.rc))
                                   : 1;
     const long long tiles = (max_seq_len + 127LL) / 128;
-    const long long most = (long long)B * Hkv * pl.chunks * tiles;
-    pl.grid = (int)std::min(most, (long long)num_sms * per_sm);
-    pl.cuts = pl.grid > 1 && tiles > 1;
-    size_t at = (size_t)(4 + 5 * pl.grid) * 4;
+    const long long units = (long long)B * Hkv * pl.chunks;
+    pl.cuts = tiles > kDecFp8WholeTiles;
+    pl.grid = (int)std::min(pl.cuts ? units * tiles : units, (long long)num_sms * per_sm);
+    size_t at = 0;
     if (pl.cuts) {
+        at = (size_t)(4 + 5 * pl.grid) * 4;
         pl.part_lse_off = (at + 255) / 256 * 256;
         pl.part_o_off = (pl.part_lse_off + (size_t)2 * pl.grid * pl.rc * 4 + 255) / 256 * 256;
         at = pl.part_o_off + (size_t)2 * pl.grid * pl.rc * d * 4;
@@ -82,7 +90,7 @@ fa_status launch_decode_fp8_rc(const DecFp8Params &p, const DecFp8Plan &pl, Devi
     if (set_smem(fa_decode_fp8_kernel<C>, C::SMEM_BYTES, info.attr_dec_fp8[slot]) != FA_OK) return FA_ERR_CUDA;
     const fa_status st = launch_overlapped(fa_decode_fp8_kernel<C>, dim3((unsigned)pl.grid), C::NUM_THREADS,
                                            C::SMEM_BYTES, 1, stream, p);
-    if (st != FA_OK || !pl.cuts) return st;
+    if (st != FA_OK || !pl.cuts || pl.grid < 2) return st;
     return launch_overlapped(fa_decode_fp8_combine_kernel<D, kFP16, RC>, dim3((unsigned)(pl.grid - 1)),
                              kDecFp8MergeThreads<RC>, 0, 1, stream, p, pl.grid);
 }
@@ -125,7 +133,7 @@ fa_status decode_fp8_impl(const void *q, const void *k_cache, const void *v_cach
     const bool fp16 = dtype == FA_DTYPE_FP16;
     const DecFp8Plan pl = plan_decode_fp8(B, Hkv, H / Hkv * Sq, d, fp16, max_seq_len, info->num_sms);
     const size_t need = pl.bytes;
-    if (!workspace || workspace_bytes < need) return FA_ERR_INVALID_ARG;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
     const size_t rows = (size_t)B * H * Sq, qo = rows * d * 2;
     const size_t cache = (size_t)num_blocks * Hkv * block_size * d, scales = (size_t)num_blocks * Hkv * 4;
     const Extent ins[7] = {{q, qo}, {k_cache, cache}, {v_cache, cache}, {k_scale, scales}, {v_scale, scales},
@@ -147,9 +155,12 @@ fa_status decode_fp8_impl(const void *q, const void *k_cache, const void *v_cach
     p.seq_lens = seq_lens;
     p.o = o;
     p.lse = lse;
-    p.cuts = reinterpret_cast<int *>(ws);
-    p.part_lse = reinterpret_cast<float *>(ws + pl.part_lse_off);
-    p.part_o = reinterpret_cast<float *>(ws + pl.part_o_off);
+    p.whole = pl.cuts ? 0 : 1;
+    if (pl.cuts) {
+        p.cuts = reinterpret_cast<int *>(ws);
+        p.part_lse = reinterpret_cast<float *>(ws + pl.part_lse_off);
+        p.part_o = reinterpret_cast<float *>(ws + pl.part_o_off);
+    }
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;

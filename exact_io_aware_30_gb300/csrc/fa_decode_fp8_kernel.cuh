@@ -34,7 +34,8 @@
 // CTA has the same work whatever the lengths, and its pipelines run on from
 // unit to unit.  A unit that lies in one CTA is written out by it; one that is
 // cut leaves a normalised partial row and its lse per CTA, and
-// fa_decode_fp8_combine_kernel (a CTA per cut) merges them in order.
+// fa_decode_fp8_combine_kernel (a CTA per cut) merges them in order.  Where units
+// are short, a CTA takes whole ones instead, and there is nothing to merge.
 //
 // One CTA:
 //   softmax warpgroups, one per eight rows of the unit.  Thread = key for S^T
@@ -67,6 +68,7 @@ struct DecFp8Params {
     float *lse;
     float *part_o;           // [2 G, RC, d]: slot 2c: CTA c's unit begun by others; 2c + 1: one it begins and others end
     float *part_lse;         // [2 G, RC], log2 units
+    int whole;               // units are not cut: a CTA takes whole ones, and part_o, part_lse and cuts are unused
     int *cuts;               // [4 + 5 G]: total tiles (64-bit), then per CTA its first unit: b, head, chunk, tile, tiles
     int B, H, Hkv, Sq, R;    // R = H / Hkv * Sq rows per K/V head
     int chunks;              // of at most RC rows each
@@ -230,6 +232,22 @@ __device__ DecFp8It dec_fp8_begin(const DecFp8Params &p, long long *scratch) {
     const long long hc = (long long)p.Hkv * p.chunks, c = blockIdx.x;
     DecFp8It it;
     it.b = it.kvh = it.chunk = it.tile = it.L = it.nt = it.next_len = it.left = 0;
+    if (p.whole) {  // an even share of the units (there are at least as many as CTAs)
+        const long long units = p.B * hc, u0 = c * units / gridDim.x, u1 = (c + 1) * units / gridDim.x;
+        const int b0 = (int)(u0 / hc), b1 = (int)((u1 - 1) / hc);
+        int sum = 0;
+        for (int b = b0 + lane; b <= b1; b += 32)
+            sum += (int)(min(u1, (b + 1) * hc) - max(u0, b * hc)) * dec_fp8_tiles(dec_fp8_len(p, b));
+        it.left = __reduce_add_sync(0xffffffffu, sum);
+        it.b = b0;
+        it.L = dec_fp8_len(p, b0);
+        it.nt = dec_fp8_tiles(it.L);
+        it.next_len = dec_fp8_len(p, b0 + 1);
+        const int unit = (int)(u0 - b0 * hc);
+        it.kvh = unit / p.chunks;
+        it.chunk = unit - it.kvh * p.chunks;
+        return it;
+    }
     long long total = -1, G = 0, lo = 0, hi = 0;
     if (p.B > THREADS) {  // the sum first; then the requests are gone through again
         int sum = 0;

@@ -863,7 +863,8 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     try:
         if workspace is None:
             ws_bytes = _decode_fp8_workspace(dev.index, B, H, Hkv, Sq, d, bs, mb, nb, max_seq_len, mk, dt)
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+            if ws_bytes:
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         else:
             _need_tensor("workspace", workspace, dev, torch.uint8, workspace.shape)
             ws_bytes = workspace.numel()
@@ -878,7 +879,8 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
         st = (_lib or load()).fa_decode_paged_fp8(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            workspace.data_ptr(), ws_bytes, B, H, Hkv, Sq, d, bs, mb, nb, max_seq_len, scale, mk, dt, sp)
+            workspace.data_ptr() if ws_bytes else None, ws_bytes, B, H, Hkv, Sq, d, bs, mb, nb,
+            max_seq_len, scale, mk, dt, sp)
     finally:
         _leave(scope)
     if st:

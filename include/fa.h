@@ -440,7 +440,7 @@ fa_status fa_cache_append_fp8(const void *k, const void *v, long long k_token_st
  *                gets O = 0 and lse = -inf
  *   block_table  an entry outside [0, num_blocks) reads zeros
  *   workspace    at least fa_decode_fp8_workspace_query() bytes, 256-byte
- *                aligned; calls that may overlap in time (other streams, graphs
+ *                aligned (may be NULL where that is 0); calls that may overlap in time (other streams, graphs
  *                replayed beside each other) need one each
  *   max_seq_len  at most 2^31 - 513
  * Cache slots past a request's length may hold any codes, NaN included.
