@@ -391,6 +391,46 @@ def test_the_results_of_the_kernel_in_front_are_seen():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("n", [300, 3000])
+def test_a_graph_with_copies_and_a_fork_in_front(n):
+    # copy nodes before the kernels, and a join of two streams before the attention
+    p = _problem(2, 8, 2, 1, 128, 16, [n, n // 2], inputs.BF16, seed=56)
+    dev = _device(p)
+    q, k_new = dev[0].clone(), torch.randn(2, 2, 128, device="cuda").bfloat16()
+    slots = torch.tensor([int(dev[5][b, (int(l) - 1) // 16]) * 16 + (int(l) - 1) % 16 for b, l in enumerate(p["lens"])],
+                         dtype=torch.int32, device="cuda")
+    plan = fa.rope_plan(128)
+    fresh = [t.clone() for t in dev[1:5]]
+
+    def step(caches, qin, kin, side):
+        qq, kk = torch.empty_like(qin), torch.empty_like(kin)
+        qq.copy_(qin)
+        q2 = fa.rope(qq, None, plan, offset=7)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            kk.copy_(kin)
+            fa.cache_append_fp8(kk, kk, slots, *caches)
+        q3 = fa.rope(q2, None, plan, offset=-7)
+        main.wait_stream(side)
+        return fa.decode_paged_fp8(q3, *caches, dev[5], dev[6], n) + (q3,)
+
+    side = torch.cuda.Stream()
+    want = step([t.clone() for t in fresh], q, k_new, side)
+    torch.cuda.synchronize()
+    caches = [t.clone() for t in fresh]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(caches, q, k_new, side)
+    for t, f in zip(caches, fresh):
+        t.copy_(f)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ the step as it is used
 
 @pytest.mark.parametrize("dtype,H,Hkv,d,bs", [(torch.bfloat16, 8, 2, 128, 16), (torch.float16, 4, 4, 64, 32),
