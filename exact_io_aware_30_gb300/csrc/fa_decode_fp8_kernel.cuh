@@ -17,16 +17,22 @@
 //     and N = the rows again, so no part of the tensor core's work is padding
 //     for the rows that are missing, and it stays far from being the limit;
 //   * a 16-bit q and the fp32 weights are split into NP e4m3 parts with
-//     x = x1 + x2 / 16 (+ x3 / 256), each part the rounding of what the parts
-//     before it left, and the parts are columns of N beside each other; their
-//     products are summed in fp32 as they are read back.  Two parts hold the 8
-//     significant bits of bf16, three the 11 of fp16, so S is exact up to
-//     fp32 sums (a component below 2^-14 of its row's largest keeps 2^-22 of
-//     that), and a weight is rounded much as a 16-bit P would be: to fp16, 2^-11
-//     of itself, and with two parts by 2^-8 more.  Weights are taken relative to
-//     the largest score of their own step of 128 or 256 keys and the steps'
-//     outputs are rescaled in fp32, so that what is below the parts' range
-//     (2^-22 of the step's largest) is never a large share of a row.
+//     x = x1 + x2 / 16 (+ x3 / 256 + x4 / 4096), each part the rounding of what
+//     the parts before it left, and the parts are columns of N beside each
+//     other; their products are summed in fp32 as they are read back.  Two
+//     parts hold the 8 significant bits of bf16, three the 11 of fp16, so S is
+//     exact up to fp32 sums (but for components far below their row's largest:
+//     see dec_fp8_put_q), and a weight is rounded much as a 16-bit P would be: to
+//     fp16, 2^-11 of itself, and with two parts by 2^-8 more.  Up to four rows a
+//     fourth part fits into the 16 columns that N has at least: q keeps all
+//     bits there and a weight 16 (2^-16 of itself), since a few rows'
+//     weights are not rounded to 16 bits over the 16-bit cache either (4 rows, 537
+//     MB: 96 us with two parts, 97 with four; with more rows the columns and stores
+//     cost more: 8 rows at d 128 92 / 96 us, at d 64 64 / 74, 16 rows 115 / 133).  Weights
+//     are taken relative to the largest score of their own step of 128 or 256
+//     keys and the steps' outputs are rescaled in fp32, so that what is below
+//     the parts' range (2^-22, 2^-26, 2^-30 of the step's largest with two, three,
+//     four parts) is never a large share of a row.
 //
 // Work split.  The work is a line of 128-key tiles: request by request, K/V
 // head by K/V head, chunk of rows by chunk of rows (a unit), tile by tile.
@@ -88,7 +94,7 @@ struct DecFp8Cfg {
     static constexpr int RW = RC < 8 ? RC : 8;          // rows of one softmax warpgroup
     static constexpr int NWG = RC / RW;                 // softmax warpgroups, each with all keys of a tile
     static_assert(RW * NWG == RC, "whole warpgroups of rows");
-    static constexpr int NP = kFP16 ? 3 : 2;            // e4m3 parts of q and of the weights
+    static constexpr int NP = RC <= 4 ? 4 : kFP16 ? 3 : 2;  // e4m3 parts of q and of the weights
     static constexpr int N = (RC * NP + 15) / 16 * 16;  // columns: part-major, then rows
     static constexpr int BN = 128;                      // keys per tile
     static constexpr int ROWB = D < 128 ? D : 128;      // bytes of a row in one column chunk
@@ -502,15 +508,28 @@ __device__ __forceinline__ void dec_fp8_read(uint32_t col, float (&x)[G]) {
 // Two values (at most 256) as NP parts: codes[j] holds part j of a in byte 0,
 // of b in byte 1.  They are rounded to fp16 first, whose 11 bits three parts
 // hold, and every later step is exact in fp16: what a part leaves is at most
-// half a step of it, 2^-4 of the value before.
+// half a step of it, 2^-4 of the value before.  A fourth part holds what those
+// three and the rounding to fp16 left.
 template <int NP>
 __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t (&codes)[NP]) {
     const __half2 k16 = __half2half2(__ushort_as_half(0x4C00));  // 16
     const uint32_t w = ptx::pack_f16x2(a, b);
     __half2 h = *reinterpret_cast<const __half2 *>(&w);
+    float2 lost = make_float2(0.f, 0.f);
+    if constexpr (NP == 4) {
+        const float2 r = __half22float2(h);
+        lost = make_float2(a - r.x, b - r.y);  // (exact)
+    }
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
         uint16_t two;
+        if (j == 3) {
+            const float2 r = __half22float2(h);
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+                : "=h"(two) : "f"(fmaf(lost.y, 4096.f, r.y)), "f"(fmaf(lost.x, 4096.f, r.x)));
+            codes[j] = two;
+            break;
+        }
         asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(*reinterpret_cast<const uint32_t *>(&h)));
         codes[j] = two;
         if (j + 1 < NP) {
@@ -591,7 +610,10 @@ __device__ __forceinline__ void dec_fp8_load_q(const DecFp8Params &p, const DecF
 
 // q's parts into shared memory (K-major, swizzled), its rows' score multipliers
 // and last keys.  A row is scaled by a power of two so that its largest
-// component is in [128, 256); a row with an infinity or NaN becomes NaN codes.
+// component is in [128, 256).  Components of at least 2^-13 (two parts, bf16) or
+// 2^-14 (three, fp16) of the largest are exact; smaller ones are off by half the last
+// part's smallest step, at most 2^-21 (two parts), 2^-25 (three) or 2^-29 (four)
+// of the largest.  A row with an infinity or NaN becomes NaN codes.
 template <class C>
 __device__ __forceinline__ void dec_fp8_put_q(const DecFp8Params &p, const DecFp8It &u, const DecFp8Q<C> &q, uint8_t *sQ,
                                               float *mul, int *last) {

@@ -424,11 +424,12 @@ fa_status fa_cache_append_fp8(const void *k, const void *v, long long k_token_st
 /*
  * fa_decode_paged_fp8 -- fa_decode_paged over the 8-bit cache of
  * fa_cache_append_fp8: exact softmax attention over the dequantised tokens,
- * q and o in 16 bits.  q enters exactly (a component below 2^-14 of its row's
- * largest keeps 2^-22 of that), each weight is rounded to at least the 8 (bf16)
- * or 11 (fp16) bits of the type before P V, as in the 16-bit kernels, and sums
- * are fp32.  Deterministic.  Two launches at most; the workspace's contents on
- * entry do not matter.  Arguments as for fa_decode_paged, except:
+ * q and o in 16 bits.  q enters exactly, but for components below 2^-13 of
+ * their row's largest: those may be off by 2^-21 of that.  Each weight is
+ * rounded to 16 bits before P V with up to four rows per K/V head, else to 8
+ * (bf16) or 11 (fp16) bits, as where fa_decode_paged uses the tensor cores;
+ * sums are fp32.  Deterministic.  Two launches at most; the workspace's
+ * contents on entry do not matter.  Arguments as for fa_decode_paged, except:
  *
  *   k_cache, v_cache  [num_blocks, H_kv, block_size, d] e4m3
  *   k_scale, v_scale  [num_blocks, H_kv] fp32, finite (any such scales, powers
