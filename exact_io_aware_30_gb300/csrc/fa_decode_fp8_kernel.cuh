@@ -26,13 +26,17 @@
 //     fp16, 2^-11 of itself, and with two parts by 2^-8 more.  Up to four rows a
 //     fourth part fits into the 16 columns that N has at least: q keeps all
 //     bits there and a weight 16 (2^-16 of itself), since a few rows'
-//     weights are not rounded to 16 bits over the 16-bit cache either (4 rows, 537
-//     MB: 96 us with two parts, 97 with four; with more rows the columns and stores
+//     weights are not rounded to 16 bits over the 16-bit cache either (4 rows, 606
+//     MB: 97.8 us with two parts, 98.2 with four; with more rows the columns and stores
 //     cost more: 8 rows at d 128 92 / 96 us, at d 64 64 / 74, 16 rows 115 / 133).  Weights
 //     are taken relative to the largest score of their own step of 128 or 256
 //     keys and the steps' outputs are rescaled in fp32, so that what is below
 //     the parts' range (2^-22, 2^-26, 2^-30 of the step's largest with two, three,
-//     four parts) is never a large share of a row.
+//     four parts) is never a large share of a row.  What P V takes is a weight
+//     times its block's V scale, relative to the step's largest scale; in steps
+//     whose scales are far apart (V_RANGE) relative to the row's own largest
+//     product, which costs an exchange more (8 rows at d 128 88 -> 93 us, 32 rows 168
+//     -> 185 where every step is such a one).
 //
 // Work split.  The work is a line of 128-key tiles: request by request, K/V
 // head by K/V head, chunk of rows by chunk of rows (a unit), tile by tile.
@@ -114,6 +118,10 @@ struct DecFp8Cfg {
     static constexpr int MMA_WARP = 4 * NWG;
     static constexpr int TMA_WARP = 4 * NWG + 1;
     static constexpr int NUM_THREADS = 32 * (TMA_WARP + 1);
+    // How far the V scales of a step may be apart to be taken relative to the
+    // largest of them (else each row has a reference of its own): what is then
+    // lost is within 2^-20 of the row's largest weight times scale.
+    static constexpr float V_RANGE = NP == 2 ? 4.f : NP == 3 ? 64.f : 1024.f;
     // small arrays of a warpgroup, in floats, rows padded to a multiple of four
     static constexpr int RP = (RW + 3) / 4 * 4;
     static constexpr int F_M = 0;                    // [4 warps] the tile's maxima
@@ -123,8 +131,10 @@ struct DecFp8Cfg {
     static constexpr int F_C = F_V + 8 * RP;         // [2] score multipliers
     static constexpr int F_LAST = F_C + 2 * RP;      // [2] last key the row sees (int)
     static constexpr int F_L = F_LAST + 2 * RP;      // [4 warps] sums
-    static constexpr int F_RED = F_L + 4 * RP;       // [2][4 warps][RW + 1] tile maxima, largest |vs|
-    static constexpr int F_WG = (F_RED + 2 * 4 * (RW + 1) + 3) / 4 * 4;
+    static constexpr int F_N = F_L + 4 * RP;         // [4 warps] what a row's weights times V scales are multiplied by
+    static constexpr int F_TOP = F_L;                // [4 warps] largest weight times |vs|
+    static constexpr int F_RED = F_N + 4 * RP;       // [2][4 warps][RW + 2] tile maxima, largest |vs|, smallest but 0 negated
+    static constexpr int F_WG = (F_RED + 2 * 4 * (RW + 2) + 3) / 4 * 4;
     static constexpr int F_NUM = NWG * F_WG;
     static constexpr int slots(int kpt) {
         return (budget(kpt) - (1024 + 2 * Q_BYTES + 2 * kpt * P_BYTES + F_NUM * 4 + 512)) / TILE;
@@ -790,7 +800,7 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
         const int b = step & 1, k0 = it.tile * C::BN;
         bad = bad || !wait_warp(bar_addr(bars, p.stall_test && step == 0 ? C::B_NEVER : C::B_SFULL + b), (step >> 1) & 1, ctl, 78);
         float x[KPT][RW];  // scores without their row's multiplier
-        float *red = sF + C::F_RED + (b * 4 + warp) * (RW + 1);
+        float *red = sF + C::F_RED + (b * 4 + warp) * (RW + 2);
         if (!bad) {
             ptx::tc_fence_after();
 #pragma unroll
@@ -824,20 +834,27 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
                 const float top = warp_max(both);
                 if (lane == r) mine = top;
             }
-            float both = fabsf(vs[0]);
-            if constexpr (KPT == 2) both = fmaxf(both, fabsf(vs[KPT - 1]));
-            const float vtop = warp_max(both);
+            float high = 0.f, low = -INFINITY;  // (a scale of zero is near any other)
+#pragma unroll
+            for (int j = 0; j < KPT; ++j) {
+                high = fmaxf(high, fabsf(vs[j]));
+                low = fmaxf(low, vs[j] != 0.f ? -fabsf(vs[j]) : -INFINITY);
+            }
+            const float vtop = warp_max(high), vlow = warp_max(low);
             if (lane < RW) red[lane] = mine;
-            if (lane == 0) red[RW] = vtop;
+            if (lane == 0) red[RW] = vtop, red[RW + 1] = vlow;
         }
         // (a warp whose wait ran out still comes here, and the warpgroup leaves together)
         if (ptx::named_bar_any(1 + wg, 128, bad)) return;
-        const float *all = sF + C::F_RED + b * 4 * (RW + 1);
-        const float vtop = fmaxf(fmaxf(all[RW], all[2 * RW + 1]), fmaxf(all[3 * RW + 2], all[4 * RW + 3]));
+        const float *all = sF + C::F_RED + b * 4 * (RW + 2), *all1 = all + (RW + 2), *all2 = all1 + (RW + 2), *all3 = all2 + (RW + 2);
+        const float vtop = fmaxf(fmaxf(all[RW], all1[RW]), fmaxf(all2[RW], all3[RW]));
+        const float vlow = -fmaxf(fmaxf(all[RW + 1], all1[RW + 1]), fmaxf(all2[RW + 1], all3[RW + 1]));
+        const bool apart = vtop > C::V_RANGE * vlow;  // (the same in the whole warpgroup)
         float *sM = sF + C::F_M + warp * RP, *sB = sF + C::F_B + warp * RP;
         float *sA = sF + C::F_A + (b * 4 + warp) * RP, *sW = sF + C::F_V + (b * 4 + warp) * RP;
+        float *sN = sF + C::F_N + warp * RP;
         if (lane < RW) {
-            const float top = fmaxf(fmaxf(all[lane], all[RW + 1 + lane]), fmaxf(all[2 * RW + 2 + lane], all[3 * RW + 3 + lane]));
+            const float top = fmaxf(fmaxf(all[lane], all1[lane]), fmaxf(all2[lane], all3[lane]));
             const float m_tile = top * mul[lane];
             const bool none = m_tile == -INFINITY;  // the row sees no key of the tile
             const float m_new = fmaxf(m_run, m_tile), m_use = m_new == -INFINITY ? 0.f : m_new;
@@ -845,27 +862,59 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
             sM[lane] = none ? 0.f : m_tile;
             sB[lane] = beta;
             sA[lane] = ptx::ex2_approx(m_run - m_use);
+            sN[lane] = 1.f;
             sW[lane] = beta * (vtop * 0.00390625f);  // O holds 256 times its weights over vtop
             m_run = m_new;
         }
         __syncwarp();
-        // weights: of the sum in fp32, of V (times the block's scale over the
-        // step's largest, times 256) as parts.  P V of two steps before is done
-        // (its O has been read), so its buffer is free.
+        if (apart) {
+            // A block of a much larger scale, in keys that carry little of the row
+            // (or none, where the row does not see them), must not push the others
+            // below the parts' range: the reference is the row's own largest weight
+            // times scale, brought into [128, 256) by a power of two.  One exchange
+            // more, in the steps that need it.  (The sums' array is free here: it is read
+            // out before the next step's barrier, and written behind the wait for this
+            // step's O, which every warp's weights come before.)
+            float *sT = sF + C::F_TOP;
+            float mine = 0.f;
+#pragma unroll
+            for (int r = 0; r < RW; ++r) {
+                float most = 0.f;
+#pragma unroll
+                for (int j = 0; j < KPT; ++j) most = fmaxf(most, ptx::ex2_approx(fmaf(x[j][r], mul[r], -sM[r])) * fabsf(vs[j]));
+                most = warp_max(most);
+                if (lane == r) mine = most;
+            }
+            if (lane < RW) sT[warp * RP + lane] = mine;
+            ptx::named_bar_sync(1 + wg, 128);
+            if (lane < RW) {
+                const float most = fmaxf(fmaxf(sT[lane], sT[RP + lane]), fmaxf(sT[2 * RP + lane], sT[3 * RP + lane]));
+                // biased exponent, kept where the factor and its inverse are normal numbers
+                const uint32_t ex = min(max(__float_as_uint(most) >> 23, 8u), 253u);
+                sN[lane] = __uint_as_float((261u - ex) << 23);
+                sW[lane] = sB[lane] * __uint_as_float((ex - 7u) << 23);
+            }
+            __syncwarp();
+        }
+        // weights: of the sum in fp32, of V (times the block's scale, relative to
+        // the step's largest times 1 / 256 or to the row's own reference) as
+        // parts.  P V of two steps before is done (its O has been read), so its
+        // buffer is free.
         {
             float share[KPT];
 #pragma unroll
-            for (int j = 0; j < KPT; ++j) share[j] = vtop > 0.f ? vs[j] / vtop * 256.f : 0.f;
+            for (int j = 0; j < KPT; ++j) share[j] = apart ? vs[j] : vtop > 0.f ? vs[j] / vtop * 256.f : 0.f;
             const uint32_t buf = p_addr + b * KPT * C::P_BYTES;
             constexpr int S = RW < 4 ? 1 : 4;  // rows at a time
             static_assert(RW == 1 || RW % 4 == 0, "one row, or whole fours");
 #pragma unroll
             for (int g = 0; g < RW; g += S) {
-                float m[S], c[S], a[S], e[S], v[KPT][(S + 1) / 2 * 2];
+                float m[S], c[S], a[S], e[S], n[S], v[KPT][(S + 1) / 2 * 2];
                 lds_row<S>(sM + g, m);
                 lds_row<S>(mul + g, c);
                 lds_row<S>(sA + g, a);
                 lds_row<S>(sB + g, e);
+                lds_row<S>(sN + g, n);
 #pragma unroll
                 for (int r = 0; r < S; ++r) {
                     float sum = 0.f;
@@ -873,7 +922,7 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
                     for (int j = 0; j < KPT; ++j) {
                         const float w = ptx::ex2_approx(fmaf(x[j][g + r], c[r], -m[r]));
                         sum += w;
-                        v[j][r] = w * share[j];
+                        v[j][r] = w * share[j] * n[r];
                     }
                     l[g + r] = fmaf(l[g + r], a[r], sum * e[r]);
                 }
@@ -886,10 +935,10 @@ __device__ void dec_fp8_softmax_role(const DecFp8Params &p, DecFp8It it, uint8_t
                         split_e4m3<C::NP>(v[j][r], v[j][r + 1], codes);
 #pragma unroll
                         for (int i = 0; i < C::NP; ++i) {
-                            const int n = i * C::RC + g + r;  // (the warpgroup's first row is 0 modulo 8)
-                            st_shared_u8((buf ^ (uint32_t)((n & 7) << 4)) + j * C::P_BYTES + n * 128, codes[i]);
+                            const int at = i * C::RC + g + r;  // (the warpgroup's first row is 0 modulo 8)
+                            st_shared_u8((buf ^ (uint32_t)((at & 7) << 4)) + j * C::P_BYTES + at * 128, codes[i]);
                             if (r + 1 < S)
-                                st_shared_u8((buf ^ (uint32_t)(((n + 1) & 7) << 4)) + j * C::P_BYTES + (n + 1) * 128,
+                                st_shared_u8((buf ^ (uint32_t)(((at + 1) & 7) << 4)) + j * C::P_BYTES + (at + 1) * 128,
                                              codes[i] >> 8);
                         }
                     }

@@ -428,7 +428,9 @@ fa_status fa_cache_append_fp8(const void *k, const void *v, long long k_token_st
  * their row's largest: those may be off by 2^-21 of that.  Each weight is
  * rounded to 16 bits before P V with up to four rows per K/V head, else to 8
  * (bf16) or 11 (fp16) bits, as where fa_decode_paged uses the tensor cores;
- * sums are fp32.  Deterministic.  Two launches at most; the workspace's
+ * a weight times its V scale below 2^-20 of the row's largest such product
+ * among up to 256 neighbouring keys may be off by that 2^-20.  Sums are fp32.
+ * Deterministic.  Two launches at most; the workspace's
  * contents on entry do not matter.  Arguments as for fa_decode_paged, except:
  *
  *   k_cache, v_cache  [num_blocks, H_kv, block_size, d] e4m3
