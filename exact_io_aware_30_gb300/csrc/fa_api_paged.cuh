@@ -39,7 +39,7 @@ constexpr int kUpdateRowsPerCta = 2048;
 fa_status paged_update_impl(const int *seq_lens, const int *delta, int *block_table, int *free_ring,
                             const int *ring_state, int *seq_lens_out, int *ring_state_out, int *slot_map,
                             int *positions, int *status, int B, int max_blocks, int ring_size, int block_size,
-                            int max_tokens, cudaStream_t stream) {
+                            int max_tokens, int per_request, cudaStream_t stream) {
     const int bs_log2 = block_size_log2(block_size);
     if (bs_log2 < 0) return FA_ERR_UNSUPPORTED;
     if (B < 1 || max_blocks < 1 || ring_size < 1 || max_tokens < 0) return FA_ERR_INVALID_ARG;
@@ -81,6 +81,7 @@ fa_status paged_update_impl(const int *seq_lens, const int *delta, int *block_ta
     p.ring_size = ring_size;
     p.bs_log2 = bs_log2;
     p.max_tokens = max_tokens;
+    p.per_request = per_request;
     // In place, the CTAs have to meet: one cluster of a portable size.
     const bool in_place = seq_lens_out == seq_lens || ring_state_out == ring_state;
     const int most = in_place ? 8 : 32;
@@ -193,8 +194,18 @@ fa_status fa_paged_update(const int *seq_lens, const int *delta, int *block_tabl
                           int *positions, int *status, int B, int max_blocks, int ring_size, int block_size,
                           int max_tokens, fa_stream_t stream) {
     return fa::paged_update_impl(seq_lens, delta, block_table, free_ring, ring_state, seq_lens_out, ring_state_out,
-                                 slot_map, positions, status, B, max_blocks, ring_size, block_size, max_tokens,
+                                 slot_map, positions, status, B, max_blocks, ring_size, block_size, max_tokens, 0,
                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+fa_status fa_paged_update_by_request(const int *seq_lens, const int *delta, int *block_table, int *free_ring,
+                                     const int *ring_state, int *seq_lens_out, int *ring_state_out, int *slot_map,
+                                     int *positions, int *status, int B, int max_blocks, int ring_size,
+                                     int block_size, int rows_per_request, fa_stream_t stream) {
+    if (B < 1 || rows_per_request < 1 || (long long)B * rows_per_request > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+    return fa::paged_update_impl(seq_lens, delta, block_table, free_ring, ring_state, seq_lens_out, ring_state_out,
+                                 slot_map, positions, status, B, max_blocks, ring_size, block_size,
+                                 B * rows_per_request, rows_per_request, reinterpret_cast<cudaStream_t>(stream));
 }
 
 fa_status fa_cache_append_fp8(const void *k, const void *v, long long k_token_stride, long long k_head_stride,

@@ -26,7 +26,9 @@ namespace fa {
 // request's numbers: logical block n is table[b][n] for n < have, else ring
 // entry head + start + n - have.  One launch: every CTA scans all requests
 // (1,024 at a time) by itself and then takes its share of the token rows; a
-// binary search over the chunk's prefix sums finds a row's request.  The bytes
+// binary search over the chunk's prefix sums finds a row's request (where every
+// request has per_request rows of its own, a division does; its tokens are the
+// last of them, as the attention of a few new rows per request takes them).  The bytes
 // are few (8 per row, 16 per request); what it costs is the launch and the
 // latency of a scan, a search and a dependent load, which is why it is one
 // launch and no workspace.  Where an output is its input (lengths, ring state)
@@ -40,6 +42,7 @@ struct PagedUpdateParams {
     int *block_table, *free_ring;
     int *seq_lens_out, *ring_state_out, *slot_map, *positions, *status;
     int B, max_blocks, ring_size, bs_log2, max_tokens;
+    int per_request;         // rows of each request, or 0: the tokens' rows follow each other
     int meet;                // the grid is one cluster, and outputs may be inputs
 };
 
@@ -97,10 +100,19 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
         const long long old = real ? min(max((long long)p.seq_lens[b], 0LL), most) : 0;
         const long long delta = real ? p.delta[b] : 0;
         const long long add = max(delta, 0LL);
-        long long sum;
-        const long long first = tokens + paged_scan<W>(add, warp_sums, &sum);
+        const int n_req = min(kPagedThreads, p.B - c0);
+        long long sum, first;
+        bool no_rows;
+        if (p.per_request > 0) {
+            sum = (long long)n_req * p.per_request;
+            first = (b + 1LL) * p.per_request - add;
+            no_rows = add > p.per_request;
+        } else {
+            first = tokens + paged_scan<W>(add, warp_sums, &sum);
+            no_rows = first + add > p.max_tokens;
+        }
         const long long have = (old + bs - 1) >> p.bs_log2;
-        const bool too_long = old + add > most, no_rows = first + add > p.max_tokens;
+        const bool too_long = old + add > most;
         const long long need =
             add > 0 && !too_long && !no_rows ? ((old + add + bs - 1) >> p.bs_log2) - have : 0;
         const long long left = max(old + min(delta, 0LL), 0LL);  // a shrinking request's new length
@@ -126,7 +138,6 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
         __syncthreads();
 
         // rows of this chunk's tokens
-        const int n_req = min(kPagedThreads, p.B - c0);
         const int n_pow2 = n_req > 1 ? 1 << (31 - __clz(n_req - 1)) : 0;  // first stride of the search
         const int t0 = (int)min(tokens, (long long)p.max_tokens);
         const int t1 = (int)min(tokens + sum, (long long)p.max_tokens);
@@ -139,8 +150,13 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
                 int req[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) req[u] = 0;
+                if (p.per_request > 0) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        req[u] = (int)(min(base + u * kPagedThreads, t1 - 1LL) / p.per_request) - c0;
+                }
                 // the last request whose first row is <= t
-                for (int half = n_pow2; half > 0; half >>= 1) {
+                for (int half = p.per_request > 0 ? 0 : n_pow2; half > 0; half >>= 1) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const int mid = req[u] + half;
@@ -152,7 +168,7 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
                 for (int u = 0; u < U; ++u) {
                     const long long t = base + u * kPagedThreads;
                     const int q = req[u], old_q = s_old[q];
-                    pos[u] = t < t1 && s_ok[q] ? old_q + (int)(t - s_first[q]) : -1;
+                    pos[u] = t < t1 && s_ok[q] && t >= s_first[q] ? old_q + (int)(t - s_first[q]) : -1;
                     const int n = max(pos[u], 0) >> p.bs_log2, n_have = (old_q + bs - 1) >> p.bs_log2;
                     long long at = head + s_start[q] + n - n_have;  // below twice the ring's size
                     at -= at >= p.ring_size ? p.ring_size : 0;

@@ -53,7 +53,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_fp16", "fa_fwd_gqa", "fa_fwd_fp8", "fa_bwd", "fa_bw
            "fa_bwd_workspace_query", "fa_decode_paged", "fa_decode_workspace_query",
            "fa_workspace_query", "fa_status_string", "fa_describe", "fa_get_device_error",
            "fa_fwd_host", "fa_fwd_host_workspace_query", "fa_set_debug_stall_ms",
-           "fa_rope", "fa_rope_frequencies", "fa_paged_update", "fa_cache_append_fp8",
+           "fa_rope", "fa_rope_frequencies", "fa_paged_update", "fa_paged_update_by_request",
+           "fa_cache_append_fp8",
            "fa_decode_paged_fp8", "fa_decode_fp8_workspace_query")
 
 
@@ -132,8 +133,10 @@ def load(path: str | None = None):
         lib.fa_rope_frequencies.argtypes = [_i, ctypes.c_double, _i, ctypes.c_double,
                                             ctypes.c_double, ctypes.c_double, ctypes.c_double, _vp,
                                             ctypes.POINTER(ctypes.c_float)]
-        lib.fa_paged_update.restype = _i
-        lib.fa_paged_update.argtypes = [_vp] * 10 + [_i] * 5 + [_vp]
+        for name in ("fa_paged_update", "fa_paged_update_by_request"):
+            fn = getattr(lib, name)
+            fn.restype = _i
+            fn.argtypes = [_vp] * 10 + [_i] * 5 + [_vp]
         lib.fa_cache_append_fp8.restype = _i
         lib.fa_cache_append_fp8.argtypes = [_vp, _vp, _ll, _ll, _ll, _ll, _vp, _vp, _vp, _vp, _vp,
                                             _i, _i, _i, _i, _i, _i, _vp]
@@ -721,25 +724,35 @@ and position of every row [max_tokens], and the status of every request [B]
 
 def paged_update(seq_lens, delta, block_table, free_ring, ring_state, block_size: int,
                  max_tokens: int | None = None, seq_lens_out=None, ring_state_out=None, slot_map=None,
-                 positions=None, status=None, stream=None) -> PagedStep:
-    """One step of a paged cache's bookkeeping on the GPU (fa_paged_update).
+                 positions=None, status=None, stream=None, rows_per_request: int | None = None) -> PagedStep:
+    """One step of a paged cache's bookkeeping on the GPU (fa_paged_update, fa_paged_update_by_request).
 
     seq_lens and delta int32 [B] (tokens cached, and added or taken off);
     block_table int32 [B, max_blocks] and free_ring int32 [ring_size] are
     updated in place; ring_state int32 [2] is (head, count) of the free
     blocks.  ``max_tokens`` rows of slots and positions are written (given by
-    slot_map's length if that is passed).  Outputs are allocated unless given;
-    seq_lens_out and ring_state_out may be their inputs.
+    slot_map's length if that is passed), the added tokens' one after the
+    other.  With ``rows_per_request`` = n there are B * n rows instead, request
+    b's tokens in the last of rows b * n .. b * n + n - 1 and slot -1 in the
+    others: what a batch laid out by request, [B, heads, n, d], needs where a
+    request may add fewer than n tokens, or none.  Outputs are allocated unless
+    given; seq_lens_out and ring_state_out may be their inputs.
     """
     import torch
     if not seq_lens.is_cuda or seq_lens.dim() != 1 or block_table.dim() != 2 or free_ring.dim() != 1:
         raise FAError(FA_ERR_INVALID_ARG, "seq_lens [B] on a CUDA device, block_table [B,max_blocks], free_ring [n]")
     dev, i32 = seq_lens.device, torch.int32
     B, mb = seq_lens.shape[0], block_table.shape[1]
+    call, rows = "fa_paged_update", max_tokens
+    if rows_per_request is not None:
+        call, rows = "fa_paged_update_by_request", int(rows_per_request)
+        if max_tokens is not None and max_tokens != B * rows:
+            raise FAError(FA_ERR_INVALID_ARG, f"max_tokens is {max_tokens}, B * rows_per_request {B * rows}")
+        max_tokens = max(0, B * rows)
     if max_tokens is None:
         if slot_map is None and positions is None:
             raise FAError(FA_ERR_INVALID_ARG, "max_tokens, or slot_map, is needed")
-        max_tokens = (slot_map if slot_map is not None else positions).shape[0]
+        max_tokens = rows = (slot_map if slot_map is not None else positions).shape[0]
     _need_tensor("seq_lens", seq_lens, dev, i32, (B,))
     _need_tensor("delta", delta, dev, i32, (B,))
     _need_tensor("block_table", block_table, dev, i32, (B, mb))
@@ -756,14 +769,14 @@ def paged_update(seq_lens, delta, block_table, free_ring, ring_state, block_size
             else:
                 _need_tensor(name, t, dev, i32, (n,))
             outs.append(t)
-        st = (_lib or load()).fa_paged_update(
+        st = getattr(_lib or load(), call)(
             seq_lens.data_ptr(), delta.data_ptr(), block_table.data_ptr(), free_ring.data_ptr(),
             ring_state.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
             outs[3].data_ptr(), outs[4].data_ptr(), B, mb, free_ring.shape[0], int(block_size),
-            int(max_tokens), sp)
+            int(rows), sp)
     finally:
         _leave(scope)
-    _check(st, "fa_paged_update")
+    _check(st, call)
     return PagedStep(*outs)
 
 

@@ -386,6 +386,26 @@ fa_status fa_paged_update(const int *seq_lens, const int *delta, int *block_tabl
                           int block_size, int max_tokens, fa_stream_t stream);
 
 /*
+ * fa_paged_update_by_request -- fa_paged_update for batches laid out by request,
+ * as fa_decode_paged_fp8 takes q: slot_map and positions are
+ * [B, rows_per_request], and the delta tokens that request b adds are the LAST of
+ * its rows, so that row i of a request stands at position seq_lens_out[b] -
+ * rows_per_request + i.  Rows in front of them, and all rows of a request that
+ * adds none (an idle one, a finished one, a padding row of a captured batch), get
+ * slot -1 and position 0: nothing is written for them.  FA_PAGED_NO_ROWS: delta
+ * > rows_per_request.  rows_per_request >= 1; the rest as above.
+ *
+ * fa_paged_update's rows, in contrast, follow each other without gaps: row t is
+ * the t-th added token of the batch, so request b's are rows b .. only while
+ * every request adds exactly one.
+ */
+fa_status fa_paged_update_by_request(const int *seq_lens, const int *delta, int *block_table,
+                                     int *free_ring, const int *ring_state, int *seq_lens_out,
+                                     int *ring_state_out, int *slot_map, int *positions, int *status,
+                                     int B, int max_blocks, int ring_size, int block_size,
+                                     int rows_per_request, fa_stream_t stream);
+
+/*
  * fa_cache_append_fp8 -- writes new K and V rows into a paged cache held in
  * e4m3 codes with one scale per (block, K/V head), K and V apart: the value of
  * a code is code * scale.  For every block the call writes to:

@@ -67,14 +67,14 @@ def decode(q, kc, vc, ks, vs, table, lens, scale, mask):
     return o, lse, spread, reach, rest, small
 
 
-def check(got, q, kc, vc, ks, vs, table, lens, scale, mask):
+def check(got, q, kc, vc, ks, vs, table, lens, scale, mask, rows=None):
     """Scores: a dot of at most 256 exact products in fp32, 2^-18 of the sum of their sizes, a q
     component below 2^-13 of its row's largest off by 2^-21 of that, and the few steps of exponent
     and logarithm.  Weights: what P V takes is a weight times its block's scale, rounded to 16 bits
     with at most four rows per K/V head, else to 8 bits (bf16: fp16's 11, then two parts of 4) or 11
     (fp16), half a step each, or to 2^-20 of the largest such product of the step's keys (at most 256, so
     within a tile and its neighbours).  fp32 sums: 2^-16 of sum p |v| over the lengths here.  O is
-    rounded once."""
+    rounded once.  `rows`: rows per K/V head of the call, where q is a part of it."""
     want, want_lse, spread, reach, rest, small = decode(q, kc, vc, ks, vs, table, lens, scale, mask)
     o, lse = got[0].double(), got[1].double()
     none = torch.isneginf(want_lse)
@@ -84,7 +84,7 @@ def check(got, q, kc, vc, ks, vs, table, lens, scale, mask):
     tol = 2.0 ** -18 * reach + 2.0 ** -21 * small + 2.0 ** -20 * (1 + want_lse.abs())
     off = (lse - want_lse).abs()
     assert bool((off <= tol).all()), float((off / tol).max())
-    rows = q.shape[1] // kc.shape[1] * q.shape[2]
+    rows = rows or q.shape[1] // kc.shape[1] * q.shape[2]
     weight = 2.0 ** -16 if rows <= 4 else 2.0 ** -11 + (2.0 ** -8 if q.dtype == torch.bfloat16 else 0.0)
     bound = (weight + 2.0 ** -16 + 2 * tol[..., None]) * spread + HALF_STEP[q.dtype] * want.abs() + 2.0 ** -20 * rest + \
         2.0 ** -24
