@@ -250,9 +250,11 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
 // every growth of its scale.
 //
 // The tokens of one block stand together in slot_map, so the first of them
-// (the leader) stands for the block: a CTA takes a few consecutive rows of
-// slot_map and some of the (head, K or V) pairs, works out once for each leader
-// among its rows which row writes which slot of the block, and then gives each
+// (the leader) stands for the block.  Of G CTAs, one takes the leaders with rows
+// behind them among a few consecutive rows of slot_map, those that stand alone
+// among every G-th row (a prompt's blocks lie apart; the live rows of a decode step
+// in a map that is mostly padding lie together), and some of the (head, K or V)
+// pairs; it works out which row writes which slot of the block, and then gives each
 // pair's block to a group of WPU warps: enough that a lane holds its whole
 // share, eight 16-byte vectors (sixteen for blocks of 32,768 values), between
 // finding the maximum and writing the codes.  So a row is read once.  Bound by
@@ -303,202 +305,266 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t two) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// The slot of a row, -1 where it is skipped or there is none.  (The load is
+// unconditional, so that several are on their way at once.)
+__device__ __forceinline__ int append_slot(const int *slot_map, long long slots, int T, int row) {
+    const int s = slot_map[min(max(row, 0), T - 1)];
+    return row >= 0 && row < T && s >= 0 && s < slots ? s : -1;
+}
+
+// Long runs of skipped rows (a captured step with room for many tokens) are
+// looked through by the whole CTA, 16 rows per thread at a time.
+constexpr int kAppendLook = 16;
+
+// The last live row before `hi`, or -1.  All threads of the CTA.
+__device__ __noinline__ int append_last_live(const int *slot_map, long long slots, int T, int hi, int *s_row) {
+    const int tid = (int)threadIdx.x;
+    for (; hi > 0; hi -= kAppendLook * kAppendThreads) {
+        if (tid == 0) *s_row = -1;
+        __syncthreads();
+        int last = -1;
+#pragma unroll
+        for (int i = 0; i < kAppendLook; ++i) {
+            const int row = hi - 1 - i * kAppendThreads - tid;
+            if (append_slot(slot_map, slots, T, row) >= 0) last = max(last, row);
+        }
+        if (last >= 0) atomicMax(s_row, last);
+        __syncthreads();
+        last = *s_row;
+        __syncthreads();
+        if (last >= 0) return last;
+    }
+    return -1;
+}
+
+// Enters the rows of `block` from r0 on, up to the first live row of another
+// block, into owner.  All threads of the CTA.
+__device__ __noinline__ void append_rows_after(const int *slot_map, long long slots, int T, int bs_log2, int r0, int block,
+                                               int *owner, int *s_row) {
+    const int tid = (int)threadIdx.x, bs = 1 << bs_log2;
+    int stop = T;
+    if (r0 < stop) {  // (most blocks end soon: one row per thread first)
+        __syncthreads();
+        if (tid == 0) *s_row = stop;
+        __syncthreads();
+        const int s = append_slot(slot_map, slots, T, r0 + tid);
+        if (s >= 0 && s >> bs_log2 != block) atomicMin(s_row, r0 + tid);
+        __syncthreads();
+        stop = *s_row;
+        if (s >= 0 && r0 + tid < stop) atomicMax(&owner[s & (bs - 1)], r0 + tid);
+        r0 += kAppendThreads;
+    }
+    for (; r0 < stop; r0 += kAppendLook * kAppendThreads) {
+        __syncthreads();
+        if (tid == 0) *s_row = stop;
+        __syncthreads();
+        int s[kAppendLook], other = stop, high = -1;
+#pragma unroll
+        for (int i = 0; i < kAppendLook; ++i) s[i] = append_slot(slot_map, slots, T, r0 + i * kAppendThreads + tid);
+#pragma unroll
+        for (int i = kAppendLook - 1; i >= 0; --i) {
+            if (s[i] >= 0 && s[i] >> bs_log2 != block) other = r0 + i * kAppendThreads + tid;
+            high = max(high, s[i]);
+        }
+        if (other < stop) atomicMin(s_row, other);
+        const bool any = __syncthreads_or(high >= 0);
+        stop = *s_row;
+        if (!any) continue;
+#pragma unroll
+        for (int i = 0; i < kAppendLook; ++i) {
+            const int row = r0 + i * kAppendThreads + tid;
+            if (s[i] >= 0 && row < stop) atomicMax(&owner[s[i] & (bs - 1)], row);
+        }
+    }
+}
+
 template <bool kFP16, bool kVec, int HOLD>
 __global__ void __launch_bounds__(kAppendThreads, HOLD == 8 ? 4 : 2) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
-    constexpr int BACK = 128;       // rows looked at before the CTA's first, and from a leader on
+    constexpr int BACK = 128;       // rows looked at before a row, and from it on
     __shared__ int win[3 * BACK];   // slots of rows row0 - BACK .., -1 where a row is skipped or there is none
+    __shared__ int near[2 * BACK];  // the same round one row outside the CTA's
     __shared__ int owner[128];      // row that writes this slot of the block, or -1
-    __shared__ int s_row;
+    __shared__ int found[2 * 128];
+    __shared__ int s_row, s_found;
     __shared__ uint32_t s_max[kAppendThreads / 32];
+    static_assert(2 * BACK == kAppendThreads, "a slot of `near` per thread");
     const int tid = (int)threadIdx.x, lane = tid & 31, bs = 1 << p.bs_log2;
     const int row0 = (int)blockIdx.x * p.rows_per_cta;
     const int row1 = min(row0 + p.rows_per_cta, p.T);
-    auto slot_of = [&](int row) -> int {  // -1: skipped
-        const int s = row >= 0 && row < p.T ? p.slot_map[row] : -1;
-        return s >= 0 && s < p.slots ? s : -1;
-    };
     const int first = row0 - BACK;
+    auto slot_of = [&](int row) { return append_slot(p.slot_map, p.slots, p.T, row); };
+    auto same = [&](int s, int of) { return s >= 0 && s >> p.bs_log2 == of >> p.bs_log2; };
     ptx::wait_for_previous_kernel();
     for (int j = tid; j < BACK + p.rows_per_cta + BACK; j += kAppendThreads) win[j] = slot_of(first + j);
+    int alone = -1;  // a row that leads and is not followed by another of its block
+    if (tid < p.rows_per_cta) {
+        const int row = (int)blockIdx.x + (int)gridDim.x * tid;
+        const int s = slot_of(row);
+        if (s >= 0 && !same(slot_of(row - 1), s) && !same(slot_of(row + 1), s)) alone = row;
+    }
     if (tid < bs) owner[tid] = -1;
+    if (tid == 0) s_found = 0;
     // this thread's group, its place in it, and the pairs it takes
     const int gsize = 32 << p.wpu_log2, group = tid / gsize, in_group = tid & (gsize - 1);
     const int groups = kAppendThreads / gsize, pairs = 2 * p.Hkv;
     const int vec_log2 = p.d_log2 - 3, units = 1 << (vec_log2 + p.bs_log2);  // 8-value vectors of a row, a block
     __syncthreads();
+    if (tid < row1 - row0) {
+        const int *w = win + BACK + tid;
+        if (w[0] >= 0 && !same(w[-1], w[0]) && same(w[1], w[0])) found[atomicAdd(&s_found, 1)] = row0 + tid;
+    }
+    if (alone >= 0) found[atomicAdd(&s_found, 1)] = alone;
+    __syncthreads();
+    // (in any order: each has a block of its own)
+    for (int f = 0; f < s_found; ++f) {
+        const int row = found[f];
+        if (f > 0) {
+            __syncthreads();  // the block before is done with
+            if (tid < bs) owner[tid] = -1;
+        }
+        const int *w = win + (row - row0);  // w[BACK] is the row's slot
+        if (row < row0 || row >= row1) {
+            near[tid] = slot_of(row - BACK + tid);
+            w = near;
+        }
+        __syncthreads();
+        const int block = w[BACK] >> p.bs_log2;
 
-    // the block of the last live row before the CTA's rows (every warp for itself)
-    int prev = -1;
-    {
-        int at = -1;
+        // the block of the last live row before it (every warp for itself)
+        int prev = -1, at = -1;
 #pragma unroll
         for (int k = 0; k < BACK / 32; ++k) {
-            const uint32_t live = __ballot_sync(0xffffffffu, win[k * 32 + lane] >= 0);
+            const uint32_t live = __ballot_sync(0xffffffffu, w[k * 32 + lane] >= 0);
             if (live) at = k * 32 + 31 - __clz(live);
         }
         if (at >= 0) {
-            prev = win[at] >> p.bs_log2;
-        } else if (first > 0) {  // (a long run of skipped rows)
-            int seen = -1;
-            for (int hi = first; hi > 0 && seen < 0; hi -= 32) {
-                const uint32_t live = __ballot_sync(0xffffffffu, slot_of(hi - 1 - lane) >= 0);
-                if (live) seen = hi - __ffs(live);
-            }
+            prev = w[at] >> p.bs_log2;
+        } else if (row > BACK) {  // (a long run of skipped rows)
+            const int seen = append_last_live(p.slot_map, p.slots, p.T, row - BACK, &s_row);
             if (seen >= 0) prev = p.slot_map[seen] >> p.bs_log2;
         }
-    }
-    // The leaders among the CTA's rows, 32 at a time (every warp for itself): a
-    // live row whose last live row before it is of another block.
-    bool used = false;  // owner holds an earlier leader's rows
-    for (int seg = row0; seg < row1; seg += 32) {
-        const int here = seg + lane < row1 ? win[seg + lane - first] : -1;
-        const uint32_t live = __ballot_sync(0xffffffffu, here >= 0), before = live & ((1u << lane) - 1);
-        const int at_before = __shfl_sync(0xffffffffu, here, before ? 31 - __clz(before) : 0);
-        const int block_before = before ? at_before >> p.bs_log2 : prev;
-        uint32_t leaders = __ballot_sync(0xffffffffu, here >= 0 && here >> p.bs_log2 != block_before);
-        if (live) prev = __shfl_sync(0xffffffffu, here, 31 - __clz(live)) >> p.bs_log2;
-        for (; leaders; leaders &= leaders - 1) {
-            const int row = seg + __ffs(leaders) - 1, j0 = row - first;
-            const int block = win[j0] >> p.bs_log2;
+        if (prev == block) continue;
 
-            // its rows: up to the first live row of another block
-            if (used) {
-                __syncthreads();
-                if (tid < bs) owner[tid] = -1;
-                __syncthreads();
-            }
-            used = true;
-            int end = BACK;
+        // its rows: up to the first live row of another block
+        int end = BACK;
 #pragma unroll
-            for (int k = BACK / 32 - 1; k >= 0; --k) {
-                const int s = win[j0 + k * 32 + lane];
-                const uint32_t other = __ballot_sync(0xffffffffu, s >= 0 && s >> p.bs_log2 != block);
-                if (other) end = k * 32 + __ffs(other) - 1;
-            }
-            if (tid < end) {  // a slot named twice: the later row
-                const int s = win[j0 + tid];
-                if (s >= 0) atomicMax(&owner[s & (bs - 1)], row + tid);
-            }
-            if (end == BACK) {  // (rows past the first look)
-                int stop = p.T;
-                for (int r0 = row + BACK; r0 < stop; r0 += kAppendThreads) {
-                    __syncthreads();
-                    if (tid == 0) s_row = stop;
-                    __syncthreads();
-                    const int s = slot_of(r0 + tid);
-                    if (s >= 0 && s >> p.bs_log2 != block) atomicMin(&s_row, r0 + tid);
-                    __syncthreads();
-                    stop = s_row;
-                    if (s >= 0 && r0 + tid < stop) atomicMax(&owner[s & (bs - 1)], r0 + tid);
+        for (int k = BACK / 32 - 1; k >= 0; --k) {
+            const int s = w[BACK + k * 32 + lane];
+            const uint32_t other = __ballot_sync(0xffffffffu, s >= 0 && s >> p.bs_log2 != block);
+            if (other) end = k * 32 + __ffs(other) - 1;
+        }
+        if (tid < end) {  // a slot named twice: the later row
+            const int s = w[BACK + tid];
+            if (s >= 0) atomicMax(&owner[s & (bs - 1)], row + tid);
+        }
+        if (end == BACK)  // (past the first look)
+            append_rows_after(p.slot_map, p.slots, p.T, p.bs_log2, row + BACK, block, owner, &s_row);
+        __syncthreads();
+
+        const bool begun = owner[0] >= 0;
+        for (int pair = (int)blockIdx.y * groups + group; pair < pairs; pair += (int)gridDim.y * groups) {
+            const int kv = pair >= p.Hkv, head = pair - (kv ? p.Hkv : 0);
+            const uint16_t *x = reinterpret_cast<const uint16_t *>(p.x[kv]) + head * p.head_stride[kv];
+            const size_t bh = (size_t)block * p.Hkv + head;
+            uint8_t *codes = p.cache[kv] + (bh << (p.d_log2 + p.bs_log2));
+            const float old = p.scale[kv][bh];
+            auto source = [&](int u, int r) {
+                return x + r * p.token_stride[kv] + ((u & ((1 << vec_log2) - 1)) << 3);
+            };
+            // Only what every call does is unrolled (registers cannot be indexed
+            // otherwise); infinities, scales that are no powers of two and growth
+            // of the scale take the short loops, which read again: the whole in
+            // line was several times the code, and fetching it cost a decode step
+            // more than its data (128 rows x 40 heads: 19 us against 12; 8,203 rows
+            // of prompts x 8 heads: 45 against 24).
+            uint4 held[HOLD];
+            uint32_t mine = 0;  // which of this lane's vectors are written
+#pragma unroll
+            for (int i = 0; i < HOLD; ++i) {
+                const int u = in_group + i * gsize;
+                const int r = u < units ? owner[u >> vec_log2] : -1;
+                held[i] = make_uint4(0, 0, 0, 0);
+                if (r >= 0) {
+                    mine |= 1u << i;
+                    held[i] = load8_16<kVec>(source(u, r));
                 }
             }
-            __syncthreads();
-
-            const bool begun = owner[0] >= 0;
-            for (int pair = (int)blockIdx.y * groups + group; pair < pairs; pair += (int)gridDim.y * groups) {
-                const int kv = pair >= p.Hkv, head = pair - (kv ? p.Hkv : 0);
-                const uint16_t *x = reinterpret_cast<const uint16_t *>(p.x[kv]) + head * p.head_stride[kv];
-                const size_t bh = (size_t)block * p.Hkv + head;
-                uint8_t *codes = p.cache[kv] + (bh << (p.d_log2 + p.bs_log2));
-                const float old = p.scale[kv][bh];
-                auto source = [&](int u, int r) {
-                    return x + r * p.token_stride[kv] + ((u & ((1 << vec_log2) - 1)) << 3);
-                };
-                // Only what every call does is unrolled (registers cannot be indexed
-                // otherwise); infinities, scales that are no powers of two and growth
-                // of the scale take the short loops, which read again: the whole in
-                // line was several times the code, and fetching it cost a decode step
-                // more than its data (128 rows x 40 heads: 19 us against 12; 8,203 rows
-                // of prompts x 8 heads: 45 against 24).
-                uint4 held[HOLD];
-                uint32_t mine = 0;  // which of this lane's vectors are written
+            // 16-bit magnitudes are ordered as whole numbers
+            uint32_t top2 = 0;
+#pragma unroll
+            for (int i = 0; i < HOLD; ++i) {
+                top2 = __vmaxu2(top2, __vmaxu2(held[i].x & 0x7fff7fffu, held[i].y & 0x7fff7fffu));
+                top2 = __vmaxu2(top2, __vmaxu2(held[i].z & 0x7fff7fffu, held[i].w & 0x7fff7fffu));
+            }
+            constexpr uint32_t kInf = kFP16 ? 0x7c00u : 0x7f80u;
+            uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+            if (top >= kInf) {  // the largest finite one
+                top = 0;
+                for (int u = in_group; u < units; u += gsize) {
+                    const int r = owner[u >> vec_log2];
+                    for (int j = 0; r >= 0 && j < 8; ++j) {
+                        const uint32_t v = source(u, r)[j] & 0x7fffu;
+                        top = max(top, v < kInf ? v : 0u);
+                    }
+                }
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (p.wpu_log2 > 0) {
+                if ((tid & 31) == 0) s_max[tid >> 5] = top;
+                ptx::named_bar_sync(1 + group, gsize);  // also: the group has read the old scale
+                for (int w = 0; w < gsize / 32; ++w) top = max(top, s_max[group * (gsize / 32) + w]);
+                ptx::named_bar_sync(1 + group, gsize);
+            }
+            __syncwarp();
+            const float need = scale_for(unpack16<kFP16>(top).x);
+            // (an old scale that is no positive finite number counts as none)
+            const float now = begun || !(old > need) || isinf(old) ? need : old;
+            const bool grew = !begun && old > 0.f && now > old;
+            const uint32_t nb = __float_as_uint(now);
+            if ((nb & 0x7fffffu) == 0 && (nb >> 23) < 254) {  // x / now by its exact inverse
+                const float inv = __uint_as_float((254u - (nb >> 23)) << 23);
 #pragma unroll
                 for (int i = 0; i < HOLD; ++i) {
-                    const int u = in_group + i * gsize;
-                    const int r = u < units ? owner[u >> vec_log2] : -1;
-                    held[i] = make_uint4(0, 0, 0, 0);
-                    if (r >= 0) {
-                        mine |= 1u << i;
-                        held[i] = load8_16<kVec>(source(u, r));
-                    }
-                }
-                // 16-bit magnitudes are ordered as whole numbers
-                uint32_t top2 = 0;
+                    if (!(mine >> i & 1)) continue;
+                    const uint32_t ws[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
+                    float f[8];
 #pragma unroll
-                for (int i = 0; i < HOLD; ++i) {
-                    top2 = __vmaxu2(top2, __vmaxu2(held[i].x & 0x7fff7fffu, held[i].y & 0x7fff7fffu));
-                    top2 = __vmaxu2(top2, __vmaxu2(held[i].z & 0x7fff7fffu, held[i].w & 0x7fff7fffu));
-                }
-                constexpr uint32_t kInf = kFP16 ? 0x7c00u : 0x7f80u;
-                uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-                if (top >= kInf) {  // the largest finite one
-                    top = 0;
-                    for (int u = in_group; u < units; u += gsize) {
-                        const int r = owner[u >> vec_log2];
-                        for (int j = 0; r >= 0 && j < 8; ++j) {
-                            const uint32_t v = source(u, r)[j] & 0x7fffu;
-                            top = max(top, v < kInf ? v : 0u);
-                        }
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 y = unpack16<kFP16>(ws[j]);
+                        f[2 * j] = y.x * inv;
+                        f[2 * j + 1] = y.y * inv;
                     }
+                    *reinterpret_cast<uint2 *>(codes + (size_t)(in_group + i * gsize) * 8) =
+                        make_uint2(ptx::pack_e4m3x4(f[0], f[1], f[2], f[3]), ptx::pack_e4m3x4(f[4], f[5], f[6], f[7]));
                 }
-                top = __reduce_max_sync(0xffffffffu, top);
-                if (p.wpu_log2 > 0) {
-                    if ((tid & 31) == 0) s_max[tid >> 5] = top;
-                    ptx::named_bar_sync(1 + group, gsize);  // also: the group has read the old scale
-                    for (int w = 0; w < gsize / 32; ++w) top = max(top, s_max[group * (gsize / 32) + w]);
-                    ptx::named_bar_sync(1 + group, gsize);
+            } else {
+#pragma unroll 1
+                for (int u = in_group; u < units; u += gsize) {
+                    const int r = owner[u >> vec_log2];
+#pragma unroll 1
+                    for (int j = 0; r >= 0 && j < 8; ++j)
+                        codes[(size_t)u * 8 + j] =
+                            (uint8_t)ptx::pack_e4m3x4(__fdiv_rn(unpack16<kFP16>(source(u, r)[j]).x, now), 0.f, 0.f, 0.f);
                 }
-                __syncwarp();
-                const float need = scale_for(unpack16<kFP16>(top).x);
-                // (an old scale that is no positive finite number counts as none)
-                const float now = begun || !(old > need) || isinf(old) ? need : old;
-                const bool grew = !begun && old > 0.f && now > old;
-                const uint32_t nb = __float_as_uint(now);
-                if ((nb & 0x7fffffu) == 0 && (nb >> 23) < 254) {  // x / now by its exact inverse
-                    const float inv = __uint_as_float((254u - (nb >> 23)) << 23);
-#pragma unroll
-                    for (int i = 0; i < HOLD; ++i) {
-                        if (!(mine >> i & 1)) continue;
-                        const uint32_t ws[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
-                        float f[8];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 y = unpack16<kFP16>(ws[j]);
-                            f[2 * j] = y.x * inv;
-                            f[2 * j + 1] = y.y * inv;
-                        }
-                        *reinterpret_cast<uint2 *>(codes + (size_t)(in_group + i * gsize) * 8) =
-                            make_uint2(ptx::pack_e4m3x4(f[0], f[1], f[2], f[3]), ptx::pack_e4m3x4(f[4], f[5], f[6], f[7]));
-                    }
-                } else {
-#pragma unroll 1
-                    for (int u = in_group; u < units; u += gsize) {
-                        const int r = owner[u >> vec_log2];
-#pragma unroll 1
-                        for (int j = 0; r >= 0 && j < 8; ++j)
-                            codes[(size_t)u * 8 + j] =
-                                (uint8_t)ptx::pack_e4m3x4(__fdiv_rn(unpack16<kFP16>(source(u, r)[j]).x, now), 0.f, 0.f, 0.f);
-                    }
-                }
-                if (grew) {
-#pragma unroll 1
-                    for (int u = in_group; u < units; u += gsize) {
-                        if (owner[u >> vec_log2] >= 0) continue;
-                        uint2 *dst = reinterpret_cast<uint2 *>(codes + (size_t)u * 8);
-                        const uint2 w = *dst;
-                        uint32_t out[2] = {0, 0};
-#pragma unroll 1
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 y = unpack_e4m3x2((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
-                            const uint32_t two = ptx::pack_e4m3x4(__fdiv_rn(y.x * old, now), __fdiv_rn(y.y * old, now), 0.f, 0.f);
-                            if (j < 2) out[0] |= two << (16 * j);
-                            else out[1] |= two << (16 * (j - 2));
-                        }
-                        *dst = make_uint2(out[0], out[1]);
-                    }
-                }
-                if (in_group == 0) p.scale[kv][bh] = now;
             }
+            if (grew) {
+#pragma unroll 1
+                for (int u = in_group; u < units; u += gsize) {
+                    if (owner[u >> vec_log2] >= 0) continue;
+                    uint2 *dst = reinterpret_cast<uint2 *>(codes + (size_t)u * 8);
+                    const uint2 w = *dst;
+                    uint32_t out[2] = {0, 0};
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 y = unpack_e4m3x2((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
+                        const uint32_t two = ptx::pack_e4m3x4(__fdiv_rn(y.x * old, now), __fdiv_rn(y.y * old, now), 0.f, 0.f);
+                        if (j < 2) out[0] |= two << (16 * j);
+                        else out[1] |= two << (16 * (j - 2));
+                    }
+                    *dst = make_uint2(out[0], out[1]);
+                }
+            }
+            if (in_group == 0) p.scale[kv][bh] = now;
         }
     }
 }
