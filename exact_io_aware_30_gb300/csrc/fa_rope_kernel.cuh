@@ -12,7 +12,10 @@
 // 2^-64 turn), so n * f_i modulo one turn is one wrapping integer product, as
 // exact at position 10^9 as at 0 -- an fp32 product would lose the angle of
 // far positions (2^-24 n radians) and an fp64 one would run at a few per cent
-// of the fp32 rate.  The top 32 bits become half turns in fp32 for sincospi.
+// of the fp32 rate.  Of the top 32 bits the nearest quarter turn comes off in whole
+// numbers, and the rest, at most an eighth of a turn, becomes half turns in fp32 for
+// sincospi: off by 2^-27 of a half turn, where the whole angle in one float was
+// off by up to 2^-25.
 // Products and sums are fp32, each output rounded once.
 //
 // What bounds it: every element is read and written once, 3 flops each, so
@@ -138,9 +141,19 @@ __global__ void __launch_bounds__(256, 4) fa_rope_kernel(const __grid_constant__
             int pair = slot * V + i;
             if (kInterleaved && V > 1) pair = i < V / 2 ? e0 / 2 + i : e1 / 2 + i - V / 2;
             const unsigned long long phase = (unsigned long long)n * p.freq[pair];
-            const float x = (float)(int)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
+            const uint32_t turned = (uint32_t)(phase >> 32) + (1u << 29);  // from an eighth of a turn before
+            const float x = (float)((int)(turned & 0x3fffffffu) - (1 << 29)) * 4.656612873077393e-10f;  // 2^-31
             float si, co;
             sincospif(x, &si, &co);
+            if (turned & (1u << 30)) {  // a quarter turn on
+                const float was = si;
+                si = co;
+                co = -was;
+            }
+            if (turned & (1u << 31)) {
+                si = -si;
+                co = -co;
+            }
             cs[i] = co * p.amplitude;
             sn[i] = si * p.amplitude * p.sin_sign;
         }
