@@ -110,7 +110,7 @@ fa_status rope_impl(const void *q, const long long *q_strides, void *q_out, cons
     if (S == 0) return FA_OK;
     if (!q || !q_strides || !q_out || !q_out_strides || !freq) return FA_ERR_INVALID_ARG;
     if (Hkv > 0 && (!k || !k_strides || !k_out || !k_out_strides)) return FA_ERR_INVALID_ARG;
-    if (pos_stride < 0) return FA_ERR_INVALID_ARG;
+    if (pos_stride < 0 || pos_stride > (1LL << 40)) return FA_ERR_INVALID_ARG;  // (as the other strides below)
 
     const int elem = dtype == FA_DTYPE_FP32 ? 4 : 2;
     const int n_views = Hkv > 0 ? 2 : 1;

@@ -300,8 +300,8 @@ fa_status fa_decode_workspace_query(int B, int H, int H_kv, int Sq, int d, int b
  *   k, k_out   [B, H_kv, S, d] alike; H_kv == 0: no k, the four are not
  *              examined
  *   positions  device int32, row (b, s) at positions[b * position_stride + s]
- *              (stride 0: one row for every batch), or NULL: 0 .. S-1;
- *              negative ones are allowed
+ *              (stride 0: one row for every batch; at most 2^40), or NULL:
+ *              0 .. S-1; negative ones are allowed
  *   offset     added to every position
  *   freq       device array of rot_dim / 2 frequencies, turns per position
  *              times 2^64, as fa_rope_frequencies writes them; 8-byte aligned
