@@ -635,6 +635,9 @@ def _rope(q, k, plan, positions, offset, layout, out_q, out_k, stream, direction
     lay = ROPE_LAYOUTS.get(layout)
     if lay is None:
         raise FAError(FA_ERR_UNSUPPORTED, f"layout {layout!r}: one of {list(ROPE_LAYOUTS)}")
+    rot_dim, freq, amplitude = plan
+    if freq.dtype != torch.int64 or not freq.is_contiguous() or 2 * freq.numel() < rot_dim:
+        raise FAError(FA_ERR_INVALID_ARG, f"the plan's frequencies must be {rot_dim // 2} contiguous int64")
     dt = _rope_dtype(q)
     dev, dtype = q.device, q.dtype
     if not q.is_cuda or q.dim() != 4:
@@ -653,7 +656,6 @@ def _rope(q, k, plan, positions, offset, layout, out_q, out_k, stream, direction
         _need_tensor("out_q", out_q, dev, dtype, q_shape, contiguous=False)
     if out_k is not None:
         _need_tensor("out_k", out_k, dev, dtype, k_shape, contiguous=False)
-    rot_dim, freq, amplitude = plan
     if freq.device != dev:
         raise FAError(FA_ERR_INVALID_ARG, f"the plan is on {freq.device}, the tensors on {dev}")
     pos_ptr, pos_stride = None, 0
