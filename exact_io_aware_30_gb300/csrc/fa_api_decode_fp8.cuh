@@ -46,6 +46,19 @@ struct DecFp8Plan {
     size_t part_lse_off = 0, part_o_off = 0, bytes = 0;
 };
 
+// Tiles per step as they were measured: a change of the shared memory's small
+// arrays must not change them unseen.
+template <int D, int RC>
+constexpr bool dec_fp8_tiles_per_step(int bf16, int fp16) {
+    return DecFp8Cfg<D, false, RC>::KPT == bf16 && DecFp8Cfg<D, true, RC>::KPT == fp16;
+}
+static_assert(dec_fp8_tiles_per_step<64, 1>(1, 1) && dec_fp8_tiles_per_step<64, 4>(1, 1) && dec_fp8_tiles_per_step<64, 8>(2, 2) &&
+              dec_fp8_tiles_per_step<64, 16>(2, 2) && dec_fp8_tiles_per_step<64, 24>(2, 2) && dec_fp8_tiles_per_step<64, 32>(2, 1));
+static_assert(dec_fp8_tiles_per_step<128, 1>(1, 1) && dec_fp8_tiles_per_step<128, 4>(1, 1) && dec_fp8_tiles_per_step<128, 8>(1, 1) &&
+              dec_fp8_tiles_per_step<128, 16>(2, 2) && dec_fp8_tiles_per_step<128, 24>(2, 2) && dec_fp8_tiles_per_step<128, 32>(2, 1));
+static_assert(dec_fp8_tiles_per_step<256, 1>(1, 1) && dec_fp8_tiles_per_step<256, 4>(1, 1) && dec_fp8_tiles_per_step<256, 8>(1, 1) &&
+              dec_fp8_tiles_per_step<256, 16>(1, 1) && dec_fp8_tiles_per_step<256, 24>(1, 1));
+
 template <int D, bool kFP16>
 int dec_fp8_ctas_per_sm(int rc) {
     return rc == 1    ? DecFp8Cfg<D, kFP16, 1>::CTAS_PER_SM

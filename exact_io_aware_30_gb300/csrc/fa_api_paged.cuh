@@ -159,10 +159,11 @@ fa_status cache_append_impl(const void *k, const void *v, long long k_token_stri
     const int block_log2 = p.d_log2 + p.bs_log2;
     p.wpu_log2 = std::min(std::max(block_log2 - 11, 0), 3);
     const bool big = block_log2 > 14;  // 32,768 values: sixteen vectors a lane
-    // Two pairs per group, and rows until the grid is about two waves (four
-    // CTAs per SM), at most a block's: in a decode step every row leads a block
-    // of its own; in a prompt one row of a block does, and the others only read
-    // their slot.
+    // Two pairs per group, and rows until the grid is at most two waves (of four
+    // CTAs per SM) or a block's: in a decode step every row leads a block of its own;
+    // in a prompt one row of a block does, and the others only read their slot.
+    // (Two waves at most, not one: 128 rows x 40 heads are 640 CTAs, 32 more than fit
+    // at once.  Four waves 15.0 us for 8,203 rows in blocks of 16 where two take 11.8.)
     const int groups = kAppendThreads / (32 << p.wpu_log2);
     const int y = std::max(1, (2 * Hkv + 2 * groups - 1) / (2 * groups));
     p.rows_per_cta = 1;

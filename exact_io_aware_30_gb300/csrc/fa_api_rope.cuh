@@ -88,7 +88,8 @@ template <typename T, int V>
 fa_status launch_rope(const RopeParams &p, int layout, dim3 grid, cudaStream_t stream) {
     // Two heads in flight; one for interleaved pairs of part of the head (bf16,
     // half of d 128, 134 MB: one 29 us, two 31, four 47; all of it, fp16, 268 MB:
-    // one 55 us, two 48, four 47; half layout: one 54 us, two 48, four 49).
+    // one 55 us, two 48, four 47; half layout: one 54 us, two 48, four 49).  With two, whole
+    // heads in bf16 spill 12 to 16 bytes a thread.
     auto kern = layout != FA_ROPE_INTERLEAVED ? fa_rope_kernel<T, V, false, 2>
                 : p.rot < p.d                 ? fa_rope_kernel<T, V, true, 1>
                                               : fa_rope_kernel<T, V, true, 2>;

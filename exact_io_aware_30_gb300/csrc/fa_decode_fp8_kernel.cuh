@@ -56,9 +56,11 @@
 //   an MMA warp: S^T of step s + 1 before O^T of step s;
 //   a TMA warp: a lane per block of the tile, K and V rings.
 //
-// Measured: 128 requests x 40 heads, up to 2,048 tokens, fp16: 237 us (6.4 TB/s,
-// 95 % of a copy); 64 requests, 32 heads on 8, up to 8,192, bf16: 97 us (92 %); d 64
-// 51 us for 269 MB; 16 rows 112, 32 rows 164 us where one takes 90.
+// Measured: 128 requests x 40 heads, up to 2,048 tokens, fp16: 247 us (6.2 TB/s,
+// 91 % of a copy); 64 requests, 32 heads on 8, up to 8,192, bf16: 97 us (92 %).  64
+// requests x 8 K/V heads, full lengths, bf16, with 1 / 4 / 8 rows: 52 / 63 / 61 us at d
+// 64 (269 MB), 87 / 90 / 88 at d 128 and 83 / 84 / 87 at d 256 (537 MB); 16, 24, 32 rows
+// at d 128 108, 130, 167.
 #pragma once
 
 #include <math.h>
@@ -143,7 +145,8 @@ struct DecFp8Cfg {
     // rings keep two steps.  Most of a step's time is a chain of waits,
     // exchanges and short loads that does not grow with its keys (d 64, 8 rows:
     // 84 -> 66 us; d 128, 24 rows: 193 -> 145 us); with shorter rings the
-    // second step's copies start late (d 128, 1 row: 92 -> 107 us).
+    // second step's copies start late (d 128, 1 row: 92 -> 107 us).  That is two for
+    // 8 to 24 rows at d 64, 16 and 24 at d 128, and 32 there in bf16.
     static constexpr int KPT = cols(2) <= 512 / ctas(2) && slots(2) >= 8 ? 2 : 1;
     static constexpr int COLS = cols(KPT);
     static constexpr int CTAS_PER_SM = ctas(KPT);

@@ -258,8 +258,10 @@ __global__ void __launch_bounds__(kPagedThreads) fa_paged_update_kernel(const Pa
 // pair's block to a group of WPU warps: enough that a lane holds its whole
 // share, eight 16-byte vectors (sixteen for blocks of 32,768 values), between
 // finding the maximum and writing the codes.  So a row is read once.  Bound by
-// latency, slots then rows and scale then stores: 128 rows x 40 heads 8.8 us, 8,203
-// rows x 8 heads (50 MB) 14.3 us, where the copy rate would take 0.6 and 7.4.
+// latency, slots then rows and scale then stores: 128 rows x 40 heads 9.1 us, 8,203
+// rows x 8 heads (50 MB) 17.3 us, where the copy rate would take 0.6 and 7.4.  64
+// live rows in front of 65,472 skipped ones 38 us, behind them 22 (950 and 988
+// where every CTA walked back through them 32 at a time), every row skipped 8.
 
 struct AppendParams {
     const uint8_t *x[2];        // new K and V rows, 16-bit
@@ -313,7 +315,8 @@ __device__ __forceinline__ int append_slot(const int *slot_map, long long slots,
 }
 
 // Long runs of skipped rows (a captured step with room for many tokens) are
-// looked through by the whole CTA, 16 rows per thread at a time.
+// looked through by the whole CTA, 16 rows per thread at a time.  (Out of line:
+// few calls need it.)
 constexpr int kAppendLook = 16;
 
 // The last live row before `hi`, or -1.  All threads of the CTA.

@@ -80,7 +80,7 @@ struct alignas(sizeof(T) * V) RopeVec {
 
 // V elements per vector; each thread rotates V pairs (two vectors).  U heads are
 // in flight at once: four CTAs of 64 registers a thread hide the memory's
-// latency, and more heads per thread spill.
+// latency; two heads fill those registers (the host's comment has the figures).
 template <typename T, int V, bool kInterleaved, int U>
 __global__ void __launch_bounds__(256, 4) fa_rope_kernel(const __grid_constant__ RopeParams p) {
     using Vec = RopeVec<T, V>;

@@ -287,9 +287,11 @@ fa_status fa_decode_workspace_query(int B, int H, int H_kv, int Sq, int d, int b
  * i of a row at position n becomes
  *     y1 = a (x1 cos t - x2 sin t),  y2 = a (x1 sin t + x2 cos t),
  *     t = n * f_i,   a = amplitude,
- * and components rot_dim .. d pass through.  Angles are taken modulo a turn in
- * 64-bit fixed point, so they are as accurate at position 2^31 as at 0.
- * Products and sums are fp32, each output is rounded once.
+ * and components rot_dim .. d pass through.  The product n * f_i is exact
+ * modulo a turn (64-bit fixed point); the f_i of fa_rope_frequencies are fp64, so
+ * that an angle is within 2^-53 of its whole size, 2^-22 radians at position
+ * 2^31, of the formula's.  Products and sums are fp32, each output is rounded
+ * once.
  *
  *   q, q_out   [B, H, S, d] by strides: q_strides[3] are the element strides of
  *              batch, head and token, on the host; components are adjacent.
@@ -448,9 +450,8 @@ fa_status fa_cache_append_fp8(const void *k, const void *v, long long k_token_st
  * their row's largest: those may be off by 2^-21 of that.  Each weight is
  * rounded to 16 bits before P V with up to four rows per K/V head, else to 8
  * (bf16) or 11 (fp16) bits, as where fa_decode_paged uses the tensor cores;
- * a weight times its V scale below 2^-20 of the row's largest such product
- * among up to 256 neighbouring keys may be off by that 2^-20.  Sums are fp32.
- * Deterministic.  Two launches at most; the workspace's
+ * and to no finer than 2^-20 of the row's largest product of a weight and its
+ * V scale among up to 256 neighbouring keys.  Sums are fp32.  Deterministic.  Two launches at most; the workspace's
  * contents on entry do not matter.  Arguments as for fa_decode_paged, except:
  *
  *   k_cache, v_cache  [num_blocks, H_kv, block_size, d] e4m3
@@ -466,7 +467,10 @@ fa_status fa_cache_append_fp8(const void *k, const void *v, long long k_token_st
  *                aligned (may be NULL where that is 0); calls that may overlap in time (other streams, graphs
  *                replayed beside each other) need one each
  *   max_seq_len  at most 2^31 - 513
- * Cache slots past a request's length may hold any codes, NaN included.
+ * Cache slots past a request's length may hold any codes, NaN included.  A NaN
+ * code of V within the length makes its column NaN in all rows of the request
+ * and K/V head, also in those that FA_MASK_CAUSAL hides it from (a weight of 0
+ * times NaN).
  */
 fa_status fa_decode_paged_fp8(const void *q, const void *k_cache, const void *v_cache,
                               const float *k_scale, const float *v_scale, const int *block_table,
