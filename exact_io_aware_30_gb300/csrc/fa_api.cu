@@ -2,8 +2,8 @@
 // validation, TMA tensor-map encoding, kernel selection and launch.  This file
 // holds the shared helpers and the forward (fa_fwd, fa_fwd_fp16, fa_fwd_gqa);
 // the backward, paged decoding, the 8-bit forward, the forward from host
-// memory, rotary positions, the paged cache's updates and decoding over the
-// 8-bit cache are in the other fa_api_*.cuh, included at the end (one
+// memory, rotary positions, the paged cache's updates, decoding over the 8-bit
+// cache and the 4-bit cache are in the other fa_api_*.cuh, included at the end (one
 // translation unit).
 //
 // Validation happens before anything is enqueued and never falls back to a
@@ -47,6 +47,7 @@ struct DeviceInfo {
     bool attr_dec[6] = {false, false, false, false, false, false};
     bool attr_fp8[3] = {false, false, false};  // 8-bit forward, d = 64, 128, 256
     bool attr_dec_fp8[36] = {};  // 8-bit cache decode: d = 64, 128, 256 x bf16, fp16 x rows
+    bool attr_dec_int4[18] = {};  // 4-bit cache decode: d = 64, 128, 256 x groups of 32, 64 x rows
     bool attr_gemv[12] = {};  // few-row decode: d = 64, 128, 256 x bf16, fp16 x 1, 2 rows
 };
 
@@ -522,8 +523,8 @@ fa_status fa_get_device_error(void) {
 
 // The other entry points, each with its kernels: the backward, decoding over a
 // paged cache, the 8-bit forward, the forward from host memory, rotary
-// positions, the paged cache's bookkeeping and 8-bit writes, and decoding over
-// the 8-bit cache.
+// positions, the paged cache's bookkeeping and 8-bit writes, decoding over the
+// 8-bit cache, and the 4-bit cache.
 #include "fa_api_bwd.cuh"
 #include "fa_api_decode.cuh"
 #include "fa_api_fp8.cuh"
@@ -531,3 +532,4 @@ fa_status fa_get_device_error(void) {
 #include "fa_api_rope.cuh"
 #include "fa_api_paged.cuh"
 #include "fa_api_decode_fp8.cuh"
+#include "fa_api_int4.cuh"

@@ -1,0 +1,252 @@
+// fa_int4_kernel.cuh -- a paged K/V cache held in 4 bits, for sm_103a: the write
+// that quantises rows (fa_cache_append_int4) and reading rows back in 16 bits
+// (fa_cache_read_int4).  The attention over it is in fa_decode_int4_kernel.cuh.
+//
+// A cached row of d components is in groups of G (32 or 64) adjacent ones.  A
+// group is G codes c = 0 .. 15, two to a byte (component 2i in the low half of
+// byte i), and one word: the scale s >= 0 (bf16) in its high half, the zero z (a
+// whole number, |z| <= 2048, in fp16) in its low half.  The value is s (c - z).
+//
+// Write, per group of finite values x_i, lo and hi the smallest and largest:
+//     t   = max((hi - lo) / 15, max |x| / 2048)      in fp32
+//     s   = t rounded up to bf16
+//     n_i = x_i / s rounded to nearest even, c_i = min(n_i - min n, 15), z = -min n
+// The second term bounds z: a group whose values lie close together far from 0
+// is held to 2^-12 of its largest, finer than bf16.  Rounding s up keeps the
+// grid over [lo, hi], so a value is off by at most s / 2.  All zero: s = c = z =
+// 0.  A group with an infinity or NaN: s is NaN, c = z = 0, and it reads as NaN.
+#pragma once
+
+#include <stdint.h>
+
+#include "fa_paged_kernel.cuh"
+
+namespace fa {
+
+constexpr int kInt4Threads = 256;
+constexpr int kInt4Look = 128;     // a slot's later writer is looked for among this many rows
+constexpr int kInt4MaxRows = 64;   // rows of a CTA of the append
+
+struct Int4AppendParams {
+    const uint16_t *x[2];       // new K and V rows, 16-bit
+    long long token_stride[2], head_stride[2];  // in elements
+    uint8_t *codes[2];          // [num_blocks, Hkv, bs, d / 2]
+    uint32_t *words[2];         // [num_blocks, Hkv, bs, d / G]
+    const int *slot_map;        // [T]
+    long long slots;            // num_blocks * bs
+    int T, Hkv, d_log2, g_log2, bs_log2, rows_per_cta;
+    int items_log2;             // threads along a row's (K or V, head, vector of 8) items
+};
+
+// The integer nearest to y (ties to even), |y| < 2^22: in [2^23, 2^24) the step
+// of fp32 is 1.
+__device__ __forceinline__ float round_even(float y) { return (y + 12582912.f) - 12582912.f; }
+
+// 8 values of a group, rounded to the group's grid as whole numbers.  The
+// quotient is x times 1 / s, corrected once by its own remainder (Markstein's
+// step), which makes it exact wherever it has few bits, halves among them: so
+// ties are found.  A quotient that is no tie is at least 2^-13 of a step away
+// from one (x has at most 11 bits and s 8), far more than the quotient is off.
+__device__ __forceinline__ float int4_grid(float x, float s, float inv) {
+    const float y = x * inv;
+    return round_even(fmaf(fmaf(-y, s, x), inv, y));
+}
+
+template <bool kFP16>
+struct Int4Group {
+    uint32_t codes;  // of the thread's 8 values
+    uint32_t word;
+};
+
+// Quantises the 8 values of each thread; 1 << lanes_log2 adjacent threads hold a group.
+template <bool kFP16>
+__device__ __forceinline__ Int4Group<kFP16> int4_quantise(uint4 v, int lanes_log2) {
+    constexpr uint32_t kInf = kFP16 ? 0x7c00u : 0x7f80u;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16<kFP16>(w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+    const uint32_t mag = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                  __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+    float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    if (max(mag & 0xffffu, mag >> 16) >= kInf) hi = INFINITY;  // (finite values stay below it)
+    for (int i = 0; i < lanes_log2; ++i) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1 << i));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1 << i));
+    }
+    Int4Group<kFP16> out;
+    if (hi == INFINITY) {
+        out.codes = 0;
+        out.word = 0x7fc00000u;
+        return out;
+    }
+    // (hi - lo) / 15, from sixteenths so that the difference cannot overflow
+    const float t = fmaxf(__fdiv_rn(hi * 0.0625f - lo * 0.0625f, 0.9375f), fmaxf(fabsf(hi), fabsf(lo)) * 0.00048828125f);
+    const float s = __uint_as_float((__float_as_uint(t) + 0xffffu) & 0xffff0000u);
+    float n[8], base;
+    if (s > 8.67361738e-19f) {  // 2^-60: no part of the quotient's steps is below the normal numbers
+        const float inv = __fdiv_rn(1.f, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = int4_grid(x[i], s, inv);
+        base = int4_grid(lo, s, inv);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = s > 0.f ? round_even(__fdiv_rn(x[i], s)) : 0.f;
+        base = s > 0.f ? round_even(__fdiv_rn(lo, s)) : 0.f;
+    }
+    // four codes as the digits of one number below 2^16, read off its place in [2^23, 2^24)
+    uint32_t half[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float sum = 8388608.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sum = fmaf(fminf(n[4 * h + i] - base, 15.f), (float)(1 << (4 * i)), sum);
+        half[h] = __float_as_uint(sum);
+    }
+    out.codes = __byte_perm(half[0], half[1], 0x5410);
+    out.word = __float_as_uint(s) | (ptx::pack_f16x2(0.f - base, 0.f) & 0xffffu);
+    return out;
+}
+
+// A thread stands for 8 adjacent values of one head of K or V and goes through
+// its CTA's rows, four in flight.
+template <bool kFP16, bool kVec>
+__global__ void __launch_bounds__(kInt4Threads) fa_cache_append_int4_kernel(const __grid_constant__ Int4AppendParams p) {
+    __shared__ int s_slot[kInt4MaxRows + kInt4Look];
+    __shared__ int s_late[kInt4MaxRows];  // the slot is written by a later row
+    constexpr int U = 4;
+    const int tid = (int)threadIdx.x;
+    const int per_row = 2 * p.Hkv << (p.d_log2 - 3);
+    const int item = ((int)blockIdx.y << p.items_log2) + (tid & ((1 << p.items_log2) - 1));
+    const int lane_row = tid >> p.items_log2, rows_at_once = kInt4Threads >> p.items_log2;
+    const bool have = item < per_row;
+    const int vec = item & ((1 << (p.d_log2 - 3)) - 1);
+    const int unit = have ? item >> (p.d_log2 - 3) : 0, kv = unit >= p.Hkv ? 1 : 0, head = unit - (kv ? p.Hkv : 0);
+    const int row0 = (int)blockIdx.x * p.rows_per_cta, rows = min(p.rows_per_cta, p.T - row0);
+    const uint16_t *x = p.x[kv] + row0 * p.token_stride[kv] + head * p.head_stride[kv] + vec * 8;
+    ptx::wait_for_previous_kernel();
+    for (int j = tid; j < p.rows_per_cta + kInt4Look; j += kInt4Threads)
+        s_slot[j] = append_slot(p.slot_map, p.slots, p.T, row0 + j);
+    if (tid < kInt4MaxRows) s_late[tid] = 0;
+    uint4 held[U];
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * rows_at_once + lane_row;
+            held[u] = make_uint4(0, 0, 0, 0);
+            if (have && r < rows) held[u] = load8_16<kVec>(x + r * p.token_stride[kv]);
+        }
+    };
+    fetch(0);
+    __syncthreads();
+    for (int i = tid; i < rows * kInt4Look; i += kInt4Threads) {
+        const int r = i / kInt4Look, k = i % kInt4Look;
+        if (k > 0 && s_slot[r] >= 0 && s_slot[r + k] == s_slot[r]) s_late[r] = 1;
+    }
+    __syncthreads();
+    for (int r0 = 0; r0 < rows; r0 += U * rows_at_once) {
+        if (r0 > 0) fetch(r0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r0 + u * rows_at_once >= rows) break;  // (the same in the whole CTA)
+            const int r = r0 + u * rows_at_once + lane_row;
+            const Int4Group<kFP16> q = int4_quantise<kFP16>(held[u], p.g_log2 - 3);
+            if (!have || r >= rows || s_slot[r] < 0 || s_late[r]) continue;
+            const int slot = s_slot[r];
+            const long long at = ((((long long)(slot >> p.bs_log2) * p.Hkv + head) << p.bs_log2) + (slot & ((1 << p.bs_log2) - 1)));
+            reinterpret_cast<uint32_t *>(p.codes[kv])[(at << (p.d_log2 - 3)) + vec] = q.codes;
+            if ((vec & ((1 << (p.g_log2 - 3)) - 1)) == 0)
+                p.words[kv][(at << (p.d_log2 - p.g_log2)) + (vec >> (p.g_log2 - 3))] = q.word;
+        }
+    }
+}
+
+// --------------------------------------------------------------- reading back
+
+struct Int4ReadParams {
+    const uint8_t *codes[2];
+    const uint32_t *words[2];
+    const int *block_table, *seq_lens, *starts;
+    uint16_t *out[2];
+    long long stride[2][3];     // of (request, head, row), in elements
+    int Hkv, rows, max_blocks, num_blocks, d_log2, g_log2, bs_log2;
+    int rows_per_cta, chunks;   // CTAs of a request
+    int items_log2;
+};
+
+// A thread stands for 8 adjacent values of one head of K or V; its rows' table
+// entries, then codes and words, four rows in flight.
+template <bool kFP16, bool kVec>
+__global__ void __launch_bounds__(kInt4Threads) fa_cache_read_int4_kernel(const __grid_constant__ Int4ReadParams p) {
+    constexpr int U = 4;
+    const int tid = (int)threadIdx.x;
+    const int per_row = 2 * p.Hkv << (p.d_log2 - 3);
+    const int item = ((int)blockIdx.y << p.items_log2) + (tid & ((1 << p.items_log2) - 1));
+    const int lane_row = tid >> p.items_log2, rows_at_once = kInt4Threads >> p.items_log2;
+    const int b = (int)blockIdx.x / p.chunks, row0 = ((int)blockIdx.x - b * p.chunks) * p.rows_per_cta;
+    const int vec = item & ((1 << (p.d_log2 - 3)) - 1);
+    const int unit = item >> (p.d_log2 - 3), kv = unit >= p.Hkv ? 1 : 0, head = unit - (kv ? p.Hkv : 0);
+    ptx::wait_for_previous_kernel();
+    if (item >= per_row) return;
+    const long long first = p.starts ? p.starts[b] : 0;
+    const long long len = min(max(p.seq_lens[b], 0), p.max_blocks << p.bs_log2);
+    // rows whose positions lie in [0, len)
+    const int begin = (int)max((long long)row0, -first);
+    const int end = (int)min((long long)min(row0 + p.rows_per_cta, p.rows), len - first);
+    const int *table = p.block_table + (size_t)b * p.max_blocks;
+    uint16_t *out = p.out[kv] + b * p.stride[kv][0] + head * p.stride[kv][1] + vec * 8;
+    const uint32_t *codes = reinterpret_cast<const uint32_t *>(p.codes[kv]) + vec;
+    const uint32_t *words = p.words[kv] + (vec >> (p.g_log2 - 3));
+    for (int r0 = begin + lane_row; r0 < end; r0 += U * rows_at_once) {
+        int entry[U];
+        uint32_t c[U], w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = min(r0 + u * rows_at_once, end - 1);
+            entry[u] = table[(first + r) >> p.bs_log2];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = min(r0 + u * rows_at_once, end - 1);
+            const bool in = entry[u] >= 0 && entry[u] < p.num_blocks;  // (outside the pool: zeros)
+            const long long at = (((long long)(in ? entry[u] : 0) * p.Hkv + head) << p.bs_log2) +
+                                 ((first + r) & ((1 << p.bs_log2) - 1));
+            c[u] = codes[at << (p.d_log2 - 3)];
+            w[u] = words[at << (p.d_log2 - p.g_log2)];
+            if (!in) w[u] = 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * rows_at_once;
+            if (r >= end) break;
+            const float s = __uint_as_float(w[u] & 0xffff0000u);
+            // 2^23 + z: whole, as every step of s (c - z) before the product is
+            const float z = 8388608.f + unpack16<true>(w[u]).x;
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = __uint_as_float(0x4b000000u | ((c[u] >> (8 * i)) & 15u)) - z;
+                const float e = __uint_as_float(0x4b000000u | ((c[u] >> (8 * i + 4)) & 15u)) - z;
+                y[i] = pack2b<kFP16>(s * a, s * e);
+            }
+            uint16_t *dst = out + r * p.stride[kv][2];
+            if constexpr (kVec) {
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dst[2 * i] = (uint16_t)y[i];
+                    dst[2 * i + 1] = (uint16_t)(y[i] >> 16);
+                }
+            }
+        }
+    }
+}
+
+}  // namespace fa

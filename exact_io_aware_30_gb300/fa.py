@@ -1,7 +1,7 @@
 """ctypes binding of libfa.so (include/fa.h) -- argument marshalling only.
 
 Every step of the attention forward, backward and paged decoding, of rotary
-positions and of the paged cache's updates runs inside the library's CUDA
+positions and of the paged cache's updates, writes and reads runs inside the library's CUDA
 kernels; this module checks tensor metadata, allocates
 outputs (and workspaces) with torch and passes raw pointers and sizes through
 the C ABI.  If the library is missing or
@@ -55,7 +55,9 @@ EXPORTS = ("fa_fwd", "fa_fwd_fp16", "fa_fwd_gqa", "fa_fwd_fp8", "fa_bwd", "fa_bw
            "fa_fwd_host", "fa_fwd_host_workspace_query", "fa_set_debug_stall_ms",
            "fa_rope", "fa_rope_frequencies", "fa_paged_update", "fa_paged_update_by_request",
            "fa_cache_append_fp8",
-           "fa_decode_paged_fp8", "fa_decode_fp8_workspace_query")
+           "fa_decode_paged_fp8", "fa_decode_fp8_workspace_query",
+           "fa_cache_append_int4", "fa_cache_read_int4", "fa_decode_paged_int4",
+           "fa_decode_int4_workspace_query")
 
 
 class FAError(RuntimeError):
@@ -145,6 +147,15 @@ def load(path: str | None = None):
             [ctypes.c_float, _i, _i, _vp]
         lib.fa_decode_fp8_workspace_query.restype = _i
         lib.fa_decode_fp8_workspace_query.argtypes = [_i] * 11 + [ctypes.POINTER(ctypes.c_size_t)]
+        lib.fa_cache_append_int4.restype = _i
+        lib.fa_cache_append_int4.argtypes = [_vp, _vp, _ll, _ll, _ll, _ll] + [_vp] * 5 + [_i] * 7 + [_vp]
+        lib.fa_cache_read_int4.restype = _i
+        lib.fa_cache_read_int4.argtypes = [_vp] * 11 + [_i] * 9 + [_vp]
+        lib.fa_decode_paged_int4.restype = _i
+        lib.fa_decode_paged_int4.argtypes = [_vp] * 10 + [ctypes.c_size_t] + [_i] * 10 + \
+            [ctypes.c_float, _i, _i, _vp]
+        lib.fa_decode_int4_workspace_query.restype = _i
+        lib.fa_decode_int4_workspace_query.argtypes = [_i] * 12 + [ctypes.POINTER(ctypes.c_size_t)]
         lib.fa_describe.restype = _i
         lib.fa_describe.argtypes = [_i, _i, _i, ctypes.c_char_p, ctypes.c_size_t]
         lib.fa_get_device_error.restype = _i
@@ -900,4 +911,190 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
         _leave(scope)
     if st:
         _check(st, "fa_decode_paged_fp8")
+    return out, lse
+
+
+# --------------------------------------------------------------- the paged cache in 4 bits
+
+def int4_cache(num_blocks: int, H_kv: int, block_size: int, d: int, group: int = 32, device="cuda"):
+    """An empty 4-bit paged cache: (k_cache, v_cache, k_scale, v_scale), all zeros.
+
+    The caches are uint8 [num_blocks, H_kv, block_size, d / 2], two codes to a
+    byte; the scales int32 words [num_blocks, H_kv, block_size, d / group], a
+    group's scale (bf16) in the high half and its zero (fp16) in the low one.
+    """
+    import torch
+    if d not in (64, 128, 256) or group not in (32, 64) or block_size not in (16, 32, 64, 128):
+        raise FAError(FA_ERR_UNSUPPORTED, "d must be 64, 128 or 256, group 32 or 64, block_size 16, 32, 64 or 128")
+    rows = (int(num_blocks), int(H_kv), int(block_size))
+    return (*(torch.zeros((*rows, d // 2), dtype=torch.uint8, device=device) for _ in range(2)),
+            *(torch.zeros((*rows, d // group), dtype=torch.int32, device=device) for _ in range(2)))
+
+
+def _need_int4_cache(k_cache, v_cache, k_scale, v_scale, dev):
+    """Checks the four tensors of a 4-bit cache; returns (num_blocks, H_kv, block_size, d, group)."""
+    import torch
+    shape, words = k_cache.shape, k_scale.shape
+    if len(shape) != 4 or len(words) != 4:
+        raise FAError(FA_ERR_INVALID_ARG, "the caches must be [num_blocks,H_kv,block_size,d/2], the scales "
+                                          "[num_blocks,H_kv,block_size,d/group]")
+    d = 2 * shape[3]
+    if words[3] < 1 or d % words[3]:
+        raise FAError(FA_ERR_INVALID_ARG, f"{words[3]} scales per row do not divide {d} components into groups")
+    want = (*shape[:3], words[3])
+    _need_tensor("k_cache", k_cache, dev, torch.uint8, shape)
+    _need_tensor("v_cache", v_cache, dev, torch.uint8, shape)
+    _need_tensor("k_scale", k_scale, dev, torch.int32, want)
+    _need_tensor("v_scale", v_scale, dev, torch.int32, want)
+    return shape[0], shape[1], shape[2], d, d // words[3]
+
+
+def cache_append_int4(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
+    """Quantises new K and V rows into a 4-bit paged cache, in place (fa_cache_append_int4).
+
+    k, v [T, H_kv, d] (bf16 or fp16; any strides with the last dimension
+    contiguous); slot_map int32 [T] (negative: the row is skipped); the caches
+    and scales as ``int4_cache`` makes them.
+    """
+    import torch
+    if not k.is_cuda or k.dim() != 3:
+        raise FAError(FA_ERR_INVALID_ARG, "k must be a CUDA tensor [T,H_kv,d]")
+    dev = k.device
+    dt = _dtype_code(k)
+    T, Hkv, d = k.shape
+    _need_tensor("v", v, dev, k.dtype, k.shape, contiguous=False)
+    nb, hc, bs, dc, group = _need_int4_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if (hc, dc) != (Hkv, d):
+        raise FAError(FA_ERR_INVALID_ARG, "the caches' heads and components must be those of k")
+    if k.numel() and (k.stride(2) != 1 or v.stride(2) != 1):
+        raise FAError(FA_ERR_INVALID_ARG, "k and v: the last dimension must be contiguous")
+    _need_tensor("slot_map", slot_map, dev, torch.int32, (T,))
+    sp, scope = _enter(dev, stream)
+    try:
+        st = (_lib or load()).fa_cache_append_int4(
+            k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+            slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), T, Hkv, d, group, bs, nb, dt, sp)
+    finally:
+        _leave(scope)
+    _check(st, "fa_cache_append_int4")
+
+
+def cache_read_int4(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, rows: int, starts=None,
+                    dtype=None, out_k=None, out_v=None, stream=None):
+    """Reads rows of a 4-bit paged cache back in 16 bits (fa_cache_read_int4).
+
+    Row i of request b is its token ``starts[b] + i`` (starts int32 [B]; None: 0),
+    i < rows.  Returns (k, v) [B, H_kv, rows, d], as ``forward`` takes them.
+    Rows without a token are zeros, or stay as they were in ``out_k`` and
+    ``out_v`` (bf16 or fp16; any strides with the last dimension contiguous;
+    both or none).  ``dtype`` is the outputs' where they are not given (bf16).
+    """
+    import torch
+    if not k_cache.is_cuda or block_table.dim() != 2:
+        raise FAError(FA_ERR_INVALID_ARG, "the caches must be CUDA tensors, block_table [B,max_blocks]")
+    dev = k_cache.device
+    nb, Hkv, bs, d, group = _need_int4_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    B, mb = block_table.shape
+    rows = int(rows)
+    if rows < 0 or (out_k is None) != (out_v is None):
+        raise FAError(FA_ERR_INVALID_ARG, "rows must be >= 0, and out_k and out_v given both or not at all")
+    _need_tensor("block_table", block_table, dev, torch.int32, (B, mb))
+    _need_tensor("seq_lens", seq_lens, dev, torch.int32, (B,))
+    if starts is not None:
+        _need_tensor("starts", starts, dev, torch.int32, (B,))
+    shape = (B, Hkv, rows, d)
+    sp, scope = _enter(dev, stream)
+    try:
+        if out_k is None:
+            dtype = dtype or torch.bfloat16
+            out_k, out_v = (torch.zeros(shape, dtype=dtype, device=dev) for _ in range(2))
+        dt = _dtype_code(out_k)
+        if dtype is not None and out_k.dtype != dtype:
+            raise FAError(FA_ERR_INVALID_ARG, f"out_k is {out_k.dtype}, dtype {dtype}")
+        _need_tensor("out_k", out_k, dev, out_k.dtype, shape, contiguous=False)
+        _need_tensor("out_v", out_v, dev, out_k.dtype, shape, contiguous=False)
+        if rows and B and (out_k.stride(3) != 1 or out_v.stride(3) != 1):
+            raise FAError(FA_ERR_INVALID_ARG, "out_k and out_v: the last dimension must be contiguous")
+        st = (_lib or load()).fa_cache_read_int4(
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), None if starts is None else starts.data_ptr(),
+            out_k.data_ptr(), _longs(out_k.stride()[:3]), out_v.data_ptr(), _longs(out_v.stride()[:3]),
+            B, Hkv, rows, d, group, bs, mb, nb, dt, sp)
+    finally:
+        _leave(scope)
+    _check(st, "fa_cache_read_int4")
+    return out_k, out_v
+
+
+def decode_int4_workspace_query(B, H, H_kv, Sq, d, group, block_size, max_blocks, num_blocks, max_seq_len,
+                                mask="none", dtype=DTYPE_BF16):
+    """(status, bytes) of fa_decode_int4_workspace_query."""
+    n = ctypes.c_size_t(12345)
+    st = load().fa_decode_int4_workspace_query(int(B), int(H), int(H_kv), int(Sq), int(d), int(group),
+                                               int(block_size), int(max_blocks), int(num_blocks),
+                                               int(max_seq_len), mask_code(mask), int(dtype), ctypes.byref(n))
+    return st, n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_int4_workspace(device_index, *sizes):
+    """Workspace bytes for these sizes on this device (the current one); refusals are not kept."""
+    n = ctypes.c_size_t(0)
+    _check(load().fa_decode_int4_workspace_query(*sizes, ctypes.byref(n)), "fa_decode_int4_workspace_query")
+    return n.value
+
+
+def decode_paged_int4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, max_seq_len: int,
+                      scale: float | None = None, mask="none", out=None, lse=None, workspace=None,
+                      stream=None):
+    """Attention of q's new rows over a 4-bit paged cache (fa_decode_paged_int4).
+
+    q [B, H, Sq, d] bf16 or fp16; the caches and scales as ``cache_append_int4``
+    writes them; block_table int32 [B, max_blocks], seq_lens int32 [B] (0
+    allowed: the row's output is 0 and its lse -inf).  Returns (o, lse).
+    """
+    import torch
+    q_shape, t_shape = q.shape, block_table.shape
+    if not q.is_cuda or len(q_shape) != 4 or not q.is_contiguous() or len(t_shape) != 2:
+        raise FAError(FA_ERR_INVALID_ARG, "q must be a contiguous CUDA tensor [B,H,Sq,d], block_table [B,max_blocks]")
+    dev = q.device
+    dt = _dtype_code(q)
+    B, H, Sq, d = q_shape
+    nb, Hkv, bs, dc, group = _need_int4_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if dc != d:
+        raise FAError(FA_ERR_INVALID_ARG, f"the caches hold rows of {dc} components, q of {d}")
+    mb = t_shape[1]
+    _need_tensor("block_table", block_table, dev, torch.int32, (B, mb))
+    _need_tensor("seq_lens", seq_lens, dev, torch.int32, (B,))
+    mk = mask_code(mask)
+    if scale is None:
+        scale = d ** -0.5
+    max_seq_len = int(max_seq_len)
+    sp, scope = _enter(dev, stream)
+    try:
+        if workspace is None:
+            ws_bytes = _decode_int4_workspace(dev.index, B, H, Hkv, Sq, d, group, bs, mb, nb, max_seq_len, mk, dt)
+            if ws_bytes:
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        else:
+            _need_tensor("workspace", workspace, dev, torch.uint8, workspace.shape)
+            ws_bytes = workspace.numel()
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _need_tensor("out", out, dev, q.dtype, q_shape)
+        if lse is None:
+            lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
+        else:
+            _need_tensor("lse", lse, dev, torch.float32, (B, H, Sq))
+        st = (_lib or load()).fa_decode_paged_int4(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr() if ws_bytes else None, ws_bytes, B, H, Hkv, Sq, d, group, bs, mb, nb,
+            max_seq_len, scale, mk, dt, sp)
+    finally:
+        _leave(scope)
+    if st:
+        _check(st, "fa_decode_paged_int4")
     return out, lse

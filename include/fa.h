@@ -489,6 +489,114 @@ fa_status fa_decode_fp8_workspace_query(int B, int H, int H_kv, int Sq, int d, i
                                         int dtype, size_t *bytes);
 
 /*
+ * The paged cache in 4 bits.  A cached row of d components is in groups of
+ * `group` (32 or 64) adjacent ones: codes c = 0 .. 15, two to a byte (component
+ * 2i in the low half of byte i), and one 32-bit word per group: the scale s >= 0
+ * (bf16) in its high half, the zero z (a whole number, |z| <= 2048, in fp16) in
+ * its low half.  The value of a code is s (c - z).
+ *   k_cache, v_cache  [num_blocks, H_kv, block_size, d / 2] bytes of codes
+ *   k_scale, v_scale  [num_blocks, H_kv, block_size, d / group] words
+ * all 16-byte aligned; d 64, 128 or 256; block_size 16, 32, 64 or 128.  Blocks,
+ * tables and slots are those of fa_paged_update.  (0.625 bytes per value with
+ * groups of 32, 0.5625 with 64.)
+ */
+
+/*
+ * fa_cache_append_int4 -- writes new K and V rows into a 4-bit paged cache.  Per
+ * group of values x_i of a row, lo and hi the smallest and largest of them:
+ *     t   = max((hi - lo) / 15, max |x| / 2048), in fp32 (the difference and
+ *           the quotient rounded to nearest), s = t rounded up to bf16
+ *     n_i = x_i / s to the nearest whole number, ties to even
+ *     c_i = min(n_i - min n, 15), z = -min n
+ * so that a value is off by at most s / 2.  All zero: s, c and z are 0.  A group
+ * with an infinity or NaN: s is NaN, c and z are 0.
+ *
+ *   k, v        [T, H_kv, d] 16-bit by element strides (token, head); values
+ *               of a head adjacent; the strides are >= 0; T <= 2^30, H_kv <=
+ *               65535
+ *   slot_map    device int32 [T]: row t goes to slot s = block * block_size +
+ *               place; rows whose slot is outside [0, num_blocks * block_size)
+ *               are skipped.  Rows may stand in any order.  A slot named twice
+ *               gets the later row where the two are less than 128 rows apart;
+ *               farther apart, each of its groups is undefined
+ *   dtype       FA_DTYPE_BF16 or FA_DTYPE_FP16 (k and v)
+ * Slots without a row are left as they were.  T == 0: FA_OK.  Outputs may not
+ * overlap inputs or each other.  One launch; no workspace.
+ */
+fa_status fa_cache_append_int4(const void *k, const void *v, long long k_token_stride,
+                               long long k_head_stride, long long v_token_stride, long long v_head_stride,
+                               const int *slot_map, void *k_cache, void *v_cache, unsigned *k_scale,
+                               unsigned *v_scale, int T, int H_kv, int d, int group, int block_size,
+                               int num_blocks, int dtype, fa_stream_t stream);
+
+/*
+ * fa_cache_read_int4 -- reads cached rows back in 16 bits, as the forward takes
+ * K and V: row i of request b is its token starts[b] + i, each value s (c - z)
+ * rounded once.
+ *
+ *   seq_lens    device int32 [B] (values outside [0, max_blocks * block_size]
+ *               are clamped into it)
+ *   starts      device int32 [B], or NULL: all 0
+ *   k_out, v_out  [B, H_kv, rows, d] by element strides (batch, head, row) in
+ *               host arrays of three, >= 0; every element must have an address
+ *               of its own.  Rows whose token is below 0 or not below the
+ *               request's length are left as they were
+ *   block_table device int32 [B, max_blocks]; an entry outside [0, num_blocks)
+ *               reads zeros
+ *   dtype       FA_DTYPE_BF16 or FA_DTYPE_FP16 (k_out and v_out)
+ * rows == 0: FA_OK.  Outputs may not overlap inputs or each other.  One launch;
+ * no workspace.
+ */
+fa_status fa_cache_read_int4(const void *k_cache, const void *v_cache, const unsigned *k_scale,
+                             const unsigned *v_scale, const int *block_table, const int *seq_lens,
+                             const int *starts, void *k_out, const long long *k_strides, void *v_out,
+                             const long long *v_strides, int B, int H_kv, int rows, int d, int group,
+                             int block_size, int max_blocks, int num_blocks, int dtype, fa_stream_t stream);
+
+/*
+ * fa_decode_paged_int4 -- fa_decode_paged over a 4-bit cache: exact softmax
+ * attention over the values of its codes, q and o in 16 bits.  q enters exactly,
+ * but for components below 2^-24 of their row's largest: those may be off by
+ * 2^-34 of that.  A weight times its group's V scale is rounded to 11 bits before
+ * P V, and to no finer than 2^-25 of about the largest such product of the row
+ * (the groups' scales taken relative to each group's usual one).  Sums are
+ * fp32.  Deterministic.  Two launches at most; the workspace's contents on entry
+ * do not matter.  Arguments as for fa_decode_paged, except:
+ *
+ *   k_cache, v_cache, k_scale, v_scale, group  as above; scales finite and >= 0
+ *                or NaN
+ *   q            components below 2^112 in size; a row with a larger one, an
+ *                infinity or NaN gives NaN
+ *   seq_lens     any length in [0, max_seq_len] (values outside are clamped
+ *                into it).  A row that sees no key -- length 0, or with
+ *                FA_MASK_CAUSAL a row in front of the request's first token --
+ *                gets O = 0 and lse = -inf
+ *   block_table  an entry outside [0, num_blocks) reads zeros
+ *   workspace    at least fa_decode_int4_workspace_query() bytes, 256-byte
+ *                aligned (may be NULL where that is 0); calls that may overlap
+ *                in time need one each
+ *   max_seq_len  at most 2^31 - 513
+ * Slots past a request's length may hold anything.  A NaN scale of V within the
+ * length makes its group's columns NaN in all rows of the request and K/V head,
+ * also in those that FA_MASK_CAUSAL hides it from (a weight of 0 times NaN).
+ */
+fa_status fa_decode_paged_int4(const void *q, const void *k_cache, const void *v_cache,
+                               const unsigned *k_scale, const unsigned *v_scale, const int *block_table,
+                               const int *seq_lens, void *o, float *lse, void *workspace,
+                               size_t workspace_bytes, int B, int H, int H_kv, int Sq, int d, int group,
+                               int block_size, int max_blocks, int num_blocks, int max_seq_len,
+                               float scale, int mask_kind, int dtype, fa_stream_t stream);
+
+/*
+ * fa_decode_int4_workspace_query -- workspace bytes fa_decode_paged_int4 needs
+ * on the current device and the status it would return for these sizes.
+ * bytes must be non-NULL; it is 0 whenever the status is not FA_OK.
+ */
+fa_status fa_decode_int4_workspace_query(int B, int H, int H_kv, int Sq, int d, int group,
+                                         int block_size, int max_blocks, int num_blocks,
+                                         int max_seq_len, int mask_kind, int dtype, size_t *bytes);
+
+/*
  * fa_fwd_host -- the forward end to end from host memory: Q, K, V are
  * copied into a device workspace, the fused forward of fa_fwd_gqa runs there,
  * and O and lse are copied back to host memory.  The arithmetic and the
