@@ -215,19 +215,6 @@ bool make_map_int4_codes(CUtensorMap *m, const void *base, int d, int bs, int Hk
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The words of a block and head lie in a row: box {at most 256 of them, 1, 1, 1}.
-bool make_map_int4_words(CUtensorMap *m, const void *base, int words, int Hkv, int num_blocks) {
-    auto enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[4] = {(cuuint64_t)words, (cuuint64_t)Hkv, (cuuint64_t)num_blocks, 1};
-    cuuint64_t strides[3] = {(cuuint64_t)words * 4, (cuuint64_t)words * 4 * Hkv, (cuuint64_t)words * 4 * Hkv * num_blocks};
-    cuuint32_t box[4] = {(cuuint32_t)std::min(words, 256), 1, 1, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Rows of a K/V head: at most 8 (a warp's columns), 16, or 32 in equal chunks of
 // at most that, the cache being read once more per chunk.
 DecFp8Plan plan_decode_int4(int B, int Hkv, int R, int d, int max_seq_len, int num_sms) {
@@ -310,14 +297,13 @@ fa_status decode_int4_impl(const void *q, const void *k_cache, const void *v_cac
 
     DecInt4Params p;
     std::memset(&p, 0, sizeof(p));
-    const int block_words = block_size * (d / group);
     if (!make_map_int4_codes(&p.tm_k, k_cache, d, block_size, Hkv, num_blocks) ||
-        !make_map_int4_codes(&p.tm_v, v_cache, d, block_size, Hkv, num_blocks) ||
-        !make_map_int4_words(&p.tm_kw, k_scale, block_words, Hkv, num_blocks) ||
-        !make_map_int4_words(&p.tm_vw, v_scale, block_words, Hkv, num_blocks))
+        !make_map_int4_codes(&p.tm_v, v_cache, d, block_size, Hkv, num_blocks))
         return FA_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.q = static_cast<const uint16_t *>(q);
+    p.k_words = k_scale;
+    p.v_words = v_scale;
     p.block_table = block_table;
     p.seq_lens = seq_lens;
     p.o = o;

@@ -34,11 +34,12 @@
 // whole warp that rescales what it has summed.
 //
 // Work split: the line of 128-key tiles of fa_decode_fp8_kernel.cuh, an even
-// share of it per CTA, cut units merged by its second kernel.  One CTA: a TMA
-// warp fills a ring of tiles, K and V codes and words; eight warps take 16 keys
-// of a tile each (or fewer warps more keys, the others other rows), each with a
-// running maximum and sums of its own, so that nothing is exchanged before the
-// unit's end.
+// share of it per CTA, cut units merged by its second kernel.  One CTA: a ring of
+// tiles, K and V codes and words, that its eight warps take turns at filling; a
+// warp takes 16 keys of a tile (or fewer warps more keys, the others other rows)
+// and has a running maximum and sums of its own, so that nothing is exchanged
+// before the unit's end.  (With a ninth warp for the copies two CTAs' warps get 96
+// registers instead of 128.)
 #pragma once
 
 #include <math.h>
@@ -50,7 +51,7 @@
 namespace fa {
 
 struct DecInt4Params : DecFp8Params {  // (k_scale and v_scale are not used)
-    CUtensorMap tm_kw, tm_vw;  // words, [num_blocks, Hkv, bs * d / G] 32-bit, box {min(bs * d / G, 256), 1, 1, 1}
+    const uint32_t *k_words, *v_words;  // [num_blocks, Hkv, bs, d / G]
     int fp16;
 };
 
@@ -61,7 +62,7 @@ struct DecI4Cfg {
     static constexpr int NT = NT_;                // eights of rows per warp
     static constexpr int RG = RG_;                // groups of warps with different rows
     static constexpr int RC = 8 * NT * RG;        // rows per unit
-    static constexpr int WARPS = 8;               // of the products
+    static constexpr int WARPS = 8;
     static constexpr int KW = WARPS / RG;         // warps along a tile's keys
     static constexpr int KPW = 8 / KW;            // 16-key steps per warp and tile
     static constexpr int BN = 128;
@@ -70,9 +71,9 @@ struct DecI4Cfg {
     static constexpr int ROW = D / 2;             // bytes of a row of codes
     static constexpr int TILE = BN * ROW;
     static constexpr int WORDS = BN * NG * 4;     // bytes of a tile's words
-    static constexpr int WTILE = WORDS < 1024 ? 1024 : WORDS;  // (a box begins on 128 bytes)
     static constexpr int Q_BYTES = RC * D * 2;
-    static constexpr int STAGE = (2 * TILE + 2 * WTILE + Q_BYTES + 1023) / 1024 * 1024;
+    static constexpr int O_V = TILE, O_KW = 2 * TILE, O_VW = O_KW + WORDS, O_Q = O_VW + WORDS;  // places in a stage
+    static constexpr int STAGE = (O_Q + Q_BYTES + 1023) / 1024 * 1024;
     static constexpr int OROW = D + 4;            // floats of a partial row: no two lanes of a store on a bank
     static constexpr int SCRATCH = WARPS * 8 * NT * OROW * 4;
     static constexpr int CTAS_PER_SM = D <= 128 && NT == 1 && RG == 1 ? 2 : 1;
@@ -80,9 +81,9 @@ struct DecI4Cfg {
     static constexpr int FIXED = 1024 + SCRATCH + 2 * WARPS * 8 * NT * 4 + 256;
     static constexpr int FIT = (BUDGET - FIXED) / STAGE;
     static constexpr int ST = FIT < 8 ? FIT : 8;
-    static_assert(ST >= 2, "a ring of at least two tiles");
+    static_assert(ST >= 2 && ST <= WARPS, "a ring of at least two tiles, a warp to begin each");
     static constexpr int SMEM_BYTES = FIXED + ST * STAGE;
-    static constexpr int NUM_THREADS = 32 * (WARPS + 1);
+    static constexpr int NUM_THREADS = 32 * WARPS;
     static constexpr int B_FULL = 0;
     static constexpr int B_EMPTY = ST;
     static constexpr int B_NEVER = 2 * ST;
@@ -90,63 +91,54 @@ struct DecI4Cfg {
     static_assert(NUM_BARS * 8 + 32 <= 256, "layout");
 };
 
-// ------------------------------------------------------------------- TMA
+// ------------------------------------------------------------------- copies
 
+// Lane 4k + j copies part j (K codes, V codes, K words, V words) of block k of
+// a tile; its table entry, or -1 where it has none to copy, -2 where the entry is
+// outside the pool.
 template <class C>
-__device__ void dec_i4_tma_role(const DecInt4Params &p, DecFp8It it, uint8_t *ring, uint32_t bars, Ctl *ctl) {
-    const int lane = (int)ptx::lane_id();
-    const uint64_t pol = p.chunks > 1 ? ptx::policy_evict_last() : ptx::policy_evict_first();
-    const bool mine = lane < C::BN >> p.bs_log2;  // a lane per block of the tile
-    const uint32_t code_dst = (uint32_t)(lane << p.bs_log2) * C::ROW;
-    const int block_words = C::NG << p.bs_log2;
-    const uint32_t word_dst = (uint32_t)lane * (uint32_t)max(block_words * 4, 128);
-    // hidden blocks, and entries outside the pool, are a coordinate outside the
-    // tensor, which reads zeros
-    auto look_up = [&](const DecFp8It &i) -> int {
-        const int n = ((i.tile * C::BN) >> p.bs_log2) + lane;
-        if (!mine || i.left <= 0 || (n << p.bs_log2) >= i.L) return p.num_blocks;
-        const int e = p.block_table[(size_t)i.b * p.max_blocks + n];
-        return e >= 0 && e < p.num_blocks ? e : p.num_blocks;
-    };
-    int n_loaded = 0;
-    bool begins = true;
-    int phys = look_up(it);
-    for (int t = 0; it.left > 0; ++t) {
-        const DecFp8It now = it;
-        dec_fp8_step(p, it);
-        const int next = look_up(it);
-        const int slot = t % C::ST;
-        if (!wait_warp_backoff(bar_addr(bars, C::B_EMPTY + slot), ((t / C::ST) & 1) ^ 1, ctl, 91)) break;
-        const uint32_t base = ptx::smem_addr(ring + slot * C::STAGE), bar = bar_addr(bars, C::B_FULL + slot);
-        if (lane == 0) {
-            uint32_t bytes = 2 * C::TILE + 2 * C::WORDS;
-            int rows = 0;
-            size_t row0 = 0;
-            if (begins) {
-                row0 = dec_fp8_row0(p, now.b, now.kvh, now.chunk, &rows);
-                bytes += (uint32_t)rows * C::D * 2;
-            }
-            ptx::mbar_arrive_expect_tx(bar, bytes);
-            if (begins) ptx::bulk_load(base + 2 * C::TILE + 2 * C::WTILE, p.q + row0 * C::D, (uint32_t)rows * C::D * 2, bar);
-        }
-        __syncwarp();
-        if (mine) {
-            ptx::tma_load_4d(base + code_dst, &p.tm_k, bar, 0, 0, now.kvh, phys, pol);
-            for (int w = 0; w < block_words; w += 256)
-                ptx::tma_load_4d(base + 2 * C::TILE + word_dst + w * 4, &p.tm_kw, bar, w, now.kvh, phys, 0, pol);
-            ptx::tma_load_4d(base + C::TILE + code_dst, &p.tm_v, bar, 0, 0, now.kvh, phys, pol);
-            for (int w = 0; w < block_words; w += 256)
-                ptx::tma_load_4d(base + 2 * C::TILE + C::WTILE + word_dst + w * 4, &p.tm_vw, bar, w, now.kvh, phys, 0, pol);
-        }
-        __syncwarp();
-        ++n_loaded;
-        phys = next;
-        begins = it.tile == 0;
+__device__ __forceinline__ int dec_i4_entry(const DecInt4Params &p, const DecFp8It &it) {
+    const int blk = (int)ptx::lane_id() >> 2, n = ((it.tile * C::BN) >> p.bs_log2) + blk;
+    if (blk >= C::BN >> p.bs_log2 || it.left <= 0 || (n << p.bs_log2) >= it.L) return -1;
+    const int e = p.block_table[(size_t)it.b * p.max_blocks + n];
+    return e >= 0 && e < p.num_blocks ? e : -2;
+}
+
+// Copies a tile (and q's rows, where it begins a unit here) into a stage that is
+// free.  The whole warp.  Slots behind the request's blocks are not read later;
+// a block outside the pool gets zero words, whatever its codes.
+template <class C>
+__device__ __forceinline__ void dec_i4_copy(const DecInt4Params &p, const DecFp8It &it, int entry, bool begins, uint32_t stage,
+                                            uint32_t bar, uint64_t pol) {
+    const int lane = (int)ptx::lane_id(), part = lane & 3, row = (lane >> 2) << p.bs_log2;
+    const uint32_t word_bytes = (uint32_t)(C::NG * 4) << p.bs_log2;
+    const uint32_t words_at = stage + (part & 1 ? C::O_VW : C::O_KW) + row * C::NG * 4;
+    if (entry == -2 && part >= 2) {
+        for (uint32_t i = 0; i < word_bytes; i += 16) ptx::st_shared_v4(words_at + i, 0u, 0u, 0u, 0u);
+        ptx::fence_proxy_async_smem();
     }
-    // the CTA's memory stays until its last copies have landed, also where the
-    // others gave up waiting for them
-    for (int t = n_loaded - C::ST > 0 ? n_loaded - C::ST : 0; t < n_loaded; ++t)
-        wait_bar_drain(bar_addr(bars, C::B_FULL + t % C::ST), (t / C::ST) & 1);
+    const uint32_t blocks = (uint32_t)__popc(__ballot_sync(0xffffffffu, entry >= 0)) / 4;
+    if (lane == 0) {
+        uint32_t bytes = blocks * (2 * word_bytes + ((uint32_t)(2 * C::ROW) << p.bs_log2));
+        int rows = 0;
+        size_t row0 = 0;
+        if (begins) {
+            row0 = dec_fp8_row0(p, it.b, it.kvh, it.chunk, &rows);
+            bytes += (uint32_t)rows * C::D * 2;
+        }
+        ptx::mbar_arrive_expect_tx(bar, bytes);
+        if (begins) ptx::bulk_load(stage + C::O_Q, p.q + row0 * C::D, (uint32_t)rows * C::D * 2, bar);
+    }
+    __syncwarp();
+    if (entry >= 0) {
+        if (part < 2) {
+            ptx::tma_load_4d(stage + (part ? C::O_V : 0) + row * C::ROW, part ? &p.tm_v : &p.tm_k, bar, 0, 0, it.kvh, entry, pol);
+        } else {
+            const size_t at = (((size_t)entry * p.Hkv + it.kvh) << p.bs_log2) * C::NG;
+            ptx::bulk_load(words_at, (part & 1 ? p.v_words : p.k_words) + at, word_bytes, bar);
+        }
+    }
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------- products
@@ -632,31 +624,56 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
 }
 
 template <class C>
-__device__ void dec_i4_product_role(const DecInt4Params &p, DecFp8It it, uint8_t *ring, float *scratch, float *ml,
-                                    uint32_t bars, Ctl *ctl) {
+__device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint8_t *ring, float *scratch, float *ml, uint32_t bars,
+                            int *copied, Ctl *ctl) {
     const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5, rg = warp / C::KW, kwi = warp % C::KW;
+    const uint64_t pol = p.chunks > 1 ? ptx::policy_evict_last() : ptx::policy_evict_first();
+    const uint32_t ring_addr = ptx::smem_addr(ring);
+    // The warps take turns at the copies: tile n is copied by warp n of the first
+    // ST - 1 and by the warp whose turn tile n - ST + 1 is, behind its own keys of
+    // that one; the stage's last readers were busy with the tile in front.
+    DecFp8It ahead = it;
+    for (int n = 0; n < C::ST - 1 && ahead.left > 0; ++n) {
+        if (warp == n) {
+            if (lane == 0) atomicMax(copied, n + 1);
+            dec_i4_copy<C>(p, ahead, dec_i4_entry<C>(p, ahead), n == 0 || ahead.tile == 0, ring_addr + n * C::STAGE,
+                           bar_addr(bars, C::B_FULL + n), pol);
+        }
+        dec_fp8_step(p, ahead);
+    }
     DecI4Warp<C> w;
     bool begins = true, begun_here = it.tile == 0, bad = false;
-    const int word_block = max(C::NG << (p.bs_log2 + 2), 128);  // bytes of a block's words in a tile
+    int slot = 0, prev = C::ST - 1;  // the stages of this tile and of the one in front
+    uint32_t phase = 0, prev_phase = 1;
     for (int t = 0; it.left > 0; ++t) {
-        const int slot = t % C::ST;
+        const bool turn = (t & (C::WARPS - 1)) == warp && ahead.left > 0;
+        int entry = -1;
+        if (turn) entry = dec_i4_entry<C>(p, ahead);
         // (a warp whose wait ran out goes on without its tiles, so that the others meet it at the units' ends)
-        if (!bad) bad = !wait_warp(bar_addr(bars, p.stall_test && t == 0 ? C::B_NEVER : C::B_FULL + slot), (t / C::ST) & 1, ctl, 92);
+        if (!bad) bad = !wait_warp(bar_addr(bars, p.stall_test && t == 0 ? C::B_NEVER : C::B_FULL + slot), phase, ctl, 92);
         const uint8_t *stage = ring + slot * C::STAGE;
-        if (begins) dec_i4_begin_unit<C>(p, it, reinterpret_cast<const uint16_t *>(stage + 2 * C::TILE + 2 * C::WTILE), rg, w);
+        if (begins) dec_i4_begin_unit<C>(p, it, reinterpret_cast<const uint16_t *>(stage + C::O_Q), rg, w);
         begins = false;
         const int seen_by_all = p.mask_kind == kMaskCausal ? it.L - p.Sq : it.L - 1;
 #pragma unroll 1
         for (int j = 0; j < C::KPW; ++j) {
             const int at = (kwi * C::KPW + j) * 16, key = it.tile * C::BN + at;
             if (bad || key >= it.L) break;
-            const uint32_t base = ptx::smem_addr(stage);
-            const uint32_t words = (uint32_t)((at >> p.bs_log2) * word_block + (at & ((1 << p.bs_log2) - 1)) * C::NG * 4);
-            dec_i4_keys<C>(p, w, key, it.L, seen_by_all, base + at * C::ROW, base + C::TILE + at * C::ROW,
-                           base + 2 * C::TILE + words, base + 2 * C::TILE + C::WTILE + words);
+            const uint32_t base = ring_addr + slot * C::STAGE;
+            dec_i4_keys<C>(p, w, key, it.L, seen_by_all, base + at * C::ROW, base + C::O_V + at * C::ROW,
+                           base + C::O_KW + at * C::NG * 4, base + C::O_VW + at * C::NG * 4);
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_addr(bars, C::B_EMPTY + slot));
+        if (turn && !bad) {
+            // tile t + ST - 1 goes where tile t - 1 was
+            bad = t > 0 && !wait_warp(bar_addr(bars, C::B_EMPTY + prev), prev_phase, ctl, 91);
+            if (!bad) {
+                if (lane == 0) atomicMax(copied, t + C::ST);
+                dec_i4_copy<C>(p, ahead, entry, ahead.tile == 0, ring_addr + prev * C::STAGE, bar_addr(bars, C::B_FULL + prev), pol);
+            }
+        }
+        if (ahead.left > 0) dec_fp8_step(p, ahead);
         const bool ends = it.tile + 1 == it.nt;
         if (ends || it.left == 1) {
             dec_i4_end_unit<C>(p, it, w, rg, kwi, begun_here && ends, begun_here, scratch, ml);
@@ -664,6 +681,9 @@ __device__ void dec_i4_product_role(const DecInt4Params &p, DecFp8It it, uint8_t
             begun_here = true;
         }
         dec_fp8_step(p, it);
+        prev = slot;
+        prev_phase = phase;
+        if (++slot == C::ST) slot = 0, phase ^= 1;
     }
 }
 
@@ -677,8 +697,8 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     float *ml = scratch + C::SCRATCH / 4;
     uint64_t *bar_mem = reinterpret_cast<uint64_t *>(ml + 2 * C::WARPS * 8 * C::NT);
     Ctl *ctl = reinterpret_cast<Ctl *>(bar_mem + C::NUM_BARS);
+    int *copied = reinterpret_cast<int *>(ctl + 1);  // tiles that copies were begun for
     const uint32_t bars = ptx::smem_addr(bar_mem);
-    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::ST; ++s) {
             ptx::mbar_init(bar_addr(bars, C::B_FULL + s), 1);
@@ -687,22 +707,26 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
         ptx::mbar_init(bar_addr(bars, C::B_NEVER), 1);
         ctl->abort = 0;
         ctl->limit_ns = p.wait_limit_ns;
+        *copied = 0;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
-    }
-    if (warp == C::WARPS && ptx::lane_id() == 0) {
         ptx::prefetch_tensormap(&p.tm_k);
         ptx::prefetch_tensormap(&p.tm_v);
-        ptx::prefetch_tensormap(&p.tm_kw);
-        ptx::prefetch_tensormap(&p.tm_vw);
     }
     ptx::wait_for_previous_kernel();
     const DecFp8It it = dec_fp8_begin<C::NUM_THREADS>(p, reinterpret_cast<long long *>(scratch));
     __syncthreads();
     // the merge may be set up now; it waits for this grid's end before it reads
     ptx::let_next_kernel_begin();
-    if (warp < C::WARPS) dec_i4_product_role<C>(p, it, ring, scratch, ml, bars, ctl);
-    else dec_i4_tma_role<C>(p, it, ring, bars, ctl);
+    dec_i4_warp<C>(p, it, ring, scratch, ml, bars, copied, ctl);
+    __syncthreads();
+    // the CTA's memory stays until its last copies have landed, also where the
+    // warps gave up waiting for them
+    if (ctl->abort && threadIdx.x == 0) {
+        const int n = *copied;
+        for (int t = n - C::ST > 0 ? n - C::ST : 0; t < n; ++t)
+            wait_bar_drain(bar_addr(bars, C::B_FULL + t % C::ST), (t / C::ST) & 1);
+    }
 }
 
 }  // namespace fa
