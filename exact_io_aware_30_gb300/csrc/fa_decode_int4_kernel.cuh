@@ -64,21 +64,20 @@ struct DecI4Cfg {
     static constexpr int RC = 8 * NT * RG;        // rows per unit
     static constexpr int WARPS = 8;
     static constexpr int KW = WARPS / RG;         // warps along a tile's keys
-    static constexpr int KPW = 8 / KW;            // 16-key steps per warp and tile
+    static constexpr int SPT = 8 / KW;            // steps of 16 keys of a warp per tile
     static constexpr int BN = 128;
     static constexpr int NG = D / G;
     static constexpr int NC = D / 32;             // chunks of 32 components, 16 bytes
     static constexpr int ROW = D / 2;             // bytes of a row of codes
     static constexpr int TILE = BN * ROW;
     static constexpr int WORDS = BN * NG * 4;     // bytes of a tile's words
-    static constexpr int Q_BYTES = RC * D * 2;
-    static constexpr int O_V = TILE, O_KW = 2 * TILE, O_VW = O_KW + WORDS, O_Q = O_VW + WORDS;  // places in a stage
-    static constexpr int STAGE = (O_Q + Q_BYTES + 1023) / 1024 * 1024;
-    static constexpr int OROW = D + 4;            // floats of a partial row: no two lanes of a store on a bank
-    static constexpr int SCRATCH = WARPS * 8 * NT * OROW * 4;
-    static constexpr int CTAS_PER_SM = D <= 128 && NT == 1 && RG == 1 ? 2 : 1;
-    static constexpr int BUDGET = CTAS_PER_SM == 2 ? 113 * 1024 : 226 * 1024;
-    static constexpr int FIXED = 1024 + SCRATCH + 2 * WARPS * 8 * NT * 4 + 256;
+    static constexpr int O_V = TILE, O_KW = 2 * TILE, O_VW = O_KW + WORDS;  // places in a stage
+    static constexpr int STAGE = (O_VW + WORDS + 1023) / 1024 * 1024;
+    static constexpr int PART = (2 * NT * NC + NT) * 512;  // a warp's sums, on their way to another's
+    static constexpr int PARTS = WARPS / 2;
+    static constexpr int CTAS_PER_SM = D <= 128 && NT == 1 ? 2 : 1;
+    static constexpr int BUDGET = (227 / CTAS_PER_SM - 1) * 1024;
+    static constexpr int FIXED = 1024 + PARTS * PART + 512;
     static constexpr int FIT = (BUDGET - FIXED) / STAGE;
     static constexpr int ST = FIT < 8 ? FIT : 8;
     static_assert(ST >= 2 && ST <= WARPS, "a ring of at least two tiles, a warp to begin each");
@@ -86,31 +85,64 @@ struct DecI4Cfg {
     static constexpr int NUM_THREADS = 32 * WARPS;
     static constexpr int B_FULL = 0;
     static constexpr int B_EMPTY = ST;
-    static constexpr int B_NEVER = 2 * ST;
+    static constexpr int B_NEVER = 2 * ST;        // no arrivals (the stall test's wait)
     static constexpr int NUM_BARS = 2 * ST + 1;
-    static_assert(NUM_BARS * 8 + 32 <= 256, "layout");
+    static_assert(NUM_BARS * 8 + 32 * WARPS + 32 <= 512, "layout");
 };
 
 // ------------------------------------------------------------------- copies
 
+// A warp's next tile to copy.  It lies in shared memory between its turns, so
+// that the products have its registers.
+struct alignas(16) DecI4Kept {
+    int4 a, b;
+};
+
+__device__ __forceinline__ void dec_i4_keep(const DecFp8It &it, int lane, DecI4Kept *kept) {
+    __syncwarp();
+    if (lane == 0) {
+        kept->a = make_int4(it.b, it.kvh, it.chunk, it.tile);
+        kept->b = make_int4(it.L, it.nt, it.next_len, it.left);
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ DecFp8It dec_i4_take(const DecI4Kept *kept) {
+    const int4 x = kept->a, y = kept->b;
+    DecFp8It it;
+    it.b = x.x, it.kvh = x.y, it.chunk = x.z, it.tile = x.w;
+    it.L = y.x, it.nt = y.y, it.next_len = y.z, it.left = y.w;
+    return it;
+}
+
+// n tiles on.
+__device__ __forceinline__ void dec_i4_advance(const DecInt4Params &p, DecFp8It &it, int n) {
+    while (n > 0 && it.left > 0) {
+        const int in_unit = min(n, it.nt - it.tile);  // up to the first tile of the next unit
+        it.left -= in_unit - 1;
+        it.tile += in_unit - 1;
+        dec_fp8_step(p, it);
+        n -= in_unit;
+    }
+}
+
 // Lane 4k + j copies part j (K codes, V codes, K words, V words) of block k of
-// a tile; its table entry, or -1 where it has none to copy, -2 where the entry is
+// a tile: its table entry, or -1 where it has none to copy, -2 where the entry is
 // outside the pool.
 template <class C>
-__device__ __forceinline__ int dec_i4_entry(const DecInt4Params &p, const DecFp8It &it) {
-    const int blk = (int)ptx::lane_id() >> 2, n = ((it.tile * C::BN) >> p.bs_log2) + blk;
+__device__ __forceinline__ int dec_i4_entry(const DecInt4Params &p, const DecFp8It &it, int lane) {
+    const int blk = lane >> 2, n = ((it.tile * C::BN) >> p.bs_log2) + blk;
     if (blk >= C::BN >> p.bs_log2 || it.left <= 0 || (n << p.bs_log2) >= it.L) return -1;
     const int e = p.block_table[(size_t)it.b * p.max_blocks + n];
     return e >= 0 && e < p.num_blocks ? e : -2;
 }
 
-// Copies a tile (and q's rows, where it begins a unit here) into a stage that is
-// free.  The whole warp.  Slots behind the request's blocks are not read later;
-// a block outside the pool gets zero words, whatever its codes.
+// Copies a tile into a stage that is free.  The whole warp.  Slots behind the
+// request's blocks are not read later; a block outside the pool gets zero words,
+// whatever its codes.
 template <class C>
-__device__ __forceinline__ void dec_i4_copy(const DecInt4Params &p, const DecFp8It &it, int entry, bool begins, uint32_t stage,
-                                            uint32_t bar, uint64_t pol) {
-    const int lane = (int)ptx::lane_id(), part = lane & 3, row = (lane >> 2) << p.bs_log2;
+__device__ __forceinline__ void dec_i4_copy(const DecInt4Params &p, int kvh, int entry, int lane, uint32_t stage, uint32_t bar) {
+    const int part = lane & 3, row = (lane >> 2) << p.bs_log2;
     const uint32_t word_bytes = (uint32_t)(C::NG * 4) << p.bs_log2;
     const uint32_t words_at = stage + (part & 1 ? C::O_VW : C::O_KW) + row * C::NG * 4;
     if (entry == -2 && part >= 2) {
@@ -118,23 +150,14 @@ __device__ __forceinline__ void dec_i4_copy(const DecInt4Params &p, const DecFp8
         ptx::fence_proxy_async_smem();
     }
     const uint32_t blocks = (uint32_t)__popc(__ballot_sync(0xffffffffu, entry >= 0)) / 4;
-    if (lane == 0) {
-        uint32_t bytes = blocks * (2 * word_bytes + ((uint32_t)(2 * C::ROW) << p.bs_log2));
-        int rows = 0;
-        size_t row0 = 0;
-        if (begins) {
-            row0 = dec_fp8_row0(p, it.b, it.kvh, it.chunk, &rows);
-            bytes += (uint32_t)rows * C::D * 2;
-        }
-        ptx::mbar_arrive_expect_tx(bar, bytes);
-        if (begins) ptx::bulk_load(stage + C::O_Q, p.q + row0 * C::D, (uint32_t)rows * C::D * 2, bar);
-    }
+    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, blocks * (2 * word_bytes + ((uint32_t)(2 * C::ROW) << p.bs_log2)));
     __syncwarp();
     if (entry >= 0) {
         if (part < 2) {
-            ptx::tma_load_4d(stage + (part ? C::O_V : 0) + row * C::ROW, part ? &p.tm_v : &p.tm_k, bar, 0, 0, it.kvh, entry, pol);
+            const uint64_t pol = p.chunks > 1 ? ptx::policy_evict_last() : ptx::policy_evict_first();
+            ptx::tma_load_4d(stage + (part ? C::O_V : 0) + row * C::ROW, part ? &p.tm_v : &p.tm_k, bar, 0, 0, kvh, entry, pol);
         } else {
-            const size_t at = (((size_t)entry * p.Hkv + it.kvh) << p.bs_log2) * C::NG;
+            const size_t at = (((size_t)entry * p.Hkv + kvh) << p.bs_log2) * C::NG;
             ptx::bulk_load(words_at, (part & 1 ? p.v_words : p.k_words) + at, word_bytes, bar);
         }
     }
@@ -167,13 +190,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
     return r;
 }
 
-// (v & mask) ^ flip in one instruction
-__device__ __forceinline__ uint32_t and_xor(uint32_t v, uint32_t mask, uint32_t flip) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(v), "r"(mask), "r"(flip));
-    return r;
-}
-
 __device__ __forceinline__ float lg2_approx(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -200,43 +216,59 @@ __device__ __forceinline__ float i4_zero(uint32_t w) {
     return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
 }
 
-// What a warp holds of its unit.  Lane i * 4 + t: keys i and i + 8 of a step,
-// rows 2t and 2t + 1 of each eight; of O, components 4i .. 4i + 3 of each chunk.
+// What a warp holds of its unit.  Lane 4i + t: keys i and i + 8 of a step, rows
+// 2t and 2t + 1 of each eight; of O, components 4i .. 4i + 3 of each chunk.
 template <class C>
 struct DecI4Warp {
     uint32_t q[C::NT][C::NC][4];     // fragments of q
-    float q_sum[C::NT][C::NG][2];    // 2^-20 times the groups' sums of q
+    float q_sum[C::NT][C::NG][2];    // -2^-20 times the groups' sums of q
     float mul[C::NT][2];             // from a sum of products to log2 units
-    int last[C::NT][2];              // last key the row sees
-    float m[C::NT][2];               // reference of the exponents, -inf before the first key
+    float m[C::NT][2];               // reference of the exponents
     float l[C::NT][2];               // this lane's sums of weights
-    float inv[C::NG];                // 1 / ref of the groups' V scales, a power of two; 0 before the first key
+    float inv[C::NG];                // kI4Room / ref of the groups' V scales, a power of two; 0 before the first
     float o[C::NT][C::NC][2][4];     // sums of weights times codes
     float zo[C::NT][C::NG][2];       // this lane's sums of weights times zeros
 };
 
-// q's rows from the ring into fragments.  A row is scaled by a power of two so
+constexpr float kI4None = -3.402823466e38f;  // the reference before the first key
+// What P V takes is at most 2^12: 2^6 when a row's reference has just moved,
+// which is 2^6 above its largest product then.
+constexpr float kI4Room = 4096.f;
+constexpr float kI4RoomLog2 = 12.f, kI4Ahead = 6.f;
+
+// q's rows of a unit, 16-bit: lane 4i + t has components 8t .. 8t + 7 of each chunk of rows i.
+template <class C>
+__device__ __forceinline__ void dec_i4_load_q(const DecInt4Params &p, const DecFp8It &u, int rg, int lane, uint4 (&raw)[C::NT][C::NC]) {
+    const int i = lane >> 2, t = lane & 3;
+    int rows;
+    const size_t row0 = dec_fp8_row0(p, u.b, u.kvh, u.chunk, &rows);
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) {
+        const int r = (rg * C::NT + n) * 8 + i;
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c) {
+            raw[n][c] = make_uint4(0, 0, 0, 0);
+            if (r < rows) raw[n][c] = *reinterpret_cast<const uint4 *>(p.q + (row0 + r) * C::D + 32 * c + 8 * t);
+        }
+    }
+}
+
+// q's rows into fragments, and empty sums.  A row is scaled by a power of two so
 // that its largest component is in [2^10, 2^11); 16-bit components are then
 // exact in fp16 down to 2^-24 of it (and 2^-25 of the row's scale is the most a
 // smaller one is off).  A row with an infinity, a NaN or a component of 2^112 or
 // more is NaN.
 template <class C>
-__device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const DecFp8It &u, const uint16_t *sq, int rg,
+__device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const uint4 (&raw)[C::NT][C::NC], int lane,
                                                   DecI4Warp<C> &w) {
-    const int lane = (int)threadIdx.x & 31, i = lane >> 2, t = lane & 3;
-    const int r_first = u.chunk * p.rows_per_chunk, rows = min(p.rows_per_chunk, p.R - r_first);
+    const int t = lane & 3;
 #pragma unroll
     for (int n = 0; n < C::NT; ++n) {
-        const int r = (rg * C::NT + n) * 8 + i;
-        uint4 raw[C::NC];
         uint32_t mag = 0;
 #pragma unroll
-        for (int c = 0; c < C::NC; ++c) {
-            raw[c] = make_uint4(0, 0, 0, 0);
-            if (r < rows) raw[c] = *reinterpret_cast<const uint4 *>(sq + r * C::D + 32 * c + 8 * t);
-            mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu),
-                                         __vmaxu2(raw[c].z & 0x7fff7fffu, raw[c].w & 0x7fff7fffu)));
-        }
+        for (int c = 0; c < C::NC; ++c)
+            mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(raw[n][c].x & 0x7fff7fffu, raw[n][c].y & 0x7fff7fffu),
+                                         __vmaxu2(raw[n][c].z & 0x7fff7fffu, raw[n][c].w & 0x7fff7fffu)));
         mag = max(mag & 0xffffu, mag >> 16);
         mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
         mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
@@ -251,7 +283,7 @@ __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const 
         for (int g = 0; g < C::NG; ++g) sum[g] = 0.f;
 #pragma unroll
         for (int c = 0; c < C::NC; ++c) {
-            const uint32_t ws[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+            const uint32_t ws[4] = {raw[n][c].x, raw[n][c].y, raw[n][c].z, raw[n][c].w};
             float x[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -271,16 +303,15 @@ __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const 
         for (int g = 0; g < C::NG; ++g) {
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
             sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-            sum[g] = fine ? sum[g] * 9.5367431640625e-7f : 0.f;
+            sum[g] = fine ? sum[g] * -9.5367431640625e-7f : 0.f;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int from = (2 * t + e) * 4, row = r_first + (rg * C::NT + n) * 8 + 2 * t + e;
+            const int from = (2 * t + e) * 4;
 #pragma unroll
             for (int g = 0; g < C::NG; ++g) w.q_sum[n][g][e] = __shfl_sync(0xffffffffu, sum[g], from);
             w.mul[n][e] = __shfl_sync(0xffffffffu, mul, from);
-            w.last[n][e] = p.mask_kind != kMaskCausal || p.Sq == 1 ? u.L - 1 : u.L - p.Sq + row % p.Sq;
-            w.m[n][e] = -INFINITY;
+            w.m[n][e] = kI4None;
             w.l[n][e] = 0.f;
 #pragma unroll
             for (int g = 0; g < C::NG; ++g) w.zo[n][g][e] = 0.f;
@@ -296,37 +327,38 @@ __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const 
     for (int g = 0; g < C::NG; ++g) w.inv[g] = 0.f;
 }
 
-// log2 of the largest of a key's V scales relative to their references.
+// log2 of the largest of a key's V scales relative to their references (a:
+// times kI4Room).
 template <class C>
 __device__ __forceinline__ float dec_i4_top(const float (&a)[C::NG]) {
-    float top = 9.09494702e-13f;  // 2^-40: a key without a scale does not move the reference far
+    float top = 3.7252903e-9f;  // 2^-40 of kI4Room: a key without a scale does not move the reference far
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) top = fmaxf(top, a[g]);
-    return lg2_approx(top);
+    return lg2_approx(top) - kI4RoomLog2;
 }
 
 // Moves the references of the groups' scales (where the step's largest is more
-// than 2^8 away) and of the exponents (up to the step's largest) and rescales
-// the sums.  vs: the V scales of the lane's two keys; s: their scores' sums of
-// products.  The whole warp.
+// than 2^8 away) and of the exponents (where a row's largest product is above
+// it) and rescales the sums.  vs: the V scales of the lane's keys; s: their
+// scores' sums of products.  The whole warp.
 template <class C>
 __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const float (&vs)[2][C::NG], const float (&s)[C::NT][4]) {
     float rise = -INFINITY;  // log2 of the factor of the group that grows most
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
         const float top = warp_max(fmaxf(vs[0][g], vs[1][g]));  // (a NaN scale is passed over)
-        const uint32_t ex = min(max(__float_as_uint(top) >> 23, 1u), 253u);
-        const float old = w.inv[g], now = __uint_as_float((254u - ex) << 23);
-        float factor = 1.f;
+        const uint32_t ex = min(max(__float_as_uint(top) >> 23, 13u), 253u);
+        const float old = w.inv[g] * (1.f / kI4Room), now = __uint_as_float((254u - ex) << 23);
         if (old == 0.f) {
-            if (top > 0.f) w.inv[g] = now;
-            else rise = fmaxf(rise, 0.f);  // (still without one)
+            if (top > 0.f) w.inv[g] = now * kI4Room;
+            rise = fmaxf(rise, 0.f);
             continue;
         }
+        float factor = 1.f;
         const float rel = top * old;
         if (rel > 256.f) {
             factor = now / old;  // < 1
-            w.inv[g] = now;
+            w.inv[g] = now * kI4Room;
         } else if (rel < 0.00390625f && top > 0.f) {
             // downwards as far as the sums have room in fp32
             float most = 1.f;
@@ -342,7 +374,7 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const float (&vs)[2
             most = warp_max(most);
             const uint32_t room = 200u - min(__float_as_uint(most) >> 23, 200u);  // up to 2^73
             const uint32_t from = __float_as_uint(old) >> 23, to = min(254u - ex, from + room);
-            w.inv[g] = __uint_as_float(to << 23);
+            w.inv[g] = __uint_as_float(to << 23) * kI4Room;
             factor = __uint_as_float((to - from + 127u) << 23);
         }
         if (factor != 1.f) {
@@ -376,8 +408,9 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const float (&vs)[2
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float old = w.m[n][e], now = fmaxf(old + fminf(rise, 0.f), top);
-            const float f = old == -INFINITY ? 0.f : ptx::ex2_approx(old - now);
+            // (where every group's reference rose, the exponents' may come down by as much)
+            const float old = w.m[n][e] + fminf(rise, 0.f), now = top > old ? top + kI4Ahead : old;
+            const float f = ptx::ex2_approx(w.m[n][e] - now);
             w.m[n][e] = now;
             w.l[n][e] *= f;
 #pragma unroll
@@ -392,36 +425,47 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const float (&vs)[2
         }
 }
 
-// 16 keys, the first of them `key`, at rows of codes ks and vs and words kws and vws.
+// What a lane reads of a stage at its warp's first step: K words, V matrices, words of its keys.
+struct DecI4Lane {
+    uint32_t k, v, w;
+};
+
 template <class C>
-__device__ __forceinline__ void dec_i4_keys(const DecInt4Params &p, DecI4Warp<C> &w, int key, int L, int seen_by_all,
-                                            uint32_t ks, uint32_t vs, uint32_t kws, uint32_t vws) {
-    const int lane = (int)threadIdx.x & 31, i = lane >> 2, t = lane & 3;
+__device__ __forceinline__ DecI4Lane dec_i4_lane(uint32_t ring, int lane, int first) {
     // 16-byte chunk c of row r of a box is chunk c ^ swizzle(r)
     auto swizzle = [](int r) { return C::ROW == 128 ? r & 7 : C::ROW == 64 ? (r >> 1) & 3 : (r >> 2) & 1; };
+    const int i = lane >> 2, t = lane & 3, v_row = lane & 15;
+    DecI4Lane x;
+    x.k = ring + (first + i) * C::ROW + (swizzle(i) << 4) + 4 * t;
+    x.v = ring + C::O_V + (first + v_row) * C::ROW + ((swizzle(v_row) ^ (lane >> 4)) << 4);
+    x.w = ring + C::O_KW + (first + i) * C::NG * 4;
+    return x;
+}
+
+// 16 keys, the first of them `key`, `at` bytes behind the lane's places.  Row r of
+// the K/V head, the warp's first being row0, sees keys up to L - 1 - back + r %
+// (back + 1).
+template <class C>
+__device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int back, int row0, int lane, const DecI4Lane &from,
+                                            uint32_t at, uint32_t at_words) {
+    auto load_words = [&](uint32_t where, uint32_t (&x)[2][C::NG]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) lds_words<C::NG>(where + 8 * k * C::NG * 4, x[k]);
+        if (key + 16 > L) {  // slots past the request's tokens may hold anything
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int g = 0; g < C::NG; ++g)
+                    if (key + (lane >> 2) + 8 * k >= L) x[k][g] = 0;
+        }
+    };
     uint32_t kw[2][C::NG], vw[2][C::NG];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        lds_words<C::NG>(kws + (i + 8 * k) * C::NG * 4, kw[k]);
-        lds_words<C::NG>(vws + (i + 8 * k) * C::NG * 4, vw[k]);
-    }
-    if (key + 16 > L) {  // slots past the request's tokens may hold anything
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int g = 0; g < C::NG; ++g)
-                if (key + i + 8 * k >= L) kw[k][g] = vw[k][g] = 0;
-    }
+    load_words(from.w + at_words, kw);
     float s[C::NT][4];
-#pragma unroll
-    for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-    const uint32_t k_lane = ks + i * C::ROW + (swizzle(i) << 4) + 4 * t;
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
         const float s0 = i4_scale(kw[0][g]), s1 = i4_scale(kw[1][g]);
-        const float z0 = -i4_zero(kw[0][g]), z1 = -i4_zero(kw[1][g]);
+        const float z0 = i4_zero(kw[0][g]), z1 = i4_zero(kw[1][g]);
         float acc[C::NT][4];
 #pragma unroll
         for (int n = 0; n < C::NT; ++n) {
@@ -432,50 +476,56 @@ __device__ __forceinline__ void dec_i4_keys(const DecInt4Params &p, DecI4Warp<C>
         }
 #pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
-            uint32_t a = lds32(k_lane ^ (uint32_t)(c << 4)), b = lds32((k_lane ^ (uint32_t)(c << 4)) + 8 * C::ROW);
+            const uint32_t place = (from.k + at) ^ (uint32_t)(c << 4);
+            uint32_t a = lds32(place), b = lds32(place + 8 * C::ROW);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int x = 0; x < 2; ++x) {
                 const uint32_t f[4] = {a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u};
 #pragma unroll
-                for (int n = 0; n < C::NT; ++n) mma_16816(acc[n], f, w.q[n][c][2 * h], w.q[n][c][2 * h + 1]);
+                for (int n = 0; n < C::NT; ++n) mma_16816(acc[n], f, w.q[n][c][2 * x], w.q[n][c][2 * x + 1]);
                 a >>= 8;
                 b >>= 8;
             }
         }
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n) {
-            s[n][0] = fmaf(s0, acc[n][0], s[n][0]);
-            s[n][1] = fmaf(s0, acc[n][1], s[n][1]);
-            s[n][2] = fmaf(s1, acc[n][2], s[n][2]);
-            s[n][3] = fmaf(s1, acc[n][3], s[n][3]);
-        }
+        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = g == 0 ? (e < 2 ? s0 : s1) * acc[n][e] : fmaf(e < 2 ? s0 : s1, acc[n][e], s[n][e]);
     }
+    load_words(from.w + at_words + C::WORDS, vw);
     // hidden keys: past the row's last (a select, so nothing of theirs leaks)
-    if (key + 15 > seen_by_all) {
+    if (key + 16 > L - back) {
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (key + i + 8 * (e >> 1) > w.last[n][e & 1]) s[n][e] = -INFINITY;
+            for (int e = 0; e < 2; ++e) {
+                const int row_last = back == 0 ? L - 1 : L - 1 - back + (row0 + 8 * n + 2 * (lane & 3) + e) % (back + 1);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (key + (lane >> 2) + 8 * k > row_last) s[n][2 * k + e] = -INFINITY;
+            }
     }
     float a[2][C::NG];
     {
-        float low = INFINITY;  // the smallest group's larger scale
+        bool move = false;
+        float low = INFINITY, high = 0.f;  // of the groups' larger scales of the lane's two keys
 #pragma unroll
         for (int g = 0; g < C::NG; ++g) {
             a[0][g] = i4_scale(vw[0][g]) * w.inv[g];
             a[1][g] = i4_scale(vw[1][g]) * w.inv[g];
-            low = fminf(low, fmaxf(a[0][g], a[1][g]));
+            const float most = fmaxf(a[0][g], a[1][g]);
+            low = fminf(low, most);
+            high = fmaxf(high, most);
         }
-        float la[2];
-        la[0] = dec_i4_top<C>(a[0]);
-        la[1] = dec_i4_top<C>(a[1]);
-        bool move = low < 0.00390625f || fmaxf(la[0], la[1]) > 8.f;
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n)
+        for (int k = 0; k < 2; ++k) {
+            const float la = dec_i4_top<C>(a[k]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                move = move || fmaf(s[n][e], w.mul[n][e & 1], la[e >> 1]) > w.m[n][e & 1] + 6.f;
+            for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) move |= fmaf(s[n][2 * k + e], w.mul[n][e], la) > w.m[n][e];
+        }
+        move |= (low < kI4Room / 256.f) | (high > kI4Room * 256.f);
         if (__any_sync(0xffffffffu, move)) {
             float raw[2][C::NG];
 #pragma unroll
@@ -494,23 +544,19 @@ __device__ __forceinline__ void dec_i4_keys(const DecInt4Params &p, DecI4Warp<C>
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float m = w.m[n][e & 1];
-            s[n][e] = ptx::ex2_approx(fmaf(s[n][e], w.mul[n][e & 1], m == -INFINITY ? 0.f : -m));
+            s[n][e] = ptx::ex2_approx(fmaf(s[n][e], w.mul[n][e & 1], -w.m[n][e & 1]));
             w.l[n][e & 1] += s[n][e];
         }
-    // odd keys: code 15 - c, weight negated
-    const float sign = i & 1 ? -1.f : 1.f, over = i & 1 ? 15.f : 0.f;
-    const int v_row = lane & 15;
-    const uint32_t v_lane = vs + v_row * C::ROW + ((swizzle(v_row) ^ (lane >> 4)) << 4);
     uint32_t raw[4];
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
         uint32_t pf[C::NT][2];
-        const float z0 = fmaf(sign, i4_zero(vw[0][g]), over), z1 = fmaf(sign, i4_zero(vw[1][g]), over);
-        const float a0 = sign * a[0][g], a1 = sign * a[1][g];
+        // keys 8 .. 15: code 15 - c, weight negated
+        const float z0 = i4_zero(vw[0][g]), z1 = 15.f - i4_zero(vw[1][g]);
 #pragma unroll
         for (int n = 0; n < C::NT; ++n) {
-            const uint32_t h0 = ptx::pack_f16x2(s[n][0] * a0, s[n][1] * a0), h1 = ptx::pack_f16x2(s[n][2] * a1, s[n][3] * a1);
+            const uint32_t h0 = ptx::pack_f16x2(s[n][0] * a[0][g], s[n][1] * a[0][g]);
+            const uint32_t h1 = ptx::pack_f16x2(s[n][2] * -a[1][g], s[n][3] * -a[1][g]);
             // the zeros meet the rounded weights, so that a weight's rounding is of its value's share only
             const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
             w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
@@ -520,14 +566,13 @@ __device__ __forceinline__ void dec_i4_keys(const DecInt4Params &p, DecI4Warp<C>
         }
 #pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
-            if (c % 2 == 0) ldmatrix_x4_trans(v_lane ^ (uint32_t)(c << 4), raw);
+            if (c % 2 == 0) ldmatrix_x4_trans((from.v + at) ^ (uint32_t)(c << 4), raw);
             uint32_t lo = raw[c % 2 * 2], hi = raw[c % 2 * 2 + 1];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t f[4] = {and_xor(lo, 0x000f000fu, 0x000f0000u), and_xor(lo, 0x00f000f0u, 0x00f00000u),
-                                       and_xor(hi, 0x000f000fu, 0x000f0000u), and_xor(hi, 0x00f000f0u, 0x00f00000u)};
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t f[4] = {lo & 0x000f000fu, lo & 0x00f000f0u, ~hi & 0x000f000fu, ~hi & 0x00f000f0u};
 #pragma unroll
-                for (int n = 0; n < C::NT; ++n) mma_16816(w.o[n][c][h], f, pf[n][0], pf[n][1]);
+                for (int n = 0; n < C::NT; ++n) mma_16816(w.o[n][c][x], f, pf[n][0], pf[n][1]);
                 lo >>= 8;
                 hi >>= 8;
             }
@@ -535,155 +580,201 @@ __device__ __forceinline__ void dec_i4_keys(const DecInt4Params &p, DecI4Warp<C>
     }
 }
 
-// The unit's end: the warps of a row group leave their sums, and together
-// write the rows out, or a partial of them.
+// All warps of a row group.  (A number known at compile time: a variable one
+// takes all sixteen barriers for the CTA.)
+template <class C>
+__device__ __forceinline__ void dec_i4_meet(int rg) {
+    if (C::RG == 1 || rg == 0) ptx::named_bar_sync(1, C::KW * 32);
+    else if (C::RG == 2 || rg == 1) ptx::named_bar_sync(2, C::KW * 32);
+    else if (rg == 2) ptx::named_bar_sync(3, C::KW * 32);
+    else ptx::named_bar_sync(4, C::KW * 32);
+}
+
+// The unit's end.  A row group's warps hand their sums down, half of them to the
+// other half at a time; the last writes the rows out, or a partial of them.
 template <class C>
 __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const DecFp8It &it, DecI4Warp<C> &w, int rg, int kwi,
-                                                bool whole, bool begun_here, float *scratch, float *ml) {
-    const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5, i = lane >> 2, t = lane & 3;
-    constexpr int RW = 8 * C::NT;
-    float *mine = scratch + warp * RW * C::OROW;
-    float *ml_mine = ml + warp * RW * 2;
-    int rows;
-    const size_t row0 = dec_fp8_row0(p, it.b, it.kvh, it.chunk, &rows);
-    rows = min(rows - rg * RW, RW);  // of this row group (0 or less: none)
+                                                int lane, bool whole, bool begun_here, uint8_t *parts) {
+    const int i = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int n = 0; n < C::NT; ++n) {
-        if (8 * n >= rows) break;
+    for (int n = 0; n < C::NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float l = w.l[n][e];
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            const int r = 8 * n + 2 * t + e;
-            if (i == 0) {
-                ml_mine[2 * r] = w.m[n][e];
-                ml_mine[2 * r + 1] = l;
-            }
+            for (int o = 4; o < 32; o <<= 1) w.l[n][e] += __shfl_xor_sync(0xffffffffu, w.l[n][e], o);
 #pragma unroll
             for (int g = 0; g < C::NG; ++g) {
                 float z = w.zo[n][g][e];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                const float ref = w.inv[g] == 0.f ? 0.f : __uint_as_float((254u << 23) - __float_as_uint(w.inv[g]));
-                if (r >= rows) continue;
+                // (the sums are kI4Room / ref too large)
+                const uint32_t inv = __float_as_uint(w.inv[g]);
+                const float ref = inv == 0 ? 0.f : __uint_as_float((254u << 23) - inv);
 #pragma unroll
                 for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
-                    float4 y;
-                    y.x = ref * fmaf(w.o[n][c][0][e], 16777216.f, -z);
-                    y.y = ref * fmaf(w.o[n][c][0][2 + e], 1048576.f, -z);
-                    y.z = ref * fmaf(w.o[n][c][1][e], 16777216.f, -z);
-                    y.w = ref * fmaf(w.o[n][c][1][2 + e], 1048576.f, -z);
-                    *reinterpret_cast<float4 *>(mine + r * C::OROW + 32 * c + 4 * i) = y;
+                    w.o[n][c][0][e] = ref * fmaf(w.o[n][c][0][e], 16777216.f, -z);
+                    w.o[n][c][0][2 + e] = ref * fmaf(w.o[n][c][0][2 + e], 1048576.f, -z);
+                    w.o[n][c][1][e] = ref * fmaf(w.o[n][c][1][e], 16777216.f, -z);
+                    w.o[n][c][1][2 + e] = ref * fmaf(w.o[n][c][1][2 + e], 1048576.f, -z);
+                }
+            }
+        }
+    dec_i4_meet<C>(rg);  // the unit before is read
+    {
+#pragma unroll
+        for (int half = C::KW / 2; half > 0; half >>= 1) {
+            float4 *at = reinterpret_cast<float4 *>(parts + (rg * (C::KW / 2) + kwi % half) * C::PART) + lane;
+            if (kwi >= half && kwi < 2 * half) {
+#pragma unroll
+                for (int n = 0; n < C::NT; ++n) {
+                    at[(2 * C::NT * C::NC + n) * 32] = make_float4(w.m[n][0], w.m[n][1], w.l[n][0], w.l[n][1]);
+#pragma unroll
+                    for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            at[((n * C::NC + c) * 2 + x) * 32] =
+                                make_float4(w.o[n][c][x][0], w.o[n][c][x][1], w.o[n][c][x][2], w.o[n][c][x][3]);
+                }
+            }
+            dec_i4_meet<C>(rg);
+            if (kwi < half) {
+#pragma unroll
+                for (int n = 0; n < C::NT; ++n) {
+                    const float4 ml = at[(2 * C::NT * C::NC + n) * 32];
+                    const float m0 = fmaxf(w.m[n][0], ml.x), m1 = fmaxf(w.m[n][1], ml.y);
+                    const float a0 = ptx::ex2_approx(w.m[n][0] - m0), b0 = ptx::ex2_approx(ml.x - m0);
+                    const float a1 = ptx::ex2_approx(w.m[n][1] - m1), b1 = ptx::ex2_approx(ml.y - m1);
+                    w.m[n][0] = m0;
+                    w.m[n][1] = m1;
+                    w.l[n][0] = fmaf(w.l[n][0], a0, ml.z * b0);
+                    w.l[n][1] = fmaf(w.l[n][1], a1, ml.w * b1);
+#pragma unroll
+                    for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float4 y = at[((n * C::NC + c) * 2 + x) * 32];
+                            float(&o)[4] = w.o[n][c][x];
+                            o[0] = fmaf(o[0], a0, y.x * b0);
+                            o[1] = fmaf(o[1], a1, y.y * b1);
+                            o[2] = fmaf(o[2], a0, y.z * b0);
+                            o[3] = fmaf(o[3], a1, y.w * b1);
+                        }
                 }
             }
         }
     }
-    ptx::named_bar_sync(1 + rg, C::KW * 32);
-    const float *group_o = scratch + rg * C::KW * RW * C::OROW, *group_ml = ml + rg * C::KW * RW * 2;
+    if (kwi != 0) return;
+    int rows;
+    const size_t row0 = dec_fp8_row0(p, it.b, it.kvh, it.chunk, &rows);
     const size_t slot = 2 * (size_t)blockIdx.x + (begun_here ? 1 : 0);
-    // a warp per row, lanes along its components
-    for (int r = kwi; r < rows; r += C::KW) {
-        float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < C::KW; ++k) top = fmaxf(top, group_ml[(k * RW + r) * 2]);
-        const float use = top == -INFINITY ? 0.f : top;
-        float l = 0.f, acc[C::D / 32];
+    for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-        for (int e = 0; e < C::D / 32; ++e) acc[e] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+            const int r = (rg * C::NT + n) * 8 + 2 * t + e;
+            if (r >= rows) continue;
+            const float l = w.l[n][e], inv = l == 0.f ? 0.f : 1.f / l;
+            const float lse2 = l == 0.f ? -INFINITY : w.m[n][e] + __log2f(l);  // (a NaN sum is no empty row)
+            if (i == 0) {
+                if (whole) p.lse[row0 + r] = lse2 * kLn2;
+                else p.part_lse[slot * C::RC + r] = lse2;
+            }
 #pragma unroll
-        for (int k = 0; k < C::KW; ++k) {
-            const float f = ptx::ex2_approx(group_ml[(k * RW + r) * 2] - use);
-            l = fmaf(f, group_ml[(k * RW + r) * 2 + 1], l);
-#pragma unroll
-            for (int e = 0; e < C::D / 32; e += 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(group_o + (k * RW + r) * C::OROW + 32 * e + 2 * lane);
-                acc[e] = fmaf(f, v.x, acc[e]);
-                acc[e + 1] = fmaf(f, v.y, acc[e + 1]);
+            for (int c = 0; c < C::NC; ++c) {
+                const float y0 = w.o[n][c][0][e] * inv, y1 = w.o[n][c][0][2 + e] * inv;
+                const float y2 = w.o[n][c][1][e] * inv, y3 = w.o[n][c][1][2 + e] * inv;
+                const int d = 32 * c + 4 * i;
+                if (whole)
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + (row0 + r) * C::D + d) =
+                        p.fp16 ? make_uint2(ptx::pack_f16x2(y0, y1), ptx::pack_f16x2(y2, y3))
+                               : make_uint2(ptx::pack_bf16x2(y0, y1), ptx::pack_bf16x2(y2, y3));
+                else
+                    *reinterpret_cast<float4 *>(p.part_o + (slot * C::RC + r) * C::D + d) = make_float4(y0, y1, y2, y3);
             }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const float lse2 = l == 0.f ? -INFINITY : use + __log2f(l);  // (a NaN sum is no empty row)
-        const int row = rg * RW + r;
-        if (whole) {
-            if (lane == 0) p.lse[row0 + row] = lse2 * kLn2;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + (row0 + row) * C::D);
-#pragma unroll
-            for (int e = 0; e < C::D / 32; e += 2)
-                dst[16 * e + lane] = p.fp16 ? ptx::pack_f16x2(acc[e] * inv, acc[e + 1] * inv)
-                                            : ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-        } else {
-            if (lane == 0) p.part_lse[slot * C::RC + row] = lse2;
-            float *dst = p.part_o + (slot * C::RC + row) * C::D;
-#pragma unroll
-            for (int e = 0; e < C::D / 32; e += 2)
-                *reinterpret_cast<float2 *>(dst + 32 * e + 2 * lane) = make_float2(acc[e] * inv, acc[e + 1] * inv);
-        }
-    }
-    ptx::named_bar_sync(1 + rg, C::KW * 32);  // the scratch is free again
 }
 
 template <class C>
-__device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint8_t *ring, float *scratch, float *ml, uint32_t bars,
+__device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, uint8_t *parts, DecI4Kept *kept, uint32_t bars,
                             int *copied, Ctl *ctl) {
     const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5, rg = warp / C::KW, kwi = warp % C::KW;
-    const uint64_t pol = p.chunks > 1 ? ptx::policy_evict_last() : ptx::policy_evict_first();
-    const uint32_t ring_addr = ptx::smem_addr(ring);
+    if (it.left <= 0) return;
+    uint4 raw[C::NT][C::NC];
+    dec_i4_load_q<C>(p, it, rg, lane, raw);
     // The warps take turns at the copies: tile n is copied by warp n of the first
-    // ST - 1 and by the warp whose turn tile n - ST + 1 is, behind its own keys of
-    // that one; the stage's last readers were busy with the tile in front.
+    // ST - 1, and tile t + ST - 1 by warp t % 8, behind its own keys of tile t;
+    // the stage's last readers were busy with the tile in front of that.
     DecFp8It ahead = it;
-    for (int n = 0; n < C::ST - 1 && ahead.left > 0; ++n) {
-        if (warp == n) {
-            if (lane == 0) atomicMax(copied, n + 1);
-            dec_i4_copy<C>(p, ahead, dec_i4_entry<C>(p, ahead), n == 0 || ahead.tile == 0, ring_addr + n * C::STAGE,
-                           bar_addr(bars, C::B_FULL + n), pol);
+    if (warp < C::ST - 1) {
+        dec_i4_advance(p, ahead, warp);
+        if (ahead.left > 0) {
+            if (lane == 0) atomicMax(copied, warp + 1);
+            dec_i4_copy<C>(p, ahead.kvh, dec_i4_entry<C>(p, ahead, lane), lane, ring + warp * C::STAGE, bar_addr(bars, C::B_FULL + warp));
         }
-        dec_fp8_step(p, ahead);
+        dec_i4_advance(p, ahead, C::ST - 1);
+    } else {
+        dec_i4_advance(p, ahead, warp + C::ST - 1);
     }
+    dec_i4_keep(ahead, lane, kept);
+    const DecI4Lane from = dec_i4_lane<C>(ring, lane, kwi * C::SPT * 16);
+    const int back = p.mask_kind == kMaskCausal ? p.Sq - 1 : 0;
     DecI4Warp<C> w;
-    bool begins = true, begun_here = it.tile == 0, bad = false;
-    int slot = 0, prev = C::ST - 1;  // the stages of this tile and of the one in front
-    uint32_t phase = 0, prev_phase = 1;
-    for (int t = 0; it.left > 0; ++t) {
-        const bool turn = (t & (C::WARPS - 1)) == warp && ahead.left > 0;
-        int entry = -1;
-        if (turn) entry = dec_i4_entry<C>(p, ahead);
+    dec_i4_begin_unit<C>(p, raw, lane, w);
+    bool begun_here = it.tile == 0, bad = false;
+    if (p.stall_test) bad = !wait_warp(bar_addr(bars, C::B_NEVER), 0, ctl, 92);
+    int slot = 0, turn = warp;      // turn: tiles until this warp's next copy
+    uint32_t phase = 0;
+    int t = 0;
+    for (;;) {
+        int entry = -1, kvh = 0;
+        if (turn == 0) {
+            const DecFp8It coming = dec_i4_take(kept);
+            kvh = coming.left > 0 ? coming.kvh : -1;
+            entry = dec_i4_entry<C>(p, coming, lane);
+        }
         // (a warp whose wait ran out goes on without its tiles, so that the others meet it at the units' ends)
-        if (!bad) bad = !wait_warp(bar_addr(bars, p.stall_test && t == 0 ? C::B_NEVER : C::B_FULL + slot), phase, ctl, 92);
-        const uint8_t *stage = ring + slot * C::STAGE;
-        if (begins) dec_i4_begin_unit<C>(p, it, reinterpret_cast<const uint16_t *>(stage + C::O_Q), rg, w);
-        begins = false;
-        const int seen_by_all = p.mask_kind == kMaskCausal ? it.L - p.Sq : it.L - 1;
+        if (!bad) bad = !wait_warp(bar_addr(bars, C::B_FULL + slot), phase, ctl, 92);
+        int key = it.tile * C::BN + kwi * C::SPT * 16;
 #pragma unroll 1
-        for (int j = 0; j < C::KPW; ++j) {
-            const int at = (kwi * C::KPW + j) * 16, key = it.tile * C::BN + at;
+        for (int j = 0; j < C::SPT; ++j, key += 16) {
             if (bad || key >= it.L) break;
-            const uint32_t base = ring_addr + slot * C::STAGE;
-            dec_i4_keys<C>(p, w, key, it.L, seen_by_all, base + at * C::ROW, base + C::O_V + at * C::ROW,
-                           base + C::O_KW + at * C::NG * 4, base + C::O_VW + at * C::NG * 4);
+            dec_i4_keys<C>(w, key, it.L, back, it.chunk * p.rows_per_chunk + rg * C::NT * 8, lane, from,
+                           slot * C::STAGE + j * 16 * C::ROW, slot * C::STAGE + j * 16 * C::NG * 4);
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_addr(bars, C::B_EMPTY + slot));
-        if (turn && !bad) {
-            // tile t + ST - 1 goes where tile t - 1 was
-            bad = t > 0 && !wait_warp(bar_addr(bars, C::B_EMPTY + prev), prev_phase, ctl, 91);
-            if (!bad) {
-                if (lane == 0) atomicMax(copied, t + C::ST);
-                dec_i4_copy<C>(p, ahead, entry, ahead.tile == 0, ring_addr + prev * C::STAGE, bar_addr(bars, C::B_FULL + prev), pol);
+        if (turn == 0) {
+            turn = C::WARPS;
+            if (kvh >= 0 && !bad) {
+                // where tile t - 1 was
+                const int prev = slot == 0 ? C::ST - 1 : slot - 1;
+                bad = t > 0 && !wait_warp(bar_addr(bars, C::B_EMPTY + prev), slot == 0 ? phase ^ 1 : phase, ctl, 91);
+                if (!bad) {
+                    if (lane == 0) atomicMax(copied, t + C::ST);
+                    dec_i4_copy<C>(p, kvh, entry, lane, ring + prev * C::STAGE, bar_addr(bars, C::B_FULL + prev));
+                    DecFp8It coming = dec_i4_take(kept);
+                    dec_i4_advance(p, coming, C::WARPS);
+                    dec_i4_keep(coming, lane, kept);
+                }
             }
         }
-        if (ahead.left > 0) dec_fp8_step(p, ahead);
-        const bool ends = it.tile + 1 == it.nt;
-        if (ends || it.left == 1) {
-            dec_i4_end_unit<C>(p, it, w, rg, kwi, begun_here && ends, begun_here, scratch, ml);
-            begins = true;
-            begun_here = true;
-        }
-        dec_fp8_step(p, it);
-        prev = slot;
-        prev_phase = phase;
+        --turn;
+        ++t;
         if (++slot == C::ST) slot = 0, phase ^= 1;
+        const bool ends = it.tile + 1 == it.nt, done = it.left == 1;
+        if (ends || done) {
+            DecFp8It next = it;
+            dec_fp8_step(p, next);
+            if (!done) dec_i4_load_q<C>(p, next, rg, lane, raw);
+            dec_i4_end_unit<C>(p, it, w, rg, kwi, lane, begun_here && ends, begun_here, parts);
+            if (done) break;
+            it = next;
+            dec_i4_begin_unit<C>(p, raw, lane, w);
+            begun_here = true;
+        } else {
+            ++it.tile;
+            --it.left;
+        }
     }
 }
 
@@ -693,9 +784,9 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    float *scratch = reinterpret_cast<float *>(ring + C::ST * C::STAGE);
-    float *ml = scratch + C::SCRATCH / 4;
-    uint64_t *bar_mem = reinterpret_cast<uint64_t *>(ml + 2 * C::WARPS * 8 * C::NT);
+    uint8_t *parts = ring + C::ST * C::STAGE;
+    DecI4Kept *kept = reinterpret_cast<DecI4Kept *>(parts + C::PARTS * C::PART);
+    uint64_t *bar_mem = reinterpret_cast<uint64_t *>(kept + C::WARPS);
     Ctl *ctl = reinterpret_cast<Ctl *>(bar_mem + C::NUM_BARS);
     int *copied = reinterpret_cast<int *>(ctl + 1);  // tiles that copies were begun for
     const uint32_t bars = ptx::smem_addr(bar_mem);
@@ -714,17 +805,17 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
         ptx::prefetch_tensormap(&p.tm_v);
     }
     ptx::wait_for_previous_kernel();
-    const DecFp8It it = dec_fp8_begin<C::NUM_THREADS>(p, reinterpret_cast<long long *>(scratch));
+    const DecFp8It it = dec_fp8_begin<C::NUM_THREADS>(p, reinterpret_cast<long long *>(parts));
     __syncthreads();
     // the merge may be set up now; it waits for this grid's end before it reads
     ptx::let_next_kernel_begin();
-    dec_i4_warp<C>(p, it, ring, scratch, ml, bars, copied, ctl);
+    dec_i4_warp<C>(p, it, ptx::smem_addr(ring), parts, kept + (threadIdx.x >> 5), bars, copied, ctl);
     __syncthreads();
     // the CTA's memory stays until its last copies have landed, also where the
     // warps gave up waiting for them
     if (ctl->abort && threadIdx.x == 0) {
         const int n = *copied;
-        for (int t = n - C::ST > 0 ? n - C::ST : 0; t < n; ++t)
+        for (int t = max(n - C::ST, 0); t < n; ++t)
             wait_bar_drain(bar_addr(bars, C::B_FULL + t % C::ST), (t / C::ST) & 1);
     }
 }
