@@ -223,7 +223,7 @@ DecFp8Plan plan_decode_int4(int B, int Hkv, int R, int d, int max_seq_len, int n
     pl.rows_per_chunk = (R + pl.chunks - 1) / pl.chunks;
     pl.chunks = (R + pl.rows_per_chunk - 1) / pl.rows_per_chunk;
     pl.rc = pl.rows_per_chunk <= 8 ? 8 : pl.rows_per_chunk <= 16 ? 16 : 32;
-    const int per_sm = d <= 128 && pl.rc == 8 ? 2 : 1;
+    const int per_sm = d <= 128 && pl.rc == 8 ? 3 : 2;
     const long long tiles = (max_seq_len + 127LL) / 128;
     const long long units = (long long)B * Hkv * pl.chunks;
     pl.cuts = tiles > kDecFp8WholeTiles;

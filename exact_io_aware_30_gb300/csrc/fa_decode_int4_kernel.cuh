@@ -62,10 +62,12 @@ struct DecI4Cfg {
     static constexpr int NT = NT_;                // eights of rows per warp
     static constexpr int RG = RG_;                // groups of warps with different rows
     static constexpr int RC = 8 * NT * RG;        // rows per unit
-    static constexpr int WARPS = 8;
+    static constexpr int WARPS = 4;
     static constexpr int KW = WARPS / RG;         // warps along a tile's keys
-    static constexpr int SPT = 8 / KW;            // steps of 16 keys of a warp per tile
+    static constexpr int H = D <= 128 && NT == 1 ? 2 : 1;  // 16-key halves of a step, side by side
+    static constexpr int KEYS = 16 * H;
     static constexpr int BN = 128;
+    static constexpr int SPT = BN / KEYS / KW;    // steps of a warp per tile
     static constexpr int NG = D / G;
     static constexpr int NC = D / 32;             // chunks of 32 components, 16 bytes
     static constexpr int ROW = D / 2;             // bytes of a row of codes
@@ -75,12 +77,12 @@ struct DecI4Cfg {
     static constexpr int STAGE = (O_VW + WORDS + 1023) / 1024 * 1024;
     static constexpr int PART = (2 * NT * NC + NT) * 512;  // a warp's sums, on their way to another's
     static constexpr int PARTS = WARPS / 2;
-    static constexpr int CTAS_PER_SM = D <= 128 && NT == 1 ? 2 : 1;
+    static constexpr int CTAS_PER_SM = D <= 128 && NT == 1 ? 3 : 2;
     static constexpr int BUDGET = (227 / CTAS_PER_SM - 1) * 1024;
     static constexpr int FIXED = 1024 + PARTS * PART + 512;
     static constexpr int FIT = (BUDGET - FIXED) / STAGE;
-    static constexpr int ST = FIT < 8 ? FIT : 8;
-    static_assert(ST >= 2 && ST <= WARPS, "a ring of at least two tiles, a warp to begin each");
+    static constexpr int ST = FIT < WARPS + 1 ? FIT : WARPS + 1;
+    static_assert(ST >= 2 && ST <= WARPS + 1, "a ring of at least two tiles, a warp to begin each");
     static constexpr int SMEM_BYTES = FIXED + ST * STAGE;
     static constexpr int NUM_THREADS = 32 * WARPS;
     static constexpr int B_FULL = 0;
@@ -177,6 +179,10 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
+}
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
@@ -339,14 +345,17 @@ __device__ __forceinline__ float dec_i4_top(const float (&a)[C::NG]) {
 
 // Moves the references of the groups' scales (where the step's largest is more
 // than 2^8 away) and of the exponents (where a row's largest product is above
-// it) and rescales the sums.  vs: the V scales of the lane's keys; s: their
+// it) and rescales the sums.  vw: the V words of the lane's keys; s: their
 // scores' sums of products.  The whole warp.
 template <class C>
-__device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const float (&vs)[2][C::NG], const float (&s)[C::NT][4]) {
+__device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw)[C::H][2][C::NG], const float (&s)[C::H][C::NT][4]) {
     float rise = -INFINITY;  // log2 of the factor of the group that grows most
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
-        const float top = warp_max(fmaxf(vs[0][g], vs[1][g]));  // (a NaN scale is passed over)
+        float top = 0.f;
+#pragma unroll
+        for (int h = 0; h < C::H; ++h) top = fmaxf(top, fmaxf(i4_scale(vw[h][0][g]), i4_scale(vw[h][1][g])));
+        top = warp_max(top);  // (a NaN scale is passed over)
         const uint32_t ex = min(max(__float_as_uint(top) >> 23, 13u), 253u);
         const float old = w.inv[g] * (1.f / kI4Room), now = __uint_as_float((254u - ex) << 23);
         if (old == 0.f) {
@@ -392,19 +401,24 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const float (&vs)[2
         }
         rise = fmaxf(rise, lg2_approx(factor));
     }
-    float la[2];
+    float la[C::H][2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        float a[C::NG];
+    for (int h = 0; h < C::H; ++h)
 #pragma unroll
-        for (int g = 0; g < C::NG; ++g) a[g] = vs[k][g] * w.inv[g];
-        la[k] = dec_i4_top<C>(a);
-    }
+        for (int k = 0; k < 2; ++k) {
+            float a[C::NG];
+#pragma unroll
+            for (int g = 0; g < C::NG; ++g) a[g] = i4_scale(vw[h][k][g]) * w.inv[g];
+            la[h][k] = dec_i4_top<C>(a);
+        }
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(fmaf(s[n][e], w.mul[n][e], la[0]), fmaf(s[n][2 + e], w.mul[n][e], la[1]));
+            float top = kI4None;
+#pragma unroll
+            for (int h = 0; h < C::H; ++h)
+                top = fmaxf(top, fmaxf(fmaf(s[h][n][e], w.mul[n][e], la[h][0]), fmaf(s[h][n][2 + e], w.mul[n][e], la[h][1])));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -442,140 +456,163 @@ __device__ __forceinline__ DecI4Lane dec_i4_lane(uint32_t ring, int lane, int fi
     return x;
 }
 
-// 16 keys, the first of them `key`, `at` bytes behind the lane's places.  Row r of
-// the K/V head, the warp's first being row0, sees keys up to L - 1 - back + r %
-// (back + 1).
+// A step's keys, the first of them `key`, `at` bytes behind the lane's places.
+// Row r of the K/V head, the warp's first being row0, sees keys up to L - 1 -
+// back + r % (back + 1).
 template <class C>
 __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int back, int row0, int lane, const DecI4Lane &from,
                                             uint32_t at, uint32_t at_words) {
-    auto load_words = [&](uint32_t where, uint32_t (&x)[2][C::NG]) {
+    constexpr int H = C::H, HALF = 16 * C::ROW, ROW_W = C::NG * 4;
+    const uint32_t words = from.w + at_words;
+    if (key + C::KEYS > L) {  // slots past the request's tokens may hold anything: their words become 0
+        const int mine = lane & (C::KEYS - 1);
+        if (key + mine >= L) {
+            const uint32_t row = words + (mine - (lane >> 2)) * ROW_W + (C::KEYS == 16 && lane >= 16 ? C::WORDS : 0);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) lds_words<C::NG>(where + 8 * k * C::NG * 4, x[k]);
-        if (key + 16 > L) {  // slots past the request's tokens may hold anything
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int g = 0; g < C::NG; ++g)
-                    if (key + (lane >> 2) + 8 * k >= L) x[k][g] = 0;
+            for (int g = 0; g < C::NG; ++g) {
+                sts32(row + 4 * g, 0u);
+                if (C::KEYS == 32) sts32(row + C::WORDS + 4 * g, 0u);
+            }
         }
-    };
-    uint32_t kw[2][C::NG], vw[2][C::NG];
-    load_words(from.w + at_words, kw);
-    float s[C::NT][4];
+        ptx::fence_proxy_async_smem();  // (the next copy to this stage comes behind)
+        __syncwarp();
+    }
+    uint32_t kw[H][2][C::NG], vw[H][2][C::NG];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + (16 * h + 8 * k) * ROW_W, kw[h][k]);
+    float s[H][C::NT][4];
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
-        const float s0 = i4_scale(kw[0][g]), s1 = i4_scale(kw[1][g]);
-        const float z0 = i4_zero(kw[0][g]), z1 = i4_zero(kw[1][g]);
-        float acc[C::NT][4];
+        float acc[H][C::NT][4];
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n) {
-            acc[n][0] = z0 * w.q_sum[n][g][0];
-            acc[n][1] = z0 * w.q_sum[n][g][1];
-            acc[n][2] = z1 * w.q_sum[n][g][0];
-            acc[n][3] = z1 * w.q_sum[n][g][1];
-        }
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[h][n][e] = i4_zero(kw[h][e >> 1][g]) * w.q_sum[n][g][e & 1];
 #pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
             const uint32_t place = (from.k + at) ^ (uint32_t)(c << 4);
-            uint32_t a = lds32(place), b = lds32(place + 8 * C::ROW);
+            uint32_t a[H], b[H];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const uint32_t f[4] = {a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u};
+            for (int h = 0; h < H; ++h) a[h] = lds32(place + h * HALF), b[h] = lds32(place + h * HALF + 8 * C::ROW);
 #pragma unroll
-                for (int n = 0; n < C::NT; ++n) mma_16816(acc[n], f, w.q[n][c][2 * x], w.q[n][c][2 * x + 1]);
-                a >>= 8;
-                b >>= 8;
-            }
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const uint32_t f[4] = {a[h] & 0x000f000fu, b[h] & 0x000f000fu, a[h] & 0x00f000f0u, b[h] & 0x00f000f0u};
+#pragma unroll
+                    for (int n = 0; n < C::NT; ++n) mma_16816(acc[h][n], f, w.q[n][c][2 * x], w.q[n][c][2 * x + 1]);
+                    a[h] >>= 8;
+                    b[h] >>= 8;
+                }
         }
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = g == 0 ? (e < 2 ? s0 : s1) * acc[n][e] : fmaf(e < 2 ? s0 : s1, acc[n][e], s[n][e]);
+            for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float scale = i4_scale(kw[h][e >> 1][g]);
+                    s[h][n][e] = g == 0 ? scale * acc[h][n][e] : fmaf(scale, acc[h][n][e], s[h][n][e]);
+                }
     }
-    load_words(from.w + at_words + C::WORDS, vw);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + C::WORDS + (16 * h + 8 * k) * ROW_W, vw[h][k]);
     // hidden keys: past the row's last (a select, so nothing of theirs leaks)
-    if (key + 16 > L - back) {
+    if (key + C::KEYS > L - back) {
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row_last = back == 0 ? L - 1 : L - 1 - back + (row0 + 8 * n + 2 * (lane & 3) + e) % (back + 1);
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (key + (lane >> 2) + 8 * k > row_last) s[n][2 * k + e] = -INFINITY;
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (key + (lane >> 2) + 16 * h + 8 * k > row_last) s[h][n][2 * k + e] = -INFINITY;
             }
     }
-    float a[2][C::NG];
     {
         bool move = false;
-        float low = INFINITY, high = 0.f;  // of the groups' larger scales of the lane's two keys
+        float low = INFINITY, high = 0.f;  // of the groups' largest scales of the lane's keys
+        float most[C::NG];
 #pragma unroll
-        for (int g = 0; g < C::NG; ++g) {
-            a[0][g] = i4_scale(vw[0][g]) * w.inv[g];
-            a[1][g] = i4_scale(vw[1][g]) * w.inv[g];
-            const float most = fmaxf(a[0][g], a[1][g]);
-            low = fminf(low, most);
-            high = fmaxf(high, most);
-        }
+        for (int g = 0; g < C::NG; ++g) most[g] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float la = dec_i4_top<C>(a[k]);
+        for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int n = 0; n < C::NT; ++n)
+            for (int k = 0; k < 2; ++k) {
+                float a[C::NG];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) move |= fmaf(s[n][2 * k + e], w.mul[n][e], la) > w.m[n][e];
-        }
-        move |= (low < kI4Room / 256.f) | (high > kI4Room * 256.f);
-        if (__any_sync(0xffffffffu, move)) {
-            float raw[2][C::NG];
+                for (int g = 0; g < C::NG; ++g) {
+                    a[g] = i4_scale(vw[h][k][g]) * w.inv[g];
+                    most[g] = fmaxf(most[g], a[g]);
+                }
+                const float la = dec_i4_top<C>(a);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+                for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-                for (int g = 0; g < C::NG; ++g) raw[k][g] = i4_scale(vw[k][g]);
-            dec_i4_move<C>(w, raw, s);
+                    for (int e = 0; e < 2; ++e) move |= fmaf(s[h][n][2 * k + e], w.mul[n][e], la) > w.m[n][e];
+            }
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int g = 0; g < C::NG; ++g) a[k][g] = raw[k][g] * w.inv[g];
-        }
+        for (int g = 0; g < C::NG; ++g) low = fminf(low, most[g]), high = fmaxf(high, most[g]);
+        move |= ((low < kI4Room / 256.f) & (key + C::KEYS <= L)) | (high > kI4Room * 256.f);
+        if (__any_sync(0xffffffffu, move)) dec_i4_move<C>(w, vw, s);
     }
     // weights, in place of the scores
 #pragma unroll
-    for (int n = 0; n < C::NT; ++n)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s[n][e] = ptx::ex2_approx(fmaf(s[n][e], w.mul[n][e & 1], -w.m[n][e & 1]));
-            w.l[n][e & 1] += s[n][e];
-        }
-    uint32_t raw[4];
+        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[h][n][e] = ptx::ex2_approx(fmaf(s[h][n][e], w.mul[n][e & 1], -w.m[n][e & 1]));
+                w.l[n][e & 1] += s[h][n][e];
+            }
+    uint32_t raw[H][4];
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
-        uint32_t pf[C::NT][2];
-        // keys 8 .. 15: code 15 - c, weight negated
-        const float z0 = i4_zero(vw[0][g]), z1 = 15.f - i4_zero(vw[1][g]);
+        uint32_t pf[H][C::NT][2];
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n) {
-            const uint32_t h0 = ptx::pack_f16x2(s[n][0] * a[0][g], s[n][1] * a[0][g]);
-            const uint32_t h1 = ptx::pack_f16x2(s[n][2] * -a[1][g], s[n][3] * -a[1][g]);
-            // the zeros meet the rounded weights, so that a weight's rounding is of its value's share only
-            const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
-            w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
-            w.zo[n][g][1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][1]));
-            pf[n][0] = movmatrix_trans(h0);
-            pf[n][1] = movmatrix_trans(h1);
+        for (int h = 0; h < H; ++h) {
+            // keys 8 .. 15 of a half: code 15 - c, weight negated
+            const float z0 = i4_zero(vw[h][0][g]), z1 = 15.f - i4_zero(vw[h][1][g]);
+            const float a0 = i4_scale(vw[h][0][g]) * w.inv[g], a1 = -i4_scale(vw[h][1][g]) * w.inv[g];
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n) {
+                const uint32_t h0 = ptx::pack_f16x2(s[h][n][0] * a0, s[h][n][1] * a0);
+                const uint32_t h1 = ptx::pack_f16x2(s[h][n][2] * a1, s[h][n][3] * a1);
+                // the zeros meet the rounded weights, so that a weight's rounding is of its value's share only
+                const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
+                w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
+                w.zo[n][g][1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][1]));
+                pf[h][n][0] = movmatrix_trans(h0);
+                pf[h][n][1] = movmatrix_trans(h1);
+            }
         }
 #pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
-            if (c % 2 == 0) ldmatrix_x4_trans((from.v + at) ^ (uint32_t)(c << 4), raw);
-            uint32_t lo = raw[c % 2 * 2], hi = raw[c % 2 * 2 + 1];
+            uint32_t lo[H], hi[H];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const uint32_t f[4] = {lo & 0x000f000fu, lo & 0x00f000f0u, ~hi & 0x000f000fu, ~hi & 0x00f000f0u};
-#pragma unroll
-                for (int n = 0; n < C::NT; ++n) mma_16816(w.o[n][c][x], f, pf[n][0], pf[n][1]);
-                lo >>= 8;
-                hi >>= 8;
+            for (int h = 0; h < H; ++h) {
+                if (c % 2 == 0) ldmatrix_x4_trans(((from.v + at) ^ (uint32_t)(c << 4)) + h * HALF, raw[h]);
+                lo[h] = raw[h][c % 2 * 2], hi[h] = raw[h][c % 2 * 2 + 1];
             }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const uint32_t f[4] = {lo[h] & 0x000f000fu, lo[h] & 0x00f000f0u, ~hi[h] & 0x000f000fu, ~hi[h] & 0x00f000f0u};
+#pragma unroll
+                    for (int n = 0; n < C::NT; ++n) mma_16816(w.o[n][c][x], f, pf[h][n][0], pf[h][n][1]);
+                    lo[h] >>= 8;
+                    hi[h] >>= 8;
+                }
         }
     }
 }
@@ -702,7 +739,7 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
     uint4 raw[C::NT][C::NC];
     dec_i4_load_q<C>(p, it, rg, lane, raw);
     // The warps take turns at the copies: tile n is copied by warp n of the first
-    // ST - 1, and tile t + ST - 1 by warp t % 8, behind its own keys of tile t;
+    // ST - 1, and tile t + ST - 1 by warp t % 4, behind its own keys of tile t;
     // the stage's last readers were busy with the tile in front of that.
     DecFp8It ahead = it;
     if (warp < C::ST - 1) {
@@ -716,7 +753,7 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
         dec_i4_advance(p, ahead, warp + C::ST - 1);
     }
     dec_i4_keep(ahead, lane, kept);
-    const DecI4Lane from = dec_i4_lane<C>(ring, lane, kwi * C::SPT * 16);
+    const DecI4Lane from = dec_i4_lane<C>(ring, lane, kwi * C::SPT * C::KEYS);
     const int back = p.mask_kind == kMaskCausal ? p.Sq - 1 : 0;
     DecI4Warp<C> w;
     dec_i4_begin_unit<C>(p, raw, lane, w);
@@ -734,12 +771,12 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
         }
         // (a warp whose wait ran out goes on without its tiles, so that the others meet it at the units' ends)
         if (!bad) bad = !wait_warp(bar_addr(bars, C::B_FULL + slot), phase, ctl, 92);
-        int key = it.tile * C::BN + kwi * C::SPT * 16;
+        int key = it.tile * C::BN + kwi * C::SPT * C::KEYS;
 #pragma unroll 1
-        for (int j = 0; j < C::SPT; ++j, key += 16) {
+        for (int j = 0; j < C::SPT; ++j, key += C::KEYS) {
             if (bad || key >= it.L) break;
             dec_i4_keys<C>(w, key, it.L, back, it.chunk * p.rows_per_chunk + rg * C::NT * 8, lane, from,
-                           slot * C::STAGE + j * 16 * C::ROW, slot * C::STAGE + j * 16 * C::NG * 4);
+                           slot * C::STAGE + j * C::KEYS * C::ROW, slot * C::STAGE + j * C::KEYS * C::NG * 4);
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_addr(bars, C::B_EMPTY + slot));
