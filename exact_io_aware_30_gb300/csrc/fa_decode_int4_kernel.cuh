@@ -68,6 +68,15 @@ struct DecI4Cfg {
     static constexpr int KEYS = 16 * H;
     static constexpr int BN = 128;
     static constexpr int SPT = BN / KEYS / KW;    // steps of a warp per tile
+    // Which key of a step stands in row i + 8k of the products of half h: SI i + SK k
+    // + SH h.  With two words to a key, 16 bytes hold those of two, and the order
+    // is such that the transposed words have the zeros where their products want
+    // them (see dec_i4_keys).
+    static constexpr int SI = D / G == 2 ? 2 : 1;
+    static constexpr int SK = D / G != 2 ? 8 : H == 2 ? 16 : 1;
+    static constexpr int SH = D / G != 2 ? 16 : 1;
+    static constexpr bool ZMMA = D / G >= 2;      // the zeros go through products
+    static constexpr int ZE = D / G == 2 ? 4 : 2; // sums of them a lane holds per group and eight rows
     static constexpr int NG = D / G;
     static constexpr int NC = D / 32;             // chunks of 32 components, 16 bytes
     static constexpr int ROW = D / 2;             // bytes of a row of codes
@@ -128,33 +137,34 @@ __device__ __forceinline__ void dec_i4_advance(const DecInt4Params &p, DecFp8It 
     }
 }
 
-// Lane 4k + j copies part j (K codes, V codes, K words, V words) of block k of
-// a tile: its table entry, or -1 where it has none to copy, -2 where the entry is
-// outside the pool.
+// Lane 4k + j copies part j (K codes, V codes, K words, V words) of block k of a
+// tile: whether there is such a block, and its table entry as loaded.  (Judged
+// when the copy begins, so that the load is not waited for here.)
 template <class C>
-__device__ __forceinline__ int dec_i4_entry(const DecInt4Params &p, const DecFp8It &it, int lane) {
-    const int blk = lane >> 2, n = ((it.tile * C::BN) >> p.bs_log2) + blk;
-    if (blk >= C::BN >> p.bs_log2 || it.left <= 0 || (n << p.bs_log2) >= it.L) return -1;
-    const int e = p.block_table[(size_t)it.b * p.max_blocks + n];
-    return e >= 0 && e < p.num_blocks ? e : -2;
+__device__ __forceinline__ bool dec_i4_entry(const DecInt4Params &p, const DecFp8It &it, int lane, int &entry) {
+    const int n = ((it.tile * C::BN) >> p.bs_log2) + (lane >> 2);
+    const bool some = lane >> 2 < C::BN >> p.bs_log2 && it.left > 0 && (n << p.bs_log2) < it.L;
+    entry = some ? p.block_table[(size_t)it.b * p.max_blocks + n] : 0;
+    return some;
 }
 
 // Copies a tile into a stage that is free.  The whole warp.  Slots behind the
 // request's blocks are not read later; a block outside the pool gets zero words,
 // whatever its codes.
 template <class C>
-__device__ __forceinline__ void dec_i4_copy(const DecInt4Params &p, int kvh, int entry, int lane, uint32_t stage, uint32_t bar) {
+__device__ __forceinline__ void dec_i4_copy(const DecInt4Params &p, int kvh, bool some, int entry, int lane, uint32_t stage, uint32_t bar) {
+    const bool in = some && entry >= 0 && entry < p.num_blocks;
     const int part = lane & 3, row = (lane >> 2) << p.bs_log2;
     const uint32_t word_bytes = (uint32_t)(C::NG * 4) << p.bs_log2;
     const uint32_t words_at = stage + (part & 1 ? C::O_VW : C::O_KW) + row * C::NG * 4;
-    if (entry == -2 && part >= 2) {
+    if (some && !in && part >= 2) {
         for (uint32_t i = 0; i < word_bytes; i += 16) ptx::st_shared_v4(words_at + i, 0u, 0u, 0u, 0u);
         ptx::fence_proxy_async_smem();
     }
-    const uint32_t blocks = (uint32_t)__popc(__ballot_sync(0xffffffffu, entry >= 0)) / 4;
+    const uint32_t blocks = (uint32_t)__popc(__ballot_sync(0xffffffffu, in)) / 4;
     if (lane == 0) ptx::mbar_arrive_expect_tx(bar, blocks * (2 * word_bytes + ((uint32_t)(2 * C::ROW) << p.bs_log2)));
     __syncwarp();
-    if (entry >= 0) {
+    if (in) {
         if (part < 2) {
             const uint64_t pol = p.chunks > 1 ? ptx::policy_evict_last() : ptx::policy_evict_first();
             ptx::tma_load_4d(stage + (part ? C::O_V : 0) + row * C::ROW, part ? &p.tm_v : &p.tm_k, bar, 0, 0, kvh, entry, pol);
@@ -188,6 +198,14 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+__device__ __forceinline__ void ldmatrix_x2_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+
+__device__ __forceinline__ void ldmatrix_x1_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x1.trans.shared.b16 {%0}, [%1];" : "=r"(r[0]) : "r"(addr));
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
@@ -233,7 +251,7 @@ struct DecI4Warp {
     float l[C::NT][2];               // this lane's sums of weights
     float inv[C::NG];                // kI4Room / ref of the groups' V scales, a power of two; 0 before the first
     float o[C::NT][C::NC][2][4];     // sums of weights times codes
-    float zo[C::NT][C::NG][2];       // this lane's sums of weights times zeros
+    float zo[C::NT][C::NG][C::ZE];   // sums of weights times zeros: this lane's share, or as the products leave them
 };
 
 constexpr float kI4None = -3.402823466e38f;  // the reference before the first key
@@ -320,7 +338,9 @@ __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const 
             w.m[n][e] = kI4None;
             w.l[n][e] = 0.f;
 #pragma unroll
-            for (int g = 0; g < C::NG; ++g) w.zo[n][g][e] = 0.f;
+            for (int g = 0; g < C::NG; ++g)
+#pragma unroll
+                for (int z = e; z < C::ZE; z += 2) w.zo[n][g][z] = 0.f;
         }
 #pragma unroll
         for (int c = 0; c < C::NC; ++c)
@@ -378,7 +398,8 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         most = fmaxf(most, 16777216.f * fmaxf(fabsf(w.o[n][c][0][e]), fabsf(w.o[n][c][1][e])));
-                most = fmaxf(most, fmaxf(fabsf(w.zo[n][g][0]), fabsf(w.zo[n][g][1])));
+#pragma unroll
+                for (int z = 0; z < C::ZE; ++z) most = fmaxf(most, fabsf(w.zo[n][g][z]));
             }
             most = warp_max(most);
             const uint32_t room = 200u - min(__float_as_uint(most) >> 23, 200u);  // up to 2^73
@@ -395,8 +416,8 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) w.o[n][c][h][e] *= factor;
-                w.zo[n][g][0] *= factor;
-                w.zo[n][g][1] *= factor;
+#pragma unroll
+                for (int z = 0; z < C::ZE; ++z) w.zo[n][g][z] *= factor;
             }
         }
         rise = fmaxf(rise, lg2_approx(factor));
@@ -428,7 +449,9 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
             w.m[n][e] = now;
             w.l[n][e] *= f;
 #pragma unroll
-            for (int g = 0; g < C::NG; ++g) w.zo[n][g][e] *= f;
+            for (int g = 0; g < C::NG; ++g)
+#pragma unroll
+                for (int z = e; z < C::ZE; z += 2) w.zo[n][g][z] *= f;
 #pragma unroll
             for (int c = 0; c < C::NC; ++c)
 #pragma unroll
@@ -439,20 +462,23 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
         }
 }
 
-// What a lane reads of a stage at its warp's first step: K words, V matrices, words of its keys.
+// What a lane reads of a stage at its warp's first step: K words, V matrices,
+// words of its keys, words as matrices.
 struct DecI4Lane {
-    uint32_t k, v, w;
+    uint32_t k, v, w, z;
 };
 
 template <class C>
 __device__ __forceinline__ DecI4Lane dec_i4_lane(uint32_t ring, int lane, int first) {
     // 16-byte chunk c of row r of a box is chunk c ^ swizzle(r)
     auto swizzle = [](int r) { return C::ROW == 128 ? r & 7 : C::ROW == 64 ? (r >> 1) & 3 : (r >> 2) & 1; };
-    const int i = lane >> 2, t = lane & 3, v_row = lane & 15;
+    const int k_row = C::SI * (lane >> 2), v_row = C::SI * (lane & 7) + C::SK * (lane >> 3 & 1);
+    const int z_row = C::NG == 2 ? 2 * (lane & 15) : (lane & 7) + 8 * (lane >> 3 & 1) + (C::H == 2 ? 16 * (lane >> 4) : 0);
     DecI4Lane x;
-    x.k = ring + (first + i) * C::ROW + (swizzle(i) << 4) + 4 * t;
+    x.k = ring + (first + k_row) * C::ROW + (swizzle(k_row) << 4) + 4 * (lane & 3);
     x.v = ring + C::O_V + (first + v_row) * C::ROW + ((swizzle(v_row) ^ (lane >> 4)) << 4);
-    x.w = ring + C::O_KW + (first + i) * C::NG * 4;
+    x.w = ring + C::O_KW + (first + k_row) * C::NG * 4;
+    x.z = ring + C::O_VW + (first + z_row) * C::NG * 4;
     return x;
 }
 
@@ -462,12 +488,13 @@ __device__ __forceinline__ DecI4Lane dec_i4_lane(uint32_t ring, int lane, int fi
 template <class C>
 __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int back, int row0, int lane, const DecI4Lane &from,
                                             uint32_t at, uint32_t at_words) {
-    constexpr int H = C::H, HALF = 16 * C::ROW, ROW_W = C::NG * 4;
+    constexpr int H = C::H, ROW_W = C::NG * 4;
+    constexpr int HALF = C::SH * C::ROW, OTHER = C::SK * C::ROW;  // to the second half, and to row i + 8
     const uint32_t words = from.w + at_words;
     if (key + C::KEYS > L) {  // slots past the request's tokens may hold anything: their words become 0
         const int mine = lane & (C::KEYS - 1);
         if (key + mine >= L) {
-            const uint32_t row = words + (mine - (lane >> 2)) * ROW_W + (C::KEYS == 16 && lane >= 16 ? C::WORDS : 0);
+            const uint32_t row = words + (mine - C::SI * (lane >> 2)) * ROW_W + (C::KEYS == 16 && lane >= 16 ? C::WORDS : 0);
 #pragma unroll
             for (int g = 0; g < C::NG; ++g) {
                 sts32(row + 4 * g, 0u);
@@ -481,7 +508,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + (16 * h + 8 * k) * ROW_W, kw[h][k]);
+        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + (C::SH * h + C::SK * k) * ROW_W, kw[h][k]);
     float s[H][C::NT][4];
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
@@ -497,7 +524,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
             const uint32_t place = (from.k + at) ^ (uint32_t)(c << 4);
             uint32_t a[H], b[H];
 #pragma unroll
-            for (int h = 0; h < H; ++h) a[h] = lds32(place + h * HALF), b[h] = lds32(place + h * HALF + 8 * C::ROW);
+            for (int h = 0; h < H; ++h) a[h] = lds32(place + h * HALF), b[h] = lds32(place + h * HALF + OTHER);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -522,7 +549,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + C::WORDS + (16 * h + 8 * k) * ROW_W, vw[h][k]);
+        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + C::WORDS + (C::SH * h + C::SK * k) * ROW_W, vw[h][k]);
     // hidden keys: past the row's last (a select, so nothing of theirs leaks)
     if (key + C::KEYS > L - back) {
 #pragma unroll
@@ -534,9 +561,10 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                 for (int h = 0; h < H; ++h)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        if (key + (lane >> 2) + 16 * h + 8 * k > row_last) s[h][n][2 * k + e] = -INFINITY;
+                        if (key + C::SI * (lane >> 2) + C::SH * h + C::SK * k > row_last) s[h][n][2 * k + e] = -INFINITY;
             }
     }
+    float a[H][2][C::NG];  // the keys' V scales over their references
     {
         bool move = false;
         float low = INFINITY, high = 0.f;  // of the groups' largest scales of the lane's keys
@@ -547,13 +575,12 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
         for (int h = 0; h < H; ++h)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                float a[C::NG];
 #pragma unroll
                 for (int g = 0; g < C::NG; ++g) {
-                    a[g] = i4_scale(vw[h][k][g]) * w.inv[g];
-                    most[g] = fmaxf(most[g], a[g]);
+                    a[h][k][g] = i4_scale(vw[h][k][g]) * w.inv[g];
+                    most[g] = fmaxf(most[g], a[h][k][g]);
                 }
-                const float la = dec_i4_top<C>(a);
+                const float la = dec_i4_top<C>(a[h][k]);
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -562,7 +589,15 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
         for (int g = 0; g < C::NG; ++g) low = fminf(low, most[g]), high = fmaxf(high, most[g]);
         move |= ((low < kI4Room / 256.f) & (key + C::KEYS <= L)) | (high > kI4Room * 256.f);
-        if (__any_sync(0xffffffffu, move)) dec_i4_move<C>(w, vw, s);
+        if (__any_sync(0xffffffffu, move)) {
+            dec_i4_move<C>(w, vw, s);
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int g = 0; g < C::NG; ++g) a[h][k][g] = i4_scale(vw[h][k][g]) * w.inv[g];
+        }
     }
     // weights, in place of the scores
 #pragma unroll
@@ -574,26 +609,71 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                 s[h][n][e] = ptx::ex2_approx(fmaf(s[h][n][e], w.mul[n][e & 1], -w.m[n][e & 1]));
                 w.l[n][e & 1] += s[h][n][e];
             }
+    // The zeros: sum B z over keys 0 .. 7 of a half, and sum B (15 - z) over keys 8
+    // .. 15, whose weights B are negated.  The words, transposed, are a first
+    // factor's registers as they are: row 2g has the zeros of group g (modulo
+    // four), row 2g + 1 bits of scales, which nobody reads.  15 comes from a register
+    // of rows that are else empty.  With two words to a key the 16 bytes of a row
+    // are two keys', so rows 0 and 2 are even keys' and 4 and 6 odd keys'.
+    constexpr uint32_t kMinus = 0x80008000u, kFifteen = 0x4b804b80u;
+    uint32_t zr[C::NG > 4 ? 2 : 1][4];
+    if constexpr (C::ZMMA) {
+        if constexpr (C::NG == 2 && H == 1) ldmatrix_x1_trans(from.z + at_words, zr[0]);
+        else if constexpr (C::NG == 2 || H == 1) {
+            ldmatrix_x2_trans(from.z + at_words, zr[0]);
+            if constexpr (C::NG > 4) ldmatrix_x2_trans(from.z + at_words + 16, zr[1]);
+        } else {
+            ldmatrix_x4_trans(from.z + at_words, zr[0]);
+            static_assert(C::NG <= 4 || H == 1, "two halves of at most four words to a key");
+        }
+    }
     uint32_t raw[H][4];
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
         uint32_t pf[H][C::NT][2];
+        float zs[C::NT][4];
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) zs[n][e] = 0.f;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             // keys 8 .. 15 of a half: code 15 - c, weight negated
-            const float z0 = i4_zero(vw[h][0][g]), z1 = 15.f - i4_zero(vw[h][1][g]);
-            const float a0 = i4_scale(vw[h][0][g]) * w.inv[g], a1 = -i4_scale(vw[h][1][g]) * w.inv[g];
+            const float a0 = a[h][0][g], a1 = -a[h][1][g];
 #pragma unroll
             for (int n = 0; n < C::NT; ++n) {
                 const uint32_t h0 = ptx::pack_f16x2(s[h][n][0] * a0, s[h][n][1] * a0);
                 const uint32_t h1 = ptx::pack_f16x2(s[h][n][2] * a1, s[h][n][3] * a1);
-                // the zeros meet the rounded weights, so that a weight's rounding is of its value's share only
-                const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
-                w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
-                w.zo[n][g][1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][1]));
                 pf[h][n][0] = movmatrix_trans(h0);
                 pf[h][n][1] = movmatrix_trans(h1);
+                // (the zeros meet the rounded weights, so that a weight's rounding is of its value's share only)
+                if constexpr (!C::ZMMA) {
+                    const float z0 = i4_zero(vw[h][0][g]), z1 = 15.f - i4_zero(vw[h][1][g]);
+                    const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
+                    w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
+                    w.zo[n][g][1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][1]));
+                } else if constexpr (C::NG == 2 && H == 1) {
+                    const uint32_t f[4] = {zr[0][0], 0u, kFifteen, zr[0][0] ^ kMinus};
+                    mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
+                } else if constexpr (C::NG == 2) {
+                    if (h == 0) {
+                        const uint32_t f[4] = {zr[0][0], 0u, zr[0][1] ^ kMinus, kFifteen};
+                        mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
+                    } else {
+                        const uint32_t f[4] = {0u, zr[0][0], kFifteen, zr[0][1] ^ kMinus};
+                        mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
+                    }
+                } else {
+                    const uint32_t f[4] = {zr[g / 4][2 * h], 0u, zr[g / 4][2 * h + 1] ^ kMinus, kFifteen};
+                    mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
+                }
             }
+        }
+        if constexpr (C::ZMMA) {
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w.zo[n][g][e % C::ZE] += zs[n][e];
         }
 #pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
@@ -642,8 +722,13 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
 #pragma unroll
             for (int g = 0; g < C::NG; ++g) {
                 float z = w.zo[n][g][e];
+                if constexpr (!C::ZMMA) {
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                    for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                } else {  // row 2g of the products (and row 12 + 2g)
+                    z = __shfl_sync(0xffffffffu, z, 8 * (g & 3) + t);
+                    if constexpr (C::ZE == 4) z += __shfl_sync(0xffffffffu, w.zo[n][g][2 + e], 16 + 8 * g + t);
+                }
                 // (the sums are kI4Room / ref too large)
                 const uint32_t inv = __float_as_uint(w.inv[g]);
                 const float ref = inv == 0 ? 0.f : __uint_as_float((254u << 23) - inv);
@@ -746,7 +831,9 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
         dec_i4_advance(p, ahead, warp);
         if (ahead.left > 0) {
             if (lane == 0) atomicMax(copied, warp + 1);
-            dec_i4_copy<C>(p, ahead.kvh, dec_i4_entry<C>(p, ahead, lane), lane, ring + warp * C::STAGE, bar_addr(bars, C::B_FULL + warp));
+            int entry;
+            const bool some = dec_i4_entry<C>(p, ahead, lane, entry);
+            dec_i4_copy<C>(p, ahead.kvh, some, entry, lane, ring + warp * C::STAGE, bar_addr(bars, C::B_FULL + warp));
         }
         dec_i4_advance(p, ahead, C::ST - 1);
     } else {
@@ -763,11 +850,12 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
     uint32_t phase = 0;
     int t = 0;
     for (;;) {
-        int entry = -1, kvh = 0;
+        int entry = 0, kvh = 0;
+        bool some = false;
         if (turn == 0) {
             const DecFp8It coming = dec_i4_take(kept);
             kvh = coming.left > 0 ? coming.kvh : -1;
-            entry = dec_i4_entry<C>(p, coming, lane);
+            some = dec_i4_entry<C>(p, coming, lane, entry);
         }
         // (a warp whose wait ran out goes on without its tiles, so that the others meet it at the units' ends)
         if (!bad) bad = !wait_warp(bar_addr(bars, C::B_FULL + slot), phase, ctl, 92);
@@ -788,7 +876,7 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
                 bad = t > 0 && !wait_warp(bar_addr(bars, C::B_EMPTY + prev), slot == 0 ? phase ^ 1 : phase, ctl, 91);
                 if (!bad) {
                     if (lane == 0) atomicMax(copied, t + C::ST);
-                    dec_i4_copy<C>(p, kvh, entry, lane, ring + prev * C::STAGE, bar_addr(bars, C::B_FULL + prev));
+                    dec_i4_copy<C>(p, kvh, some, entry, lane, ring + prev * C::STAGE, bar_addr(bars, C::B_FULL + prev));
                     DecFp8It coming = dec_i4_take(kept);
                     dec_i4_advance(p, coming, C::WARPS);
                     dec_i4_keep(coming, lane, kept);
@@ -819,8 +907,7 @@ template <class C>
 __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     fa_decode_int4_kernel(const __grid_constant__ DecInt4Params p) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *ring = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *ring = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *parts = ring + C::ST * C::STAGE;
     DecI4Kept *kept = reinterpret_cast<DecI4Kept *>(parts + C::PARTS * C::PART);
     uint64_t *bar_mem = reinterpret_cast<uint64_t *>(kept + C::WARPS);
