@@ -42,58 +42,79 @@ struct Int4AppendParams {
 // of fp32 is 1.
 __device__ __forceinline__ float round_even(float y) { return (y + 12582912.f) - 12582912.f; }
 
-// 8 values of a group, rounded to the group's grid as whole numbers.  The
-// quotient is x times 1 / s, corrected once by its own remainder (Markstein's
-// step), which makes it exact wherever it has few bits, halves among them: so
-// ties are found.  A quotient that is no tie is at least 2^-13 of a step away
-// from one (x has at most 11 bits and s 8), far more than the quotient is off.
-__device__ __forceinline__ float int4_grid(float x, float s, float inv) {
+// x / d by a rounded inverse of d and one correction by the quotient's own
+// remainder (Markstein's step): the correctly rounded quotient wherever it has
+// few bits, and else within the last place.  |d| and |x| far from the ends of
+// fp32's range.
+__device__ __forceinline__ float quotient(float x, float d, float inv) {
     const float y = x * inv;
-    return round_even(fmaf(fmaf(-y, s, x), inv, y));
+    return fmaf(fmaf(-y, d, x), inv, y);
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The larger (smaller) of each half; NaN if either is.
 template <bool kFP16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (kFP16) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool kFP16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (kFP16) asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 struct Int4Group {
     uint32_t codes;  // of the thread's 8 values
     uint32_t word;
 };
 
-// Quantises the 8 values of each thread; 1 << lanes_log2 adjacent threads hold a group.
+// Quantises the 8 values of each thread; 1 << lanes_log2 adjacent threads hold a
+// group.  What bounds it is instructions, so the extremes are found two values at
+// a time in 16 bits, and a division is three steps: ties are found all the same,
+// as a quotient x / s that is a half has few bits, and one that is not is at
+// least 2^-13 away from one (x has at most 11 bits and s 8).
 template <bool kFP16>
-__device__ __forceinline__ Int4Group<kFP16> int4_quantise(uint4 v, int lanes_log2) {
+__device__ __forceinline__ Int4Group int4_quantise(uint4 v, int lanes_log2) {
     constexpr uint32_t kInf = kFP16 ? 0x7c00u : 0x7f80u;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float x[8];
+    const uint32_t top2 = max2<kFP16>(max2<kFP16>(w[0], w[1]), max2<kFP16>(w[2], w[3]));
+    const uint32_t bottom2 = min2<kFP16>(min2<kFP16>(w[0], w[1]), min2<kFP16>(w[2], w[3]));
+    // low half: the largest; high half: the smallest, negated
+    uint32_t ends = max2<kFP16>(__byte_perm(top2, bottom2, 0x5410) ^ 0x80000000u, __byte_perm(top2, bottom2, 0x7632) ^ 0x80000000u);
+    for (int i = 0; i < lanes_log2; ++i) ends = max2<kFP16>(ends, __shfl_xor_sync(0xffffffffu, ends, 1 << i));
+    Int4Group out;
+    out.codes = 0;
+    out.word = 0x7fc00000u;
+    if (max(ends & 0x7fffu, ends >> 16 & 0x7fffu) >= kInf) return out;
+    const float2 hl = unpack16<kFP16>(ends);
+    const float hi = hl.x, lo = -hl.y;
+    // (hi - lo) / 15, from sixteenths so that the difference cannot overflow
+    const float wide = hi * 0.0625f - lo * 0.0625f, most = fmaxf(fabsf(hi), fabsf(lo));
+    const bool small = most < 2.58493941e-26f;  // 2^-85: below, the steps of a quotient might leave the normal numbers
+    const float t = fmaxf(small ? __fdiv_rn(wide, 0.9375f) : quotient(wide, 0.9375f, 1.06666672f), most * 0.00048828125f);
+    const float s = __uint_as_float((__float_as_uint(t) + 0xffffu) & 0xffff0000u);
+    float x[8], n[8], base;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = unpack16<kFP16>(w[i]);
         x[2 * i] = f.x;
         x[2 * i + 1] = f.y;
     }
-    const uint32_t mag = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                  __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-    float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
-    float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    if (max(mag & 0xffffu, mag >> 16) >= kInf) hi = INFINITY;  // (finite values stay below it)
-    for (int i = 0; i < lanes_log2; ++i) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1 << i));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1 << i));
-    }
-    Int4Group<kFP16> out;
-    if (hi == INFINITY) {
-        out.codes = 0;
-        out.word = 0x7fc00000u;
-        return out;
-    }
-    // (hi - lo) / 15, from sixteenths so that the difference cannot overflow
-    const float t = fmaxf(__fdiv_rn(hi * 0.0625f - lo * 0.0625f, 0.9375f), fmaxf(fabsf(hi), fabsf(lo)) * 0.00048828125f);
-    const float s = __uint_as_float((__float_as_uint(t) + 0xffffu) & 0xffff0000u);
-    float n[8], base;
-    if (s > 8.67361738e-19f) {  // 2^-60: no part of the quotient's steps is below the normal numbers
-        const float inv = __fdiv_rn(1.f, s);
+    if (!small) {
+        const float inv = rcp_approx(s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = int4_grid(x[i], s, inv);
-        base = int4_grid(lo, s, inv);
+        for (int i = 0; i < 8; ++i) n[i] = round_even(quotient(x[i], s, inv));
+        base = round_even(quotient(lo, s, inv));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) n[i] = s > 0.f ? round_even(__fdiv_rn(x[i], s)) : 0.f;
@@ -156,7 +177,7 @@ __global__ void __launch_bounds__(kInt4Threads) fa_cache_append_int4_kernel(cons
         for (int u = 0; u < U; ++u) {
             if (r0 + u * rows_at_once >= rows) break;  // (the same in the whole CTA)
             const int r = r0 + u * rows_at_once + lane_row;
-            const Int4Group<kFP16> q = int4_quantise<kFP16>(held[u], p.g_log2 - 3);
+            const Int4Group q = int4_quantise<kFP16>(held[u], p.g_log2 - 3);
             if (!have || r >= rows || s_slot[r] < 0 || s_late[r]) continue;
             const int slot = s_slot[r];
             const long long at = ((((long long)(slot >> p.bs_log2) * p.Hkv + head) << p.bs_log2) + (slot & ((1 << p.bs_log2) - 1)));
