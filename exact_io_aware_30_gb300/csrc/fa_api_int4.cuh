@@ -36,7 +36,7 @@ bool int4_aligned(const Int4Cache &c) {
 // Threads along a row's items (the smallest power of two that holds them, at
 // most a CTA's) and CTAs along them.
 void int4_items(int per_row, int *items_log2, unsigned *grid_y) {
-    *items_log2 = 4;
+    *items_log2 = 3;
     while (*items_log2 < 8 && 1 << *items_log2 < per_row) ++*items_log2;
     *grid_y = (unsigned)((per_row + (1 << *items_log2) - 1) >> *items_log2);
 }
@@ -90,12 +90,13 @@ fa_status cache_append_int4_impl(const void *k, const void *v, long long k_token
     p.g_log2 = group == 32 ? 5 : 6;
     p.bs_log2 = block_size_log2(block_size);
     unsigned y = 1;
-    int4_items(2 * Hkv * (d / 8), &p.items_log2, &y);
-    // Rows per CTA: its threads' one row each, and more until the grid is at most
-    // four waves of eight CTAs per SM.
+    int4_items(2 * Hkv * (d / 16), &p.items_log2, &y);
+    // Rows per CTA: one per thread, and up to sixteen while the grid has more than
+    // eight CTAs per SM (8,203 rows x 8 heads at d 128: one 19.9 us, eight 17.5, sixteen
+    // 16.3; 40,008 rows at d 256: 64 138 us, sixteen 112, eight 111).
     p.rows_per_cta = std::min(kInt4Threads >> p.items_log2, kInt4MaxRows);
-    while (p.rows_per_cta < kInt4MaxRows &&
-           (long long)((T + p.rows_per_cta - 1) / p.rows_per_cta) * y > 32LL * info->num_sms)
+    while (p.rows_per_cta < 16 * (kInt4Threads >> p.items_log2) && p.rows_per_cta < kInt4MaxRows &&
+           (long long)((T + p.rows_per_cta - 1) / p.rows_per_cta) * y > 8LL * info->num_sms)
         p.rows_per_cta *= 2;
     const dim3 grid((unsigned)((T + p.rows_per_cta - 1) / p.rows_per_cta), y);
     long long bits = (long long)(kp | vp);
@@ -215,15 +216,15 @@ bool make_map_int4_codes(CUtensorMap *m, const void *base, int d, int bs, int Hk
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a K/V head: at most 8 (a warp's columns), 16, or 32 in equal chunks of
+// Rows of a K/V head: at most 4, 8 (a warp's columns), 16, or 32 in equal chunks of
 // at most that, the cache being read once more per chunk.
 DecFp8Plan plan_decode_int4(int B, int Hkv, int R, int d, int max_seq_len, int num_sms) {
     DecFp8Plan pl;
     pl.chunks = (R + 31) / 32;
     pl.rows_per_chunk = (R + pl.chunks - 1) / pl.chunks;
     pl.chunks = (R + pl.rows_per_chunk - 1) / pl.rows_per_chunk;
-    pl.rc = pl.rows_per_chunk <= 8 ? 8 : pl.rows_per_chunk <= 16 ? 16 : 32;
-    const int per_sm = d <= 128 && pl.rc == 8 ? 3 : 2;
+    pl.rc = pl.rows_per_chunk <= 4 ? 4 : pl.rows_per_chunk <= 8 ? 8 : pl.rows_per_chunk <= 16 ? 16 : 32;
+    const int per_sm = d <= 128 && pl.rc <= 8 ? 3 : 2;
     const long long tiles = (max_seq_len + 127LL) / 128;
     const long long units = (long long)B * Hkv * pl.chunks;
     pl.cuts = tiles > kDecFp8WholeTiles;
@@ -238,8 +239,8 @@ DecFp8Plan plan_decode_int4(int B, int Hkv, int R, int d, int max_seq_len, int n
 
 template <class C>
 fa_status launch_decode_int4_c(const DecInt4Params &p, const DecFp8Plan &pl, DeviceInfo &info, cudaStream_t stream) {
-    constexpr int kind = C::RC == 8 ? 0 : C::RC == 16 ? 1 : 2;
-    const int slot = ((C::D == 256 ? 2 : C::D == 128 ? 1 : 0) * 2 + (C::G == 64 ? 1 : 0)) * 3 + kind;
+    constexpr int kind = C::RC == 4 ? 0 : C::RC == 8 ? 1 : C::RC == 16 ? 2 : 3;
+    const int slot = ((C::D == 256 ? 2 : C::D == 128 ? 1 : 0) * 2 + (C::G == 64 ? 1 : 0)) * 4 + kind;
     if (set_smem(fa_decode_int4_kernel<C>, C::SMEM_BYTES, info.attr_dec_int4[slot]) != FA_OK) return FA_ERR_CUDA;
     const fa_status st = launch_overlapped(fa_decode_int4_kernel<C>, dim3((unsigned)pl.grid), C::NUM_THREADS, C::SMEM_BYTES,
                                            1, stream, p);
@@ -253,6 +254,7 @@ fa_status launch_decode_int4_c(const DecInt4Params &p, const DecFp8Plan &pl, Dev
 template <int D, int G>
 fa_status launch_decode_int4(const DecInt4Params &p, const DecFp8Plan &pl, DeviceInfo &info, cudaStream_t stream) {
     constexpr int NT = D == 256 ? 1 : 2;
+    if (pl.rc == 4) return launch_decode_int4_c<DecI4Cfg<D, G, 1, 1, true>>(p, pl, info, stream);
     if (pl.rc == 8) return launch_decode_int4_c<DecI4Cfg<D, G, 1, 1>>(p, pl, info, stream);
     if (pl.rc == 16) return launch_decode_int4_c<DecI4Cfg<D, G, NT, 2 / NT>>(p, pl, info, stream);
     return launch_decode_int4_c<DecI4Cfg<D, G, NT, 4 / NT>>(p, pl, info, stream);

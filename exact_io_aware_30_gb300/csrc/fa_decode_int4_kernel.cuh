@@ -55,13 +55,17 @@ struct DecInt4Params : DecFp8Params {  // (k_scale and v_scale are not used)
     int fp16;
 };
 
-template <int D_, int G_, int NT_, int RG_>
+template <int D_, int G_, int NT_, int RG_, bool kFew_ = false>
 struct DecI4Cfg {
     static constexpr int D = D_;
     static constexpr int G = G_;                  // components per group
     static constexpr int NT = NT_;                // eights of rows per warp
     static constexpr int RG = RG_;                // groups of warps with different rows
-    static constexpr int RC = 8 * NT * RG;        // rows per unit
+    // Up to four rows stand in every other column of a product, so that a lane has
+    // one of them and the work on the weights halves.
+    static constexpr bool kFew = kFew_;
+    static constexpr int E = kFew ? 1 : 2;        // rows of each eight columns that are a lane's
+    static constexpr int RC = 4 * E * NT * RG;    // rows per unit
     static constexpr int WARPS = 4;
     static constexpr int KW = WARPS / RG;         // warps along a tile's keys
     static constexpr int H = D <= 128 && NT == 1 ? 2 : 1;  // 16-key halves of a step, side by side
@@ -76,7 +80,7 @@ struct DecI4Cfg {
     static constexpr int SK = D / G != 2 ? 8 : H == 2 ? 16 : 1;
     static constexpr int SH = D / G != 2 ? 16 : 1;
     static constexpr bool ZMMA = D / G >= 2;      // the zeros go through products
-    static constexpr int ZE = D / G == 2 ? 4 : 2; // sums of them a lane holds per group and eight rows
+    static constexpr int ZE = D / G == 2 ? 2 * E : E;  // sums of them a lane holds per group and eight rows
     static constexpr int NG = D / G;
     static constexpr int NC = D / 32;             // chunks of 32 components, 16 bytes
     static constexpr int ROW = D / 2;             // bytes of a row of codes
@@ -245,10 +249,10 @@ __device__ __forceinline__ float i4_zero(uint32_t w) {
 template <class C>
 struct DecI4Warp {
     uint32_t q[C::NT][C::NC][4];     // fragments of q
-    float q_sum[C::NT][C::NG][2];    // -2^-20 times the groups' sums of q
-    float mul[C::NT][2];             // from a sum of products to log2 units
-    float m[C::NT][2];               // reference of the exponents
-    float l[C::NT][2];               // this lane's sums of weights
+    float q_sum[C::NT][C::NG][C::E]; // -2^-20 times the groups' sums of q
+    float mul[C::NT][C::E];          // from a sum of products to log2 units
+    float m[C::NT][C::E];            // reference of the exponents
+    float l[C::NT][C::E];            // this lane's sums of weights
     float inv[C::NG];                // kI4Room / ref of the groups' V scales, a power of two; 0 before the first
     float o[C::NT][C::NC][2][4];     // sums of weights times codes
     float zo[C::NT][C::NG][C::ZE];   // sums of weights times zeros: this lane's share, or as the products leave them
@@ -268,11 +272,11 @@ __device__ __forceinline__ void dec_i4_load_q(const DecInt4Params &p, const DecF
     const size_t row0 = dec_fp8_row0(p, u.b, u.kvh, u.chunk, &rows);
 #pragma unroll
     for (int n = 0; n < C::NT; ++n) {
-        const int r = (rg * C::NT + n) * 8 + i;
+        const int r = C::kFew ? i >> 1 : (rg * C::NT + n) * 8 + i;
 #pragma unroll
         for (int c = 0; c < C::NC; ++c) {
             raw[n][c] = make_uint4(0, 0, 0, 0);
-            if (r < rows) raw[n][c] = *reinterpret_cast<const uint4 *>(p.q + (row0 + r) * C::D + 32 * c + 8 * t);
+            if (r < rows && !(C::kFew && (i & 1))) raw[n][c] = *reinterpret_cast<const uint4 *>(p.q + (row0 + r) * C::D + 32 * c + 8 * t);
         }
     }
 }
@@ -330,7 +334,7 @@ __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const 
             sum[g] = fine ? sum[g] * -9.5367431640625e-7f : 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < C::E; ++e) {
             const int from = (2 * t + e) * 4;
 #pragma unroll
             for (int g = 0; g < C::NG; ++g) w.q_sum[n][g][e] = __shfl_sync(0xffffffffu, sum[g], from);
@@ -340,7 +344,7 @@ __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const 
 #pragma unroll
             for (int g = 0; g < C::NG; ++g)
 #pragma unroll
-                for (int z = e; z < C::ZE; z += 2) w.zo[n][g][z] = 0.f;
+                for (int z = e; z < C::ZE; z += C::E) w.zo[n][g][z] = 0.f;
         }
 #pragma unroll
         for (int c = 0; c < C::NC; ++c)
@@ -368,7 +372,7 @@ __device__ __forceinline__ float dec_i4_top(const float (&a)[C::NG]) {
 // it) and rescales the sums.  vw: the V words of the lane's keys; s: their
 // scores' sums of products.  The whole warp.
 template <class C>
-__device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw)[C::H][2][C::NG], const float (&s)[C::H][C::NT][4]) {
+__device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw)[C::H][2][C::NG], const float (&s)[C::H][C::NT][2][C::E]) {
     float rise = -INFINITY;  // log2 of the factor of the group that grows most
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
@@ -435,11 +439,11 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < C::E; ++e) {
             float top = kI4None;
 #pragma unroll
             for (int h = 0; h < C::H; ++h)
-                top = fmaxf(top, fmaxf(fmaf(s[h][n][e], w.mul[n][e], la[h][0]), fmaf(s[h][n][2 + e], w.mul[n][e], la[h][1])));
+                top = fmaxf(top, fmaxf(fmaf(s[h][n][0][e], w.mul[n][e], la[h][0]), fmaf(s[h][n][1][e], w.mul[n][e], la[h][1])));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -451,7 +455,7 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
 #pragma unroll
             for (int g = 0; g < C::NG; ++g)
 #pragma unroll
-                for (int z = e; z < C::ZE; z += 2) w.zo[n][g][z] *= f;
+                for (int z = e; z < C::ZE; z += C::E) w.zo[n][g][z] *= f;
 #pragma unroll
             for (int c = 0; c < C::NC; ++c)
 #pragma unroll
@@ -509,7 +513,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
     for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + (C::SH * h + C::SK * k) * ROW_W, kw[h][k]);
-    float s[H][C::NT][4];
+    float s[H][C::NT][2][C::E];  // of keys i and i + 8 of a half, the lane's rows
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
         float acc[H][C::NT][4];
@@ -518,7 +522,11 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
             for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[h][n][e] = i4_zero(kw[h][e >> 1][g]) * w.q_sum[n][g][e & 1];
+                for (int k = 0; k < 2; ++k) {
+                    acc[h][n][2 * k + 1] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < C::E; ++e) acc[h][n][2 * k + e] = i4_zero(kw[h][k][g]) * w.q_sum[n][g][e];
+                }
 #pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
             const uint32_t place = (from.k + at) ^ (uint32_t)(c << 4);
@@ -541,9 +549,11 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
             for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float scale = i4_scale(kw[h][e >> 1][g]);
-                    s[h][n][e] = g == 0 ? scale * acc[h][n][e] : fmaf(scale, acc[h][n][e], s[h][n][e]);
+                for (int k = 0; k < 2; ++k) {
+                    const float scale = i4_scale(kw[h][k][g]);
+#pragma unroll
+                    for (int e = 0; e < C::E; ++e)
+                        s[h][n][k][e] = g == 0 ? scale * acc[h][n][2 * k + e] : fmaf(scale, acc[h][n][2 * k + e], s[h][n][k][e]);
                 }
     }
 #pragma unroll
@@ -555,13 +565,13 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row_last = back == 0 ? L - 1 : L - 1 - back + (row0 + 8 * n + 2 * (lane & 3) + e) % (back + 1);
+            for (int e = 0; e < C::E; ++e) {
+                const int row_last = back == 0 ? L - 1 : L - 1 - back + (row0 + 8 * n + C::E * (lane & 3) + e) % (back + 1);
 #pragma unroll
                 for (int h = 0; h < H; ++h)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        if (key + C::SI * (lane >> 2) + C::SH * h + C::SK * k > row_last) s[h][n][2 * k + e] = -INFINITY;
+                        if (key + C::SI * (lane >> 2) + C::SH * h + C::SK * k > row_last) s[h][n][k][e] = -INFINITY;
             }
     }
     float a[H][2][C::NG];  // the keys' V scales over their references
@@ -584,7 +594,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) move |= fmaf(s[h][n][2 * k + e], w.mul[n][e], la) > w.m[n][e];
+                    for (int e = 0; e < C::E; ++e) move |= fmaf(s[h][n][k][e], w.mul[n][e], la) > w.m[n][e];
             }
 #pragma unroll
         for (int g = 0; g < C::NG; ++g) low = fminf(low, most[g]), high = fmaxf(high, most[g]);
@@ -605,10 +615,12 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[h][n][e] = ptx::ex2_approx(fmaf(s[h][n][e], w.mul[n][e & 1], -w.m[n][e & 1]));
-                w.l[n][e & 1] += s[h][n][e];
-            }
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < C::E; ++e) {
+                    s[h][n][k][e] = ptx::ex2_approx(fmaf(s[h][n][k][e], w.mul[n][e], -w.m[n][e]));
+                    w.l[n][e] += s[h][n][k][e];
+                }
     // The zeros: sum B z over keys 0 .. 7 of a half, and sum B (15 - z) over keys 8
     // .. 15, whose weights B are negated.  The words, transposed, are a first
     // factor's registers as they are: row 2g has the zeros of group g (modulo
@@ -642,8 +654,8 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
             const float a0 = a[h][0][g], a1 = -a[h][1][g];
 #pragma unroll
             for (int n = 0; n < C::NT; ++n) {
-                const uint32_t h0 = ptx::pack_f16x2(s[h][n][0] * a0, s[h][n][1] * a0);
-                const uint32_t h1 = ptx::pack_f16x2(s[h][n][2] * a1, s[h][n][3] * a1);
+                const uint32_t h0 = ptx::pack_f16x2(s[h][n][0][0] * a0, C::kFew ? 0.f : s[h][n][0][C::E - 1] * a0);
+                const uint32_t h1 = ptx::pack_f16x2(s[h][n][1][0] * a1, C::kFew ? 0.f : s[h][n][1][C::E - 1] * a1);
                 pf[h][n][0] = movmatrix_trans(h0);
                 pf[h][n][1] = movmatrix_trans(h1);
                 // (the zeros meet the rounded weights, so that a weight's rounding is of its value's share only)
@@ -651,7 +663,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                     const float z0 = i4_zero(vw[h][0][g]), z1 = 15.f - i4_zero(vw[h][1][g]);
                     const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
                     w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
-                    w.zo[n][g][1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][1]));
+                    if constexpr (!C::kFew) w.zo[n][g][C::E - 1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][C::E - 1]));
                 } else if constexpr (C::NG == 2 && H == 1) {
                     const uint32_t f[4] = {zr[0][0], 0u, kFifteen, zr[0][0] ^ kMinus};
                     mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
@@ -673,7 +685,9 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
             for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w.zo[n][g][e % C::ZE] += zs[n][e];
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int e = 0; e < C::E; ++e) w.zo[n][g][(k * C::E + e) % C::ZE] += zs[n][2 * k + e];
         }
 #pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
@@ -716,7 +730,7 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < C::E; ++e) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) w.l[n][e] += __shfl_xor_sync(0xffffffffu, w.l[n][e], o);
 #pragma unroll
@@ -727,7 +741,7 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
                     for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
                 } else {  // row 2g of the products (and row 12 + 2g)
                     z = __shfl_sync(0xffffffffu, z, 8 * (g & 3) + t);
-                    if constexpr (C::ZE == 4) z += __shfl_sync(0xffffffffu, w.zo[n][g][2 + e], 16 + 8 * g + t);
+                    if constexpr (C::ZE == 2 * C::E) z += __shfl_sync(0xffffffffu, w.zo[n][g][C::ZE - C::E + e], 16 + 8 * g + t);
                 }
                 // (the sums are kI4Room / ref too large)
                 const uint32_t inv = __float_as_uint(w.inv[g]);
@@ -749,7 +763,7 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
             if (kwi >= half && kwi < 2 * half) {
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n) {
-                    at[(2 * C::NT * C::NC + n) * 32] = make_float4(w.m[n][0], w.m[n][1], w.l[n][0], w.l[n][1]);
+                    at[(2 * C::NT * C::NC + n) * 32] = make_float4(w.m[n][0], w.m[n][C::E - 1], w.l[n][0], w.l[n][C::E - 1]);
 #pragma unroll
                     for (int c = 0; c < C::NC; ++c)
 #pragma unroll
@@ -763,23 +777,27 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n) {
                     const float4 ml = at[(2 * C::NT * C::NC + n) * 32];
-                    const float m0 = fmaxf(w.m[n][0], ml.x), m1 = fmaxf(w.m[n][1], ml.y);
-                    const float a0 = ptx::ex2_approx(w.m[n][0] - m0), b0 = ptx::ex2_approx(ml.x - m0);
-                    const float a1 = ptx::ex2_approx(w.m[n][1] - m1), b1 = ptx::ex2_approx(ml.y - m1);
-                    w.m[n][0] = m0;
-                    w.m[n][1] = m1;
-                    w.l[n][0] = fmaf(w.l[n][0], a0, ml.z * b0);
-                    w.l[n][1] = fmaf(w.l[n][1], a1, ml.w * b1);
+                    float mine[C::E], theirs[C::E];  // what the two sides' sums are multiplied by
+#pragma unroll
+                    for (int e = 0; e < C::E; ++e) {
+                        const float m = e ? ml.y : ml.x, top = fmaxf(w.m[n][e], m);
+                        mine[e] = ptx::ex2_approx(w.m[n][e] - top);
+                        theirs[e] = ptx::ex2_approx(m - top);
+                        w.m[n][e] = top;
+                        w.l[n][e] = fmaf(w.l[n][e], mine[e], (e ? ml.w : ml.z) * theirs[e]);
+                    }
 #pragma unroll
                     for (int c = 0; c < C::NC; ++c)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const float4 y = at[((n * C::NC + c) * 2 + x) * 32];
                             float(&o)[4] = w.o[n][c][x];
-                            o[0] = fmaf(o[0], a0, y.x * b0);
-                            o[1] = fmaf(o[1], a1, y.y * b1);
-                            o[2] = fmaf(o[2], a0, y.z * b0);
-                            o[3] = fmaf(o[3], a1, y.w * b1);
+                            o[0] = fmaf(o[0], mine[0], y.x * theirs[0]);
+                            o[2] = fmaf(o[2], mine[0], y.z * theirs[0]);
+                            if constexpr (!C::kFew) {
+                                o[1] = fmaf(o[1], mine[C::E - 1], y.y * theirs[C::E - 1]);
+                                o[3] = fmaf(o[3], mine[C::E - 1], y.w * theirs[C::E - 1]);
+                            }
                         }
                 }
             }
@@ -792,8 +810,8 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = (rg * C::NT + n) * 8 + 2 * t + e;
+        for (int e = 0; e < C::E; ++e) {
+            const int r = (rg * C::NT + n) * 8 + C::E * t + e;
             if (r >= rows) continue;
             const float l = w.l[n][e], inv = l == 0.f ? 0.f : 1.f / l;
             const float lse2 = l == 0.f ? -INFINITY : w.m[n][e] + __log2f(l);  // (a NaN sum is no empty row)

@@ -74,26 +74,26 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
 }
 
 struct Int4Group {
-    uint32_t codes;  // of the thread's 8 values
+    uint32_t codes[2];  // of the thread's 16 values
     uint32_t word;
 };
 
-// Quantises the 8 values of each thread; 1 << lanes_log2 adjacent threads hold a
+// Quantises the 16 values of each thread; 1 << lanes_log2 adjacent threads hold a
 // group.  What bounds it is instructions, so the extremes are found two values at
 // a time in 16 bits, and a division is three steps: ties are found all the same,
 // as a quotient x / s that is a half has few bits, and one that is not is at
 // least 2^-13 away from one (x has at most 11 bits and s 8).
 template <bool kFP16>
-__device__ __forceinline__ Int4Group int4_quantise(uint4 v, int lanes_log2) {
+__device__ __forceinline__ Int4Group int4_quantise(const uint32_t (&w)[8], int lanes_log2) {
     constexpr uint32_t kInf = kFP16 ? 0x7c00u : 0x7f80u;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    const uint32_t top2 = max2<kFP16>(max2<kFP16>(w[0], w[1]), max2<kFP16>(w[2], w[3]));
-    const uint32_t bottom2 = min2<kFP16>(min2<kFP16>(w[0], w[1]), min2<kFP16>(w[2], w[3]));
+    uint32_t top2 = w[0], bottom2 = w[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top2 = max2<kFP16>(top2, w[i]), bottom2 = min2<kFP16>(bottom2, w[i]);
     // low half: the largest; high half: the smallest, negated
     uint32_t ends = max2<kFP16>(__byte_perm(top2, bottom2, 0x5410) ^ 0x80000000u, __byte_perm(top2, bottom2, 0x7632) ^ 0x80000000u);
     for (int i = 0; i < lanes_log2; ++i) ends = max2<kFP16>(ends, __shfl_xor_sync(0xffffffffu, ends, 1 << i));
     Int4Group out;
-    out.codes = 0;
+    out.codes[0] = out.codes[1] = 0;
     out.word = 0x7fc00000u;
     if (max(ends & 0x7fffu, ends >> 16 & 0x7fffu) >= kInf) return out;
     const float2 hl = unpack16<kFP16>(ends);
@@ -103,87 +103,93 @@ __device__ __forceinline__ Int4Group int4_quantise(uint4 v, int lanes_log2) {
     const bool small = most < 2.58493941e-26f;  // 2^-85: below, the steps of a quotient might leave the normal numbers
     const float t = fmaxf(small ? __fdiv_rn(wide, 0.9375f) : quotient(wide, 0.9375f, 1.06666672f), most * 0.00048828125f);
     const float s = __uint_as_float((__float_as_uint(t) + 0xffffu) & 0xffff0000u);
-    float x[8], n[8], base;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack16<kFP16>(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-    if (!small) {
-        const float inv = rcp_approx(s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = round_even(quotient(x[i], s, inv));
-        base = round_even(quotient(lo, s, inv));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = s > 0.f ? round_even(__fdiv_rn(x[i], s)) : 0.f;
-        base = s > 0.f ? round_even(__fdiv_rn(lo, s)) : 0.f;
-    }
+    const float inv = rcp_approx(s);
+    const float base = small ? (s > 0.f ? round_even(__fdiv_rn(lo, s)) : 0.f) : round_even(quotient(lo, s, inv));
     // four codes as the digits of one number below 2^16, read off its place in [2^23, 2^24)
-    uint32_t half[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float sum = 8388608.f;
+        uint32_t half[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            sum = fmaf(fminf(n[4 * h + i] - base, 15.f), (float)(1 << (4 * i)), sum);
-        half[h] = __float_as_uint(sum);
+        for (int j = 0; j < 2; ++j) {
+            float sum = 8388608.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 x = unpack16<kFP16>(w[4 * h + 2 * j + i]);
+                float n0 = round_even(quotient(x.x, s, inv)), n1 = round_even(quotient(x.y, s, inv));
+                if (small) {
+                    n0 = s > 0.f ? round_even(__fdiv_rn(x.x, s)) : 0.f;
+                    n1 = s > 0.f ? round_even(__fdiv_rn(x.y, s)) : 0.f;
+                }
+                sum = fmaf(fminf(n0 - base, 15.f), (float)(1 << (8 * i)), sum);
+                sum = fmaf(fminf(n1 - base, 15.f), (float)(16 << (8 * i)), sum);
+            }
+            half[j] = __float_as_uint(sum);
+        }
+        out.codes[h] = __byte_perm(half[0], half[1], 0x5410);
     }
-    out.codes = __byte_perm(half[0], half[1], 0x5410);
     out.word = __float_as_uint(s) | (ptx::pack_f16x2(0.f - base, 0.f) & 0xffffu);
     return out;
 }
 
-// A thread stands for 8 adjacent values of one head of K or V and goes through
-// its CTA's rows, four in flight.
+// A thread stands for 16 adjacent values of one head of K or V and goes through
+// its CTA's rows, U in flight.
 template <bool kFP16, bool kVec>
 __global__ void __launch_bounds__(kInt4Threads) fa_cache_append_int4_kernel(const __grid_constant__ Int4AppendParams p) {
     __shared__ int s_slot[kInt4MaxRows + kInt4Look];
-    __shared__ int s_late[kInt4MaxRows];  // the slot is written by a later row
-    constexpr int U = 4;
+    __shared__ int s_late[kInt4MaxRows];        // the slot is written by a later row
+    __shared__ long long s_row[kInt4MaxRows];   // the row's place in the cache, head 0; -1: it is not written
+    constexpr int U = 2;
     const int tid = (int)threadIdx.x;
-    const int per_row = 2 * p.Hkv << (p.d_log2 - 3);
+    const int per_row = 2 * p.Hkv << (p.d_log2 - 4);
     const int item = ((int)blockIdx.y << p.items_log2) + (tid & ((1 << p.items_log2) - 1));
     const int lane_row = tid >> p.items_log2, rows_at_once = kInt4Threads >> p.items_log2;
     const bool have = item < per_row;
-    const int vec = item & ((1 << (p.d_log2 - 3)) - 1);
-    const int unit = have ? item >> (p.d_log2 - 3) : 0, kv = unit >= p.Hkv ? 1 : 0, head = unit - (kv ? p.Hkv : 0);
+    const int vec = item & ((1 << (p.d_log2 - 4)) - 1);
+    const int unit = have ? item >> (p.d_log2 - 4) : 0, kv = unit >= p.Hkv ? 1 : 0, head = unit - (kv ? p.Hkv : 0);
     const int row0 = (int)blockIdx.x * p.rows_per_cta, rows = min(p.rows_per_cta, p.T - row0);
-    const uint16_t *x = p.x[kv] + row0 * p.token_stride[kv] + head * p.head_stride[kv] + vec * 8;
+    const uint16_t *x = p.x[kv] + row0 * p.token_stride[kv] + head * p.head_stride[kv] + vec * 16;
     ptx::wait_for_previous_kernel();
     for (int j = tid; j < p.rows_per_cta + kInt4Look; j += kInt4Threads)
         s_slot[j] = append_slot(p.slot_map, p.slots, p.T, row0 + j);
     if (tid < kInt4MaxRows) s_late[tid] = 0;
-    uint4 held[U];
-    auto fetch = [&](int r0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * rows_at_once + lane_row;
-            held[u] = make_uint4(0, 0, 0, 0);
-            if (have && r < rows) held[u] = load8_16<kVec>(x + r * p.token_stride[kv]);
+    uint32_t held[U][8];
+    auto fetch = [&](int u, int r) {
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (have && r < rows) {
+            const uint16_t *src = x + r * p.token_stride[kv];
+            a = load8_16<kVec>(src);
+            b = load8_16<kVec>(src + 8);
         }
+        held[u][0] = a.x, held[u][1] = a.y, held[u][2] = a.z, held[u][3] = a.w;
+        held[u][4] = b.x, held[u][5] = b.y, held[u][6] = b.z, held[u][7] = b.w;
     };
-    fetch(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) fetch(u, u * rows_at_once + lane_row);
     __syncthreads();
     for (int i = tid; i < rows * kInt4Look; i += kInt4Threads) {
         const int r = i / kInt4Look, k = i % kInt4Look;
         if (k > 0 && s_slot[r] >= 0 && s_slot[r + k] == s_slot[r]) s_late[r] = 1;
     }
     __syncthreads();
+    for (int r = tid; r < rows; r += kInt4Threads) {
+        const int slot = s_slot[r];
+        s_row[r] = slot < 0 || s_late[r] ? -1 : (((long long)(slot >> p.bs_log2) * p.Hkv) << p.bs_log2) + (slot & ((1 << p.bs_log2) - 1));
+    }
+    __syncthreads();
+    const bool writes_word = (vec & ((1 << (p.g_log2 - 4)) - 1)) == 0;
+    uint8_t *codes = p.codes[kv] + (((long long)head << p.bs_log2) << (p.d_log2 - 1)) + vec * 8;
+    uint32_t *words = p.words[kv] + (((long long)head << p.bs_log2) << (p.d_log2 - p.g_log2)) + (vec >> (p.g_log2 - 4));
     for (int r0 = 0; r0 < rows; r0 += U * rows_at_once) {
-        if (r0 > 0) fetch(r0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (r0 + u * rows_at_once >= rows) break;  // (the same in the whole CTA)
             const int r = r0 + u * rows_at_once + lane_row;
-            const Int4Group q = int4_quantise<kFP16>(held[u], p.g_log2 - 3);
-            if (!have || r >= rows || s_slot[r] < 0 || s_late[r]) continue;
-            const int slot = s_slot[r];
-            const long long at = ((((long long)(slot >> p.bs_log2) * p.Hkv + head) << p.bs_log2) + (slot & ((1 << p.bs_log2) - 1)));
-            reinterpret_cast<uint32_t *>(p.codes[kv])[(at << (p.d_log2 - 3)) + vec] = q.codes;
-            if ((vec & ((1 << (p.g_log2 - 3)) - 1)) == 0)
-                p.words[kv][(at << (p.d_log2 - p.g_log2)) + (vec >> (p.g_log2 - 3))] = q.word;
+            const Int4Group q = int4_quantise<kFP16>(held[u], p.g_log2 - 4);
+            fetch(u, r + U * rows_at_once);
+            const long long at = have && r < rows ? s_row[r] : -1;
+            if (at < 0) continue;
+            *reinterpret_cast<uint2 *>(codes + (at << (p.d_log2 - 1))) = make_uint2(q.codes[0], q.codes[1]);
+            if (writes_word) words[at << (p.d_log2 - p.g_log2)] = q.word;
         }
     }
 }
