@@ -189,6 +189,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same with sums that begin at 0.
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -518,16 +526,6 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
     for (int g = 0; g < C::NG; ++g) {
         float acc[H][C::NT][4];
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    acc[h][n][2 * k + 1] = 0.f;
-#pragma unroll
-                    for (int e = 0; e < C::E; ++e) acc[h][n][2 * k + e] = i4_zero(kw[h][k][g]) * w.q_sum[n][g][e];
-                }
-#pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
             const uint32_t place = (from.k + at) ^ (uint32_t)(c << 4);
             uint32_t a[H], b[H];
@@ -539,7 +537,10 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                 for (int h = 0; h < H; ++h) {
                     const uint32_t f[4] = {a[h] & 0x000f000fu, b[h] & 0x000f000fu, a[h] & 0x00f000f0u, b[h] & 0x00f000f0u};
 #pragma unroll
-                    for (int n = 0; n < C::NT; ++n) mma_16816(acc[h][n], f, w.q[n][c][2 * x], w.q[n][c][2 * x + 1]);
+                    for (int n = 0; n < C::NT; ++n) {
+                        if (x == 0 && c == g * C::G / 32) mma_16816_first(acc[h][n], f, w.q[n][c][0], w.q[n][c][1]);
+                        else mma_16816(acc[h][n], f, w.q[n][c][2 * x], w.q[n][c][2 * x + 1]);
+                    }
                     a[h] >>= 8;
                     b[h] >>= 8;
                 }
@@ -550,10 +551,12 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
             for (int n = 0; n < C::NT; ++n)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float scale = i4_scale(kw[h][k][g]);
+                    const float scale = i4_scale(kw[h][k][g]), zero = i4_zero(kw[h][k][g]);
 #pragma unroll
-                    for (int e = 0; e < C::E; ++e)
-                        s[h][n][k][e] = g == 0 ? scale * acc[h][n][2 * k + e] : fmaf(scale, acc[h][n][2 * k + e], s[h][n][k][e]);
+                    for (int e = 0; e < C::E; ++e) {
+                        const float sum = fmaf(zero, w.q_sum[n][g][e], acc[h][n][2 * k + e]);
+                        s[h][n][k][e] = g == 0 ? scale * sum : fmaf(scale, sum, s[h][n][k][e]);
+                    }
                 }
     }
 #pragma unroll
@@ -645,10 +648,6 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
         uint32_t pf[H][C::NT][2];
         float zs[C::NT][4];
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) zs[n][e] = 0.f;
-#pragma unroll
         for (int h = 0; h < H; ++h) {
             // keys 8 .. 15 of a half: code 15 - c, weight negated
             const float a0 = a[h][0][g], a1 = -a[h][1][g];
@@ -666,18 +665,19 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                     if constexpr (!C::kFew) w.zo[n][g][C::E - 1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][C::E - 1]));
                 } else if constexpr (C::NG == 2 && H == 1) {
                     const uint32_t f[4] = {zr[0][0], 0u, kFifteen, zr[0][0] ^ kMinus};
-                    mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
+                    mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
                 } else if constexpr (C::NG == 2) {
                     if (h == 0) {
                         const uint32_t f[4] = {zr[0][0], 0u, zr[0][1] ^ kMinus, kFifteen};
-                        mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
+                        mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
                     } else {
                         const uint32_t f[4] = {0u, zr[0][0], kFifteen, zr[0][1] ^ kMinus};
                         mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
                     }
                 } else {
                     const uint32_t f[4] = {zr[g / 4][2 * h], 0u, zr[g / 4][2 * h + 1] ^ kMinus, kFifteen};
-                    mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
+                    if (h == 0) mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
+                    else mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
                 }
             }
         }
