@@ -66,19 +66,21 @@ struct DecI4Cfg {
     static constexpr bool kFew = kFew_;
     static constexpr int E = kFew ? 1 : 2;        // rows of each eight columns that are a lane's
     static constexpr int RC = 4 * E * NT * RG;    // rows per unit
+    static constexpr bool kWide = D <= 128 && NT == 1;
     static constexpr int WARPS = 4;
     static constexpr int KW = WARPS / RG;         // warps along a tile's keys
-    static constexpr int H = D <= 128 && NT == 1 ? 2 : 1;  // 16-key halves of a step, side by side
+    static constexpr int H = kWide ? 2 : 1;       // sixteens of keys of a step, side by side
     static constexpr int KEYS = 16 * H;
     static constexpr int BN = 128;
     static constexpr int SPT = BN / KEYS / KW;    // steps of a warp per tile
-    // Which key of a step stands in row i + 8k of the products of half h: SI i + SK k
-    // + SH h.  With two words to a key, 16 bytes hold those of two, and the order
-    // is such that the transposed words have the zeros where their products want
-    // them (see dec_i4_keys).
-    static constexpr int SI = D / G == 2 ? 2 : 1;
-    static constexpr int SK = D / G != 2 ? 8 : H == 2 ? 16 : 1;
-    static constexpr int SH = D / G != 2 ? 16 : 1;
+    // Which key of a step stands in row i + 8k of the products of sixteen h: SI i +
+    // SK k + sixteen(h).  With two words to a key, 16 bytes hold those of two, and
+    // the order is such that the transposed words have the zeros where their
+    // products want them (see dec_i4_keys).
+    static constexpr bool kPairs = D / G == 2;
+    static constexpr int SI = kPairs ? 2 : 1;
+    static constexpr int SK = !kPairs ? 8 : H > 1 ? 16 : 1;
+    static __device__ __forceinline__ constexpr int sixteen(int h) { return kPairs && H > 1 ? (h & 1) + 32 * (h >> 1) : 16 * h; }
     static constexpr bool ZMMA = D / G >= 2;      // the zeros go through products
     static constexpr int ZE = D / G == 2 ? 2 * E : E;  // sums of them a lane holds per group and eight rows
     static constexpr int NG = D / G;
@@ -90,12 +92,12 @@ struct DecI4Cfg {
     static constexpr int STAGE = (O_VW + WORDS + 1023) / 1024 * 1024;
     static constexpr int PART = (2 * NT * NC + NT) * 512;  // a warp's sums, on their way to another's
     static constexpr int PARTS = WARPS / 2;
-    static constexpr int CTAS_PER_SM = D <= 128 && NT == 1 ? 3 : 2;
+    static constexpr int CTAS_PER_SM = kWide ? 3 : 2;
     static constexpr int BUDGET = (227 / CTAS_PER_SM - 1) * 1024;
     static constexpr int FIXED = 1024 + PARTS * PART + 512;
     static constexpr int FIT = (BUDGET - FIXED) / STAGE;
-    static constexpr int ST = FIT < WARPS + 1 ? FIT : WARPS + 1;
-    static_assert(ST >= 2 && ST <= WARPS + 1, "a ring of at least two tiles, a warp to begin each");
+    static constexpr int ST = FIT < 6 ? FIT : 6;
+    static_assert(ST >= 2, "a ring of at least two tiles");
     static constexpr int SMEM_BYTES = FIXED + ST * STAGE;
     static constexpr int NUM_THREADS = 32 * WARPS;
     static constexpr int B_FULL = 0;
@@ -105,28 +107,58 @@ struct DecI4Cfg {
     static_assert(NUM_BARS * 8 + 32 * WARPS + 32 <= 512, "layout");
 };
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// n consecutive words of shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        w[0] = lds32(addr);
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(addr + 4 * i));
+    }
+}
+
+__device__ __forceinline__ float4 lds_float4(uint32_t addr) {
+    uint32_t w[4];
+    lds_words<4>(addr, w);
+    return make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
+}
+
+__device__ __forceinline__ void sts_float4(uint32_t addr, float a, float b, float c, float d) {
+    ptx::st_shared_v4(addr, __float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+}
+
 // ------------------------------------------------------------------- copies
 
-// A warp's next tile to copy.  It lies in shared memory between its turns, so
-// that the products have its registers.
-struct alignas(16) DecI4Kept {
-    int4 a, b;
-};
+// A warp's next tile to copy lies in shared memory between its turns, so that the
+// products have its registers.
+constexpr int kI4Kept = 32;  // bytes
 
-__device__ __forceinline__ void dec_i4_keep(const DecFp8It &it, int lane, DecI4Kept *kept) {
+__device__ __forceinline__ void dec_i4_keep(const DecFp8It &it, int lane, uint32_t kept) {
     __syncwarp();
     if (lane == 0) {
-        kept->a = make_int4(it.b, it.kvh, it.chunk, it.tile);
-        kept->b = make_int4(it.L, it.nt, it.next_len, it.left);
+        ptx::st_shared_v4(kept, it.b, it.kvh, it.chunk, it.tile);
+        ptx::st_shared_v4(kept + 16, it.L, it.nt, it.next_len, it.left);
     }
     __syncwarp();
 }
 
-__device__ __forceinline__ DecFp8It dec_i4_take(const DecI4Kept *kept) {
-    const int4 x = kept->a, y = kept->b;
+__device__ __forceinline__ DecFp8It dec_i4_take(uint32_t kept) {
+    uint32_t x[8];
+    lds_words<8>(kept, x);
     DecFp8It it;
-    it.b = x.x, it.kvh = x.y, it.chunk = x.z, it.tile = x.w;
-    it.L = y.x, it.nt = y.y, it.next_len = y.z, it.left = y.w;
+    it.b = (int)x[0], it.kvh = (int)x[1], it.chunk = (int)x[2], it.tile = (int)x[3];
+    it.L = (int)x[4], it.nt = (int)x[5], it.next_len = (int)x[6], it.left = (int)x[7];
     return it;
 }
 
@@ -197,12 +229,6 @@ __device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -230,21 +256,6 @@ __device__ __forceinline__ float lg2_approx(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// n consecutive words of shared memory.
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
-    if constexpr (N == 1) {
-        w[0] = lds32(addr);
-    } else if constexpr (N == 2) {
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(addr + 4 * i));
-    }
 }
 
 __device__ __forceinline__ float i4_scale(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -485,7 +496,7 @@ __device__ __forceinline__ DecI4Lane dec_i4_lane(uint32_t ring, int lane, int fi
     // 16-byte chunk c of row r of a box is chunk c ^ swizzle(r)
     auto swizzle = [](int r) { return C::ROW == 128 ? r & 7 : C::ROW == 64 ? (r >> 1) & 3 : (r >> 2) & 1; };
     const int k_row = C::SI * (lane >> 2), v_row = C::SI * (lane & 7) + C::SK * (lane >> 3 & 1);
-    const int z_row = C::NG == 2 ? 2 * (lane & 15) : (lane & 7) + 8 * (lane >> 3 & 1) + (C::H == 2 ? 16 * (lane >> 4) : 0);
+    const int z_row = C::NG == 2 ? 2 * lane : lane;  // (lanes whose matrix is not loaded are not asked)
     DecI4Lane x;
     x.k = ring + (first + k_row) * C::ROW + (swizzle(k_row) << 4) + 4 * (lane & 3);
     x.v = ring + C::O_V + (first + v_row) * C::ROW + ((swizzle(v_row) ^ (lane >> 4)) << 4);
@@ -501,18 +512,19 @@ template <class C>
 __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int back, int row0, int lane, const DecI4Lane &from,
                                             uint32_t at, uint32_t at_words) {
     constexpr int H = C::H, ROW_W = C::NG * 4;
-    constexpr int HALF = C::SH * C::ROW, OTHER = C::SK * C::ROW;  // to the second half, and to row i + 8
+    constexpr int OTHER = C::SK * C::ROW;  // to row i + 8
     const uint32_t words = from.w + at_words;
     if (key + C::KEYS > L) {  // slots past the request's tokens may hold anything: their words become 0
-        const int mine = lane & (C::KEYS - 1);
-        if (key + mine >= L) {
-            const uint32_t row = words + (mine - C::SI * (lane >> 2)) * ROW_W + (C::KEYS == 16 && lane >= 16 ? C::WORDS : 0);
 #pragma unroll
-            for (int g = 0; g < C::NG; ++g) {
-                sts32(row + 4 * g, 0u);
-                if (C::KEYS == 32) sts32(row + C::WORDS + 4 * g, 0u);
+        for (int mine = lane; mine < C::KEYS; mine += 32)
+            if (key + mine >= L) {
+                const uint32_t row = words + (mine - C::SI * (lane >> 2)) * ROW_W;
+#pragma unroll
+                for (int g = 0; g < C::NG; ++g) {
+                    sts32(row + 4 * g, 0u);
+                    sts32(row + C::WORDS + 4 * g, 0u);
+                }
             }
-        }
         ptx::fence_proxy_async_smem();  // (the next copy to this stage comes behind)
         __syncwarp();
     }
@@ -520,7 +532,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + (C::SH * h + C::SK * k) * ROW_W, kw[h][k]);
+        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + (C::sixteen(h) + C::SK * k) * ROW_W, kw[h][k]);
     float s[H][C::NT][2][C::E];  // of keys i and i + 8 of a half, the lane's rows
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
@@ -530,7 +542,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
             const uint32_t place = (from.k + at) ^ (uint32_t)(c << 4);
             uint32_t a[H], b[H];
 #pragma unroll
-            for (int h = 0; h < H; ++h) a[h] = lds32(place + h * HALF), b[h] = lds32(place + h * HALF + OTHER);
+            for (int h = 0; h < H; ++h) a[h] = lds32(place + C::sixteen(h) * C::ROW), b[h] = lds32(place + C::sixteen(h) * C::ROW + OTHER);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -562,7 +574,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + C::WORDS + (C::SH * h + C::SK * k) * ROW_W, vw[h][k]);
+        for (int k = 0; k < 2; ++k) lds_words<C::NG>(words + C::WORDS + (C::sixteen(h) + C::SK * k) * ROW_W, vw[h][k]);
     // hidden keys: past the row's last (a select, so nothing of theirs leaks)
     if (key + C::KEYS > L - back) {
 #pragma unroll
@@ -574,7 +586,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                 for (int h = 0; h < H; ++h)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        if (key + C::SI * (lane >> 2) + C::SH * h + C::SK * k > row_last) s[h][n][k][e] = -INFINITY;
+                        if (key + C::SI * (lane >> 2) + C::sixteen(h) + C::SK * k > row_last) s[h][n][k][e] = -INFINITY;
             }
     }
     float a[H][2][C::NG];  // the keys' V scales over their references
@@ -631,15 +643,21 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
     // of rows that are else empty.  With two words to a key the 16 bytes of a row
     // are two keys', so rows 0 and 2 are even keys' and 4 and 6 odd keys'.
     constexpr uint32_t kMinus = 0x80008000u, kFifteen = 0x4b804b80u;
-    uint32_t zr[C::NG > 4 ? 2 : 1][4];
+    constexpr int ZQ = C::NG > 4 ? 2 : H > 1 && !C::kPairs ? H / 2 : 1;
+    uint32_t zr[ZQ][4];
     if constexpr (C::ZMMA) {
-        if constexpr (C::NG == 2 && H == 1) ldmatrix_x1_trans(from.z + at_words, zr[0]);
-        else if constexpr (C::NG == 2 || H == 1) {
-            ldmatrix_x2_trans(from.z + at_words, zr[0]);
-            if constexpr (C::NG > 4) ldmatrix_x2_trans(from.z + at_words + 16, zr[1]);
+        if constexpr (H == 1) {
+            if constexpr (C::kPairs) ldmatrix_x1_trans(from.z + at_words, zr[0]);
+            else {
+#pragma unroll
+                for (int x = 0; x < ZQ; ++x) ldmatrix_x2_trans(from.z + at_words + 16 * x, zr[x]);
+            }
         } else {
-            ldmatrix_x4_trans(from.z + at_words, zr[0]);
-            static_assert(C::NG <= 4 || H == 1, "two halves of at most four words to a key");
+            static_assert(C::NG <= 4, "two or four words to a key");
+            if constexpr (H == 2 && C::kPairs) ldmatrix_x2_trans(from.z + at_words, zr[0]);
+            else
+#pragma unroll
+                for (int x = 0; x < ZQ; ++x) ldmatrix_x4_trans(from.z + at_words + x * 32 * ROW_W, zr[x]);
         }
     }
     uint32_t raw[H][4];
@@ -663,19 +681,17 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                     const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
                     w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
                     if constexpr (!C::kFew) w.zo[n][g][C::E - 1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][C::E - 1]));
-                } else if constexpr (C::NG == 2 && H == 1) {
+                } else if constexpr (C::kPairs && H == 1) {
                     const uint32_t f[4] = {zr[0][0], 0u, kFifteen, zr[0][0] ^ kMinus};
                     mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
-                } else if constexpr (C::NG == 2) {
-                    if (h == 0) {
-                        const uint32_t f[4] = {zr[0][0], 0u, zr[0][1] ^ kMinus, kFifteen};
-                        mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
-                    } else {
-                        const uint32_t f[4] = {0u, zr[0][0], kFifteen, zr[0][1] ^ kMinus};
-                        mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
-                    }
+                } else if constexpr (C::kPairs) {
+                    const uint32_t z0 = zr[0][2 * (h >> 1)], z1 = zr[0][2 * (h >> 1) + 1] ^ kMinus;
+                    const uint32_t f[4] = {h & 1 ? 0u : z0, h & 1 ? z0 : 0u, h & 1 ? kFifteen : z1, h & 1 ? z1 : kFifteen};
+                    if (h == 0) mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
+                    else mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
                 } else {
-                    const uint32_t f[4] = {zr[g / 4][2 * h], 0u, zr[g / 4][2 * h + 1] ^ kMinus, kFifteen};
+                    const int q = C::NG > 4 ? g / 4 : h / 2;
+                    const uint32_t f[4] = {zr[q][2 * (h & 1)], 0u, zr[q][2 * (h & 1) + 1] ^ kMinus, kFifteen};
                     if (h == 0) mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
                     else mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
                 }
@@ -694,7 +710,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
             uint32_t lo[H], hi[H];
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                if (c % 2 == 0) ldmatrix_x4_trans(((from.v + at) ^ (uint32_t)(c << 4)) + h * HALF, raw[h]);
+                if (c % 2 == 0) ldmatrix_x4_trans(((from.v + at) ^ (uint32_t)(c << 4)) + C::sixteen(h) * C::ROW, raw[h]);
                 lo[h] = raw[h][c % 2 * 2], hi[h] = raw[h][c % 2 * 2 + 1];
             }
 #pragma unroll
@@ -725,7 +741,7 @@ __device__ __forceinline__ void dec_i4_meet(int rg) {
 // other half at a time; the last writes the rows out, or a partial of them.
 template <class C>
 __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const DecFp8It &it, DecI4Warp<C> &w, int rg, int kwi,
-                                                int lane, bool whole, bool begun_here, uint8_t *parts) {
+                                                int lane, bool whole, bool begun_here, uint32_t parts) {
     const int i = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
@@ -759,24 +775,24 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
     {
 #pragma unroll
         for (int half = C::KW / 2; half > 0; half >>= 1) {
-            float4 *at = reinterpret_cast<float4 *>(parts + (rg * (C::KW / 2) + kwi % half) * C::PART) + lane;
+            const uint32_t at = parts + (rg * (C::KW / 2) + kwi % half) * C::PART + lane * 16;
             if (kwi >= half && kwi < 2 * half) {
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n) {
-                    at[(2 * C::NT * C::NC + n) * 32] = make_float4(w.m[n][0], w.m[n][C::E - 1], w.l[n][0], w.l[n][C::E - 1]);
+                    sts_float4(at + (2 * C::NT * C::NC + n) * 512, w.m[n][0], w.m[n][C::E - 1], w.l[n][0], w.l[n][C::E - 1]);
 #pragma unroll
                     for (int c = 0; c < C::NC; ++c)
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            at[((n * C::NC + c) * 2 + x) * 32] =
-                                make_float4(w.o[n][c][x][0], w.o[n][c][x][1], w.o[n][c][x][2], w.o[n][c][x][3]);
+                            sts_float4(at + ((n * C::NC + c) * 2 + x) * 512, w.o[n][c][x][0], w.o[n][c][x][1], w.o[n][c][x][2],
+                                       w.o[n][c][x][3]);
                 }
             }
             dec_i4_meet<C>(rg);
             if (kwi < half) {
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n) {
-                    const float4 ml = at[(2 * C::NT * C::NC + n) * 32];
+                    const float4 ml = lds_float4(at + (2 * C::NT * C::NC + n) * 512);
                     float mine[C::E], theirs[C::E];  // what the two sides' sums are multiplied by
 #pragma unroll
                     for (int e = 0; e < C::E; ++e) {
@@ -790,7 +806,7 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
                     for (int c = 0; c < C::NC; ++c)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const float4 y = at[((n * C::NC + c) * 2 + x) * 32];
+                            const float4 y = lds_float4(at + ((n * C::NC + c) * 2 + x) * 512);
                             float(&o)[4] = w.o[n][c][x];
                             o[0] = fmaf(o[0], mine[0], y.x * theirs[0]);
                             o[2] = fmaf(o[2], mine[0], y.z * theirs[0]);
@@ -835,29 +851,34 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
 }
 
 template <class C>
-__device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, uint8_t *parts, DecI4Kept *kept, uint32_t bars,
+__device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, uint32_t parts, uint32_t kept, uint32_t bars,
                             int *copied, Ctl *ctl) {
     const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5, rg = warp / C::KW, kwi = warp % C::KW;
     if (it.left <= 0) return;
     uint4 raw[C::NT][C::NC];
     dec_i4_load_q<C>(p, it, rg, lane, raw);
-    // The warps take turns at the copies: tile n is copied by warp n of the first
-    // ST - 1, and tile t + ST - 1 by warp t % 4, behind its own keys of tile t;
-    // the stage's last readers were busy with the tile in front of that.
+    // The warps take turns at the copies.  Of the first ST - 1 tiles, tile n is warp
+    // n % WARPS's; warp t % WARPS copies tile t + ST - 1, behind its own keys of tile
+    // t, to where tile t - 1 was, which the others have read by then.  (In front of
+    // its keys it waits for them: kv8 84 -> 94 us.)
     DecFp8It ahead = it;
-    if (warp < C::ST - 1) {
+    int entry = 0;
+    bool some;
+    {
         dec_i4_advance(p, ahead, warp);
-        if (ahead.left > 0) {
-            if (lane == 0) atomicMax(copied, warp + 1);
-            int entry;
-            const bool some = dec_i4_entry<C>(p, ahead, lane, entry);
-            dec_i4_copy<C>(p, ahead.kvh, some, entry, lane, ring + warp * C::STAGE, bar_addr(bars, C::B_FULL + warp));
+        for (int n = warp; n < C::ST - 1; n += C::WARPS) {
+            if (ahead.left > 0) {
+                if (lane == 0) atomicMax(copied, n + 1);
+                some = dec_i4_entry<C>(p, ahead, lane, entry);
+                dec_i4_copy<C>(p, ahead.kvh, some, entry, lane, ring + n * C::STAGE, bar_addr(bars, C::B_FULL + n));
+            }
+            dec_i4_advance(p, ahead, C::WARPS);
         }
-        dec_i4_advance(p, ahead, C::ST - 1);
-    } else {
+        ahead = it;
         dec_i4_advance(p, ahead, warp + C::ST - 1);
     }
     dec_i4_keep(ahead, lane, kept);
+    some = dec_i4_entry<C>(p, ahead, lane, entry);
     const DecI4Lane from = dec_i4_lane<C>(ring, lane, kwi * C::SPT * C::KEYS);
     const int back = p.mask_kind == kMaskCausal ? p.Sq - 1 : 0;
     DecI4Warp<C> w;
@@ -868,13 +889,6 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
     uint32_t phase = 0;
     int t = 0;
     for (;;) {
-        int entry = 0, kvh = 0;
-        bool some = false;
-        if (turn == 0) {
-            const DecFp8It coming = dec_i4_take(kept);
-            kvh = coming.left > 0 ? coming.kvh : -1;
-            some = dec_i4_entry<C>(p, coming, lane, entry);
-        }
         // (a warp whose wait ran out goes on without its tiles, so that the others meet it at the units' ends)
         if (!bad) bad = !wait_warp(bar_addr(bars, C::B_FULL + slot), phase, ctl, 92);
         int key = it.tile * C::BN + kwi * C::SPT * C::KEYS;
@@ -888,16 +902,16 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
         if (lane == 0) ptx::mbar_arrive(bar_addr(bars, C::B_EMPTY + slot));
         if (turn == 0) {
             turn = C::WARPS;
-            if (kvh >= 0 && !bad) {
-                // where tile t - 1 was
+            DecFp8It coming = dec_i4_take(kept);
+            if (coming.left > 0 && !bad) {
                 const int prev = slot == 0 ? C::ST - 1 : slot - 1;
                 bad = t > 0 && !wait_warp(bar_addr(bars, C::B_EMPTY + prev), slot == 0 ? phase ^ 1 : phase, ctl, 91);
                 if (!bad) {
                     if (lane == 0) atomicMax(copied, t + C::ST);
-                    dec_i4_copy<C>(p, kvh, some, entry, lane, ring + prev * C::STAGE, bar_addr(bars, C::B_FULL + prev));
-                    DecFp8It coming = dec_i4_take(kept);
+                    dec_i4_copy<C>(p, coming.kvh, some, entry, lane, ring + prev * C::STAGE, bar_addr(bars, C::B_FULL + prev));
                     dec_i4_advance(p, coming, C::WARPS);
                     dec_i4_keep(coming, lane, kept);
+                    some = dec_i4_entry<C>(p, coming, lane, entry);
                 }
             }
         }
@@ -927,8 +941,8 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *parts = ring + C::ST * C::STAGE;
-    DecI4Kept *kept = reinterpret_cast<DecI4Kept *>(parts + C::PARTS * C::PART);
-    uint64_t *bar_mem = reinterpret_cast<uint64_t *>(kept + C::WARPS);
+    uint8_t *kept = parts + C::PARTS * C::PART;
+    uint64_t *bar_mem = reinterpret_cast<uint64_t *>(kept + C::WARPS * kI4Kept);
     Ctl *ctl = reinterpret_cast<Ctl *>(bar_mem + C::NUM_BARS);
     int *copied = reinterpret_cast<int *>(ctl + 1);  // tiles that copies were begun for
     const uint32_t bars = ptx::smem_addr(bar_mem);
@@ -951,7 +965,8 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     __syncthreads();
     // the merge may be set up now; it waits for this grid's end before it reads
     ptx::let_next_kernel_begin();
-    dec_i4_warp<C>(p, it, ptx::smem_addr(ring), parts, kept + (threadIdx.x >> 5), bars, copied, ctl);
+    dec_i4_warp<C>(p, it, ptx::smem_addr(ring), ptx::smem_addr(parts),
+                   ptx::smem_addr(kept) + (threadIdx.x >> 5) * kI4Kept, bars, copied, ctl);
     __syncthreads();
     // the CTA's memory stays until its last copies have landed, also where the
     // warps gave up waiting for them
