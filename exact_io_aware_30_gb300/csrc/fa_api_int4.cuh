@@ -222,6 +222,7 @@ DecFp8Plan plan_decode_int4(int B, int Hkv, int R, int d, int max_seq_len, int n
     DecFp8Plan pl;
     pl.chunks = (R + 31) / 32;
     pl.rows_per_chunk = (R + pl.chunks - 1) / pl.chunks;
+    if (pl.chunks > 1) pl.rows_per_chunk = (pl.rows_per_chunk + 7) / 8 * 8;  // (a warp has whole eights)
     pl.chunks = (R + pl.rows_per_chunk - 1) / pl.rows_per_chunk;
     pl.rc = pl.rows_per_chunk <= 4 ? 4 : pl.rows_per_chunk <= 8 ? 8 : pl.rows_per_chunk <= 16 ? 16 : 32;
     const int per_sm = d <= 128 && pl.rc <= 8 ? 3 : 2;

@@ -69,7 +69,7 @@ struct DecI4Cfg {
     static constexpr bool kWide = D <= 128 && NT == 1;
     static constexpr int WARPS = 4;
     static constexpr int KW = WARPS / RG;         // warps along a tile's keys
-    static constexpr int H = kWide ? 2 : 1;       // sixteens of keys of a step, side by side
+    static constexpr int H = D / G * NT <= 4 ? 2 : 1;  // sixteens of keys of a step, side by side, where registers hold their words
     static constexpr int KEYS = 16 * H;
     static constexpr int BN = 128;
     static constexpr int SPT = BN / KEYS / KW;    // steps of a warp per tile
@@ -90,7 +90,7 @@ struct DecI4Cfg {
     static constexpr int WORDS = BN * NG * 4;     // bytes of a tile's words
     static constexpr int O_V = TILE, O_KW = 2 * TILE, O_VW = O_KW + WORDS;  // places in a stage
     static constexpr int STAGE = (O_VW + WORDS + 1023) / 1024 * 1024;
-    static constexpr int PART = (2 * NT * NC + NT) * 512;  // a warp's sums, on their way to another's
+    static constexpr int PART = (E * NT * NC + NT) * 512;  // a warp's sums, on their way to another's
     static constexpr int PARTS = WARPS / 2;
     static constexpr int CTAS_PER_SM = kWide ? 3 : 2;
     static constexpr int BUDGET = (227 / CTAS_PER_SM - 1) * 1024;
@@ -643,21 +643,19 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
     // of rows that are else empty.  With two words to a key the 16 bytes of a row
     // are two keys', so rows 0 and 2 are even keys' and 4 and 6 odd keys'.
     constexpr uint32_t kMinus = 0x80008000u, kFifteen = 0x4b804b80u;
-    constexpr int ZQ = C::NG > 4 ? 2 : H > 1 && !C::kPairs ? H / 2 : 1;
+    constexpr int ZQ = C::NG > 4 ? 2 * H : H > 1 && !C::kPairs ? H / 2 : 1;
     uint32_t zr[ZQ][4];
     if constexpr (C::ZMMA) {
-        if constexpr (H == 1) {
-            if constexpr (C::kPairs) ldmatrix_x1_trans(from.z + at_words, zr[0]);
-            else {
+        if constexpr (C::NG > 4) {
 #pragma unroll
-                for (int x = 0; x < ZQ; ++x) ldmatrix_x2_trans(from.z + at_words + 16 * x, zr[x]);
-            }
+            for (int x = 0; x < ZQ; ++x) ldmatrix_x2_trans(from.z + at_words + C::sixteen(x >> 1) * ROW_W + 16 * (x & 1), zr[x]);
+        } else if constexpr (H == 1 && C::kPairs) {
+            ldmatrix_x1_trans(from.z + at_words, zr[0]);
+        } else if constexpr (H == 1 || C::kPairs) {
+            ldmatrix_x2_trans(from.z + at_words, zr[0]);
         } else {
-            static_assert(C::NG <= 4, "two or four words to a key");
-            if constexpr (H == 2 && C::kPairs) ldmatrix_x2_trans(from.z + at_words, zr[0]);
-            else
 #pragma unroll
-                for (int x = 0; x < ZQ; ++x) ldmatrix_x4_trans(from.z + at_words + x * 32 * ROW_W, zr[x]);
+            for (int x = 0; x < ZQ; ++x) ldmatrix_x4_trans(from.z + at_words + x * 32 * ROW_W, zr[x]);
         }
     }
     uint32_t raw[H][4];
@@ -690,8 +688,8 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                     if (h == 0) mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
                     else mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
                 } else {
-                    const int q = C::NG > 4 ? g / 4 : h / 2;
-                    const uint32_t f[4] = {zr[q][2 * (h & 1)], 0u, zr[q][2 * (h & 1) + 1] ^ kMinus, kFifteen};
+                    const int q = C::NG > 4 ? 2 * h + g / 4 : h / 2, x = C::NG > 4 ? 0 : 2 * (h & 1);
+                    const uint32_t f[4] = {zr[q][x], 0u, zr[q][x + 1] ^ kMinus, kFifteen};
                     if (h == 0) mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
                     else mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
                 }
@@ -779,20 +777,20 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
             if (kwi >= half && kwi < 2 * half) {
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n) {
-                    sts_float4(at + (2 * C::NT * C::NC + n) * 512, w.m[n][0], w.m[n][C::E - 1], w.l[n][0], w.l[n][C::E - 1]);
+                    sts_float4(at + (C::E * C::NT * C::NC + n) * 512, w.m[n][0], w.m[n][C::E - 1], w.l[n][0], w.l[n][C::E - 1]);
 #pragma unroll
                     for (int c = 0; c < C::NC; ++c)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            sts_float4(at + ((n * C::NC + c) * 2 + x) * 512, w.o[n][c][x][0], w.o[n][c][x][1], w.o[n][c][x][2],
-                                       w.o[n][c][x][3]);
+                        for (int e = 0; e < C::E; ++e)
+                            sts_float4(at + ((n * C::NC + c) * C::E + e) * 512, w.o[n][c][0][e], w.o[n][c][0][2 + e], w.o[n][c][1][e],
+                                       w.o[n][c][1][2 + e]);
                 }
             }
             dec_i4_meet<C>(rg);
             if (kwi < half) {
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n) {
-                    const float4 ml = lds_float4(at + (2 * C::NT * C::NC + n) * 512);
+                    const float4 ml = lds_float4(at + (C::E * C::NT * C::NC + n) * 512);
                     float mine[C::E], theirs[C::E];  // what the two sides' sums are multiplied by
 #pragma unroll
                     for (int e = 0; e < C::E; ++e) {
@@ -805,15 +803,13 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
 #pragma unroll
                     for (int c = 0; c < C::NC; ++c)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float4 y = lds_float4(at + ((n * C::NC + c) * 2 + x) * 512);
-                            float(&o)[4] = w.o[n][c][x];
-                            o[0] = fmaf(o[0], mine[0], y.x * theirs[0]);
-                            o[2] = fmaf(o[2], mine[0], y.z * theirs[0]);
-                            if constexpr (!C::kFew) {
-                                o[1] = fmaf(o[1], mine[C::E - 1], y.y * theirs[C::E - 1]);
-                                o[3] = fmaf(o[3], mine[C::E - 1], y.w * theirs[C::E - 1]);
-                            }
+                        for (int e = 0; e < C::E; ++e) {
+                            const float4 y = lds_float4(at + ((n * C::NC + c) * C::E + e) * 512);
+                            float(&o)[2][4] = w.o[n][c];
+                            o[0][e] = fmaf(o[0][e], mine[e], y.x * theirs[e]);
+                            o[0][2 + e] = fmaf(o[0][2 + e], mine[e], y.y * theirs[e]);
+                            o[1][e] = fmaf(o[1][e], mine[e], y.z * theirs[e]);
+                            o[1][2 + e] = fmaf(o[1][2 + e], mine[e], y.w * theirs[e]);
                         }
                 }
             }
@@ -891,10 +887,12 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
     for (;;) {
         // (a warp whose wait ran out goes on without its tiles, so that the others meet it at the units' ends)
         if (!bad) bad = !wait_warp(bar_addr(bars, C::B_FULL + slot), phase, ctl, 92);
+        // (a row group behind the chunk's last rows has nothing to do)
+        const bool idle = C::RG > 1 && rg * 8 * C::NT >= min(p.rows_per_chunk, p.R - it.chunk * p.rows_per_chunk);
         int key = it.tile * C::BN + kwi * C::SPT * C::KEYS;
 #pragma unroll 1
         for (int j = 0; j < C::SPT; ++j, key += C::KEYS) {
-            if (bad || key >= it.L) break;
+            if (bad || key >= it.L || idle) break;
             dec_i4_keys<C>(w, key, it.L, back, it.chunk * p.rows_per_chunk + rg * C::NT * 8, lane, from,
                            slot * C::STAGE + j * C::KEYS * C::ROW, slot * C::STAGE + j * C::KEYS * C::NG * 4);
         }
