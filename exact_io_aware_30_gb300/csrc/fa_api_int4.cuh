@@ -119,7 +119,7 @@ fa_status cache_read_int4_impl(const void *k_cache, const void *v_cache, const u
     if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) return FA_ERR_UNSUPPORTED;
     const fa_status sizes = check_int4_cache(num_blocks, Hkv, block_size, d, group);
     if (sizes != FA_OK) return sizes;
-    if (B < 1 || rows < 0 || Hkv > 65535 || max_blocks < 1) return FA_ERR_INVALID_ARG;
+    if (B < 1 || rows < 0 || rows > (1 << 30) || Hkv > 65535 || max_blocks < 1) return FA_ERR_INVALID_ARG;
     if ((long long)max_blocks * block_size > 0x7fffffffLL || (long long)B * max_blocks > 0x7fffffffLL ||
         (long long)B * rows > 0x7fffffffLL)
         return FA_ERR_INVALID_ARG;
@@ -182,7 +182,7 @@ fa_status cache_read_int4_impl(const void *k_cache, const void *v_cache, const u
     p.g_log2 = group == 32 ? 5 : 6;
     p.bs_log2 = block_size_log2(block_size);
     unsigned y = 1;
-    int4_items(2 * Hkv * (d / 8), &p.items_log2, &y);
+    int4_items(2 * Hkv * (d / 16), &p.items_log2, &y);
     // Rows per CTA: four in flight per thread, and more until the grid is at most
     // eight waves of eight CTAs per SM.
     p.rows_per_cta = 4 * (kInt4Threads >> p.items_log2);
@@ -190,12 +190,14 @@ fa_status cache_read_int4_impl(const void *k_cache, const void *v_cache, const u
         p.rows_per_cta *= 2;
     p.chunks = (rows + p.rows_per_cta - 1) / p.rows_per_cta;
     const dim3 grid((unsigned)((long long)B * p.chunks), y);
-    const bool vec = (bits & 15) == 0, fp16 = dtype == FA_DTYPE_FP16;
+    const int bytes = (bits & 31) == 0 ? 32 : (bits & 15) == 0 ? 16 : 2;
+    const bool fp16 = dtype == FA_DTYPE_FP16;
     if (log_enabled())
-        std::fprintf(stderr, "[fa] fa_cache_read_int4 B=%d Hkv=%d rows=%d d=%d group=%d bs=%d vec=%d rows_per_cta=%d grid=%d x %d\n",
-                     B, Hkv, rows, d, group, block_size, vec ? 1 : 0, p.rows_per_cta, (int)grid.x, (int)grid.y);
-    auto kern = fp16 ? (vec ? fa_cache_read_int4_kernel<true, true> : fa_cache_read_int4_kernel<true, false>)
-                     : (vec ? fa_cache_read_int4_kernel<false, true> : fa_cache_read_int4_kernel<false, false>);
+        std::fprintf(stderr, "[fa] fa_cache_read_int4 B=%d Hkv=%d rows=%d d=%d group=%d bs=%d bytes=%d rows_per_cta=%d grid=%d x %d\n",
+                     B, Hkv, rows, d, group, block_size, bytes, p.rows_per_cta, (int)grid.x, (int)grid.y);
+    auto kern = bytes == 32   ? (fp16 ? fa_cache_read_int4_kernel<true, 32> : fa_cache_read_int4_kernel<false, 32>)
+                : bytes == 16 ? (fp16 ? fa_cache_read_int4_kernel<true, 16> : fa_cache_read_int4_kernel<false, 16>)
+                              : (fp16 ? fa_cache_read_int4_kernel<true, 2> : fa_cache_read_int4_kernel<false, 2>);
     return launch_overlapped(kern, grid, kInt4Threads, 0, 1, stream, p);
 }
 

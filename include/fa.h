@@ -544,8 +544,8 @@ fa_status fa_cache_append_int4(const void *k, const void *v, long long k_token_s
  *   block_table device int32 [B, max_blocks]; an entry outside [0, num_blocks)
  *               reads zeros
  *   dtype       FA_DTYPE_BF16 or FA_DTYPE_FP16 (k_out and v_out)
- * rows == 0: FA_OK.  Outputs may not overlap inputs or each other.  One launch;
- * no workspace.
+ * rows <= 2^30, H_kv <= 65535; rows == 0: FA_OK.  Outputs may not overlap inputs
+ * or each other.  One launch; no workspace.
  */
 fa_status fa_cache_read_int4(const void *k_cache, const void *v_cache, const unsigned *k_scale,
                              const unsigned *v_scale, const int *block_table, const int *seq_lens,
@@ -566,7 +566,8 @@ fa_status fa_cache_read_int4(const void *k_cache, const void *v_cache, const uns
  *   k_cache, v_cache, k_scale, v_scale, group  as above; scales finite and >= 0
  *                or NaN
  *   q            components below 2^112 in size; a row with a larger one, an
- *                infinity or NaN gives NaN
+ *                infinity or NaN gives NaN.  A row with a score (scale q k) of
+ *                2^25 or more in size is undefined
  *   seq_lens     any length in [0, max_seq_len] (values outside are clamped
  *                into it).  A row that sees no key -- length 0, or with
  *                FA_MASK_CAUSAL a row in front of the request's first token --

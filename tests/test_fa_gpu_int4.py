@@ -11,7 +11,7 @@ torch = pytest.importorskip("torch")
 
 pytestmark = pytest.mark.gpu
 
-U = {inputs.BF16: 2.0 ** -8, inputs.FP16: 2.0 ** -11}  # half a step of the type, doubled: relative to the value's power of two
+U = {inputs.BF16: 2.0 ** -8, inputs.FP16: 2.0 ** -11}  # half a step of the type, relative to the value
 DTYPES = {inputs.BF16: torch.bfloat16, inputs.FP16: torch.float16}
 
 
@@ -228,6 +228,20 @@ def test_read_back(B, Hkv, d, group, bs, lens, rows, starts, layout, dtype):
                     want[b, :, i] = torch.from_numpy(x[:, first + i])
         # s (c - z) has at most 8 + 12 bits, exact in fp32; then one rounding
         assert torch.equal(got.cpu(), want.float().to(dt))
+
+
+@pytest.mark.parametrize("start", [-2 ** 31, -2 ** 31 + 1, 2 ** 31 - 1, -40, 39, 40])
+def test_read_back_from_far_outside_a_request(start):
+    p = _problem(2, 2, 2, 1, 64, 32, 16, [40, 40], inputs.BF16, seed=4)
+    k, v = fa.cache_read_int4(*_device(p)[1:], 60, starts=_dev(np.array([start, 0], np.int32)))
+    for got, c, w in ((k, p["kc"], p["kw"]), (v, p["vc"], p["vw"])):
+        want = torch.zeros(2, 2, 60, 64, dtype=torch.float64)
+        for b, first in enumerate((start, 0)):
+            x = torch.from_numpy(ref.gathered(c, w, p["table"][b], 40, 16))
+            for i in range(60):
+                if 0 <= first + i < 40:
+                    want[b, :, i] = x[:, first + i]
+        assert torch.equal(got.cpu(), want.float().to(torch.bfloat16))
 
 
 def test_read_back_entries_outside_the_pool_read_zeros():
