@@ -55,7 +55,7 @@ struct DecInt4Params : DecFp8Params {  // (k_scale and v_scale are not used)
     int fp16;
 };
 
-template <int D_, int G_, int NT_, int RG_, bool kFew_ = false>
+template <int D_, int G_, int NT_, int RG_, bool kFew_ = false, bool kFine_ = false>
 struct DecI4Cfg {
     static constexpr int D = D_;
     static constexpr int G = G_;                  // components per group
@@ -64,6 +64,11 @@ struct DecI4Cfg {
     // Up to four rows stand in every other column of a product, so that a lane has
     // one of them and the work on the weights halves.
     static constexpr bool kFew = kFew_;
+    // The columns between them then hold what rounding a weight to fp16 lost, where
+    // O is fp16, whose own rounding is no coarser (128 requests x 40 heads: the error
+    // of O 1.33 -> 1.00 times that rounding, 266 -> 273 us).
+    static constexpr bool kFine = kFine_;
+    static_assert(kFew || !kFine, "a column for the rest");
     static constexpr int E = kFew ? 1 : 2;        // rows of each eight columns that are a lane's
     static constexpr int RC = 4 * E * NT * RG;    // rows per unit
     static constexpr bool kWide = D <= 128 && NT == 1;
@@ -481,6 +486,10 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
                 for (int h = 0; h < 2; ++h) {
                     w.o[n][c][h][e] *= f;
                     w.o[n][c][h][2 + e] *= f;
+                    if constexpr (C::kFine) {
+                        w.o[n][c][h][1] *= f;
+                        w.o[n][c][h][3] *= f;
+                    }
                 }
         }
 }
@@ -669,8 +678,12 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
             const float a0 = a[h][0][g], a1 = -a[h][1][g];
 #pragma unroll
             for (int n = 0; n < C::NT; ++n) {
-                const uint32_t h0 = ptx::pack_f16x2(s[h][n][0][0] * a0, C::kFew ? 0.f : s[h][n][0][C::E - 1] * a0);
-                const uint32_t h1 = ptx::pack_f16x2(s[h][n][1][0] * a1, C::kFew ? 0.f : s[h][n][1][C::E - 1] * a1);
+                uint32_t h0 = ptx::pack_f16x2(s[h][n][0][0] * a0, C::kFew ? 0.f : s[h][n][0][C::E - 1] * a0);
+                uint32_t h1 = ptx::pack_f16x2(s[h][n][1][0] * a1, C::kFew ? 0.f : s[h][n][1][C::E - 1] * a1);
+                if constexpr (C::kFine) {  // the other column holds what the rounding lost
+                    h0 = ptx::pack_f16x2(s[h][n][0][0] * a0, s[h][n][0][0] * a0 - unpack16<true>(h0).x);
+                    h1 = ptx::pack_f16x2(s[h][n][1][0] * a1, s[h][n][1][0] * a1 - unpack16<true>(h1).x);
+                }
                 pf[h][n][0] = movmatrix_trans(h0);
                 pf[h][n][1] = movmatrix_trans(h1);
                 // (the zeros meet the rounded weights, so that a weight's rounding is of its value's share only)
@@ -678,7 +691,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                     const float z0 = i4_zero(vw[h][0][g]), z1 = 15.f - i4_zero(vw[h][1][g]);
                     const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
                     w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
-                    if constexpr (!C::kFew) w.zo[n][g][C::E - 1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][C::E - 1]));
+                    if constexpr (!C::kFew || C::kFine) w.zo[n][g][C::E - 1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][C::E - 1]));
                 } else if constexpr (C::kPairs && H == 1) {
                     const uint32_t f[4] = {zr[0][0], 0u, kFifteen, zr[0][0] ^ kMinus};
                     mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
@@ -701,7 +714,8 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int e = 0; e < C::E; ++e) w.zo[n][g][(k * C::E + e) % C::ZE] += zs[n][2 * k + e];
+                    for (int e = 0; e < 2; ++e)
+                        if (e < C::E || C::kFine) w.zo[n][g][(k * C::E + (C::kFew ? 0 : e)) % C::ZE] += zs[n][2 * k + e];
         }
 #pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
@@ -762,6 +776,9 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
                 const float ref = inv == 0 ? 0.f : __uint_as_float((254u << 23) - inv);
 #pragma unroll
                 for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
+                    if constexpr (C::kFine)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) w.o[n][c][x][0] += w.o[n][c][x][1], w.o[n][c][x][2] += w.o[n][c][x][3];
                     w.o[n][c][0][e] = ref * fmaf(w.o[n][c][0][e], 16777216.f, -z);
                     w.o[n][c][0][2 + e] = ref * fmaf(w.o[n][c][0][2 + e], 1048576.f, -z);
                     w.o[n][c][1][e] = ref * fmaf(w.o[n][c][1][e], 16777216.f, -z);
