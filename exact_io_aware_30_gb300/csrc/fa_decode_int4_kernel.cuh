@@ -143,6 +143,10 @@ __device__ __forceinline__ void sts_float4(uint32_t addr, float a, float b, floa
     ptx::st_shared_v4(addr, __float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
 
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // ------------------------------------------------------------------- copies
 
 // A warp's next tile to copy lies in shared memory between its turns, so that the
@@ -178,9 +182,9 @@ __device__ __forceinline__ void dec_i4_advance(const DecInt4Params &p, DecFp8It 
     }
 }
 
-// Lane 4k + j copies part j (K codes, V codes, K words, V words) of block k of a
-// tile: whether there is such a block, and its table entry as loaded.  (Judged
-// when the copy begins, so that the load is not waited for here.)
+// Lanes 4k .. 4k + 3 stand for block k of a tile: whether there is such a block,
+// and its table entry as loaded.  (Judged when the copy begins, so that the load is
+// not waited for here.)
 template <class C>
 __device__ __forceinline__ bool dec_i4_entry(const DecInt4Params &p, const DecFp8It &it, int lane, int &entry) {
     const int n = ((it.tile * C::BN) >> p.bs_log2) + (lane >> 2);
@@ -189,27 +193,62 @@ __device__ __forceinline__ bool dec_i4_entry(const DecInt4Params &p, const DecFp
     return some;
 }
 
-// Copies a tile into a stage that is free.  The whole warp.  Slots behind the
-// request's blocks are not read later; a block outside the pool gets zero words,
-// whatever its codes.
+// BYTES (4, 8 or 16) from global to shared memory, completed on a barrier by copy_arrive.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A warp issues its TMA copies lane after lane.  With blocks of 16 a tile's words
+// are therefore copied by all lanes at once, those of every 32nd key each (128
+// requests x 40 heads 272 -> 263 us); with larger ones, of which a tile has few, by
+// TMA too (kv8, blocks of 64: by lanes 84.6 -> 87.2).
+__device__ __forceinline__ bool dec_i4_words_by_lanes(const DecInt4Params &p) { return p.bs_log2 == 4; }
+
+// Copies a tile into a stage that is free.  The whole warp: lane 4k + j has part j
+// (K codes, V codes, K words, V words) of block k.  Slots behind the request's
+// blocks are not read later; a block outside the pool gets zero words, whatever its
+// codes.
 template <class C>
 __device__ __forceinline__ void dec_i4_copy(const DecInt4Params &p, int kvh, bool some, int entry, int lane, uint32_t stage, uint32_t bar) {
     const bool in = some && entry >= 0 && entry < p.num_blocks;
-    const int part = lane & 3, row = (lane >> 2) << p.bs_log2;
-    const uint32_t word_bytes = (uint32_t)(C::NG * 4) << p.bs_log2;
-    const uint32_t words_at = stage + (part & 1 ? C::O_VW : C::O_KW) + row * C::NG * 4;
-    if (some && !in && part >= 2) {
-        for (uint32_t i = 0; i < word_bytes; i += 16) ptx::st_shared_v4(words_at + i, 0u, 0u, 0u, 0u);
-        ptx::fence_proxy_async_smem();
-    }
     const uint32_t blocks = (uint32_t)__popc(__ballot_sync(0xffffffffu, in)) / 4;
-    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, blocks * (2 * word_bytes + ((uint32_t)(2 * C::ROW) << p.bs_log2)));
+    const int part = lane & 3, row = (lane >> 2) << p.bs_log2;
+    constexpr int ROW_W = C::NG * 4, PIECE = ROW_W < 16 ? ROW_W : 16;
+    uint32_t bytes = blocks * ((uint32_t)(2 * C::ROW) << p.bs_log2);
+    const uint32_t word_bytes = (uint32_t)ROW_W << p.bs_log2, words_at = stage + (part & 1 ? C::O_VW : C::O_KW) + row * ROW_W;
+    if (some && !in && part >= 2)
+        for (uint32_t i = 0; i < word_bytes; i += 16) ptx::st_shared_v4(words_at + i, 0u, 0u, 0u, 0u);
+    if (dec_i4_words_by_lanes(p)) {
+        const int judged = in ? entry : -1;
+#pragma unroll
+        for (int i = 0; i < C::BN / 32; ++i) {
+            const int key = 32 * i + lane, e = __shfl_sync(0xffffffffu, judged, key >> 4 << 2);
+            if (e < 0) continue;
+            const uint32_t dst = stage + C::O_KW + key * ROW_W;
+            const size_t at = (((size_t)e * p.Hkv + kvh) * 16 + (key & 15)) * C::NG;
+#pragma unroll
+            for (int x = 0; x < ROW_W; x += PIECE) {
+                copy_async<PIECE>(dst + x, p.k_words + at + x / 4);
+                copy_async<PIECE>(dst + C::WORDS + x, p.v_words + at + x / 4);
+            }
+        }
+        copy_arrive(bar);
+    } else {
+        if (some && !in) ptx::fence_proxy_async_smem();  // (later copies of words to this stage come behind the zeros)
+        bytes += 2 * blocks * word_bytes;
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
     __syncwarp();
     if (in) {
         if (part < 2) {
             const uint64_t pol = p.chunks > 1 ? ptx::policy_evict_last() : ptx::policy_evict_first();
             ptx::tma_load_4d(stage + (part ? C::O_V : 0) + row * C::ROW, part ? &p.tm_v : &p.tm_k, bar, 0, 0, kvh, entry, pol);
-        } else {
+        } else if (!dec_i4_words_by_lanes(p)) {
             const size_t at = (((size_t)entry * p.Hkv + kvh) << p.bs_log2) * C::NG;
             ptx::bulk_load(words_at, (part & 1 ? p.v_words : p.k_words) + at, word_bytes, bar);
         }
@@ -232,10 +271,6 @@ __device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
@@ -310,8 +345,8 @@ __device__ __forceinline__ void dec_i4_load_q(const DecInt4Params &p, const DecF
 // exact in fp16 down to 2^-24 of it (and 2^-25 of the row's scale is the most a
 // smaller one is off).  A row with an infinity, a NaN or a component of 2^112 or
 // more is NaN.
-template <class C>
-__device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const uint4 (&raw)[C::NT][C::NC], int lane,
+template <class C, bool kFP16>
+__device__ __forceinline__ void dec_i4_q_unit(const DecInt4Params &p, const uint4 (&raw)[C::NT][C::NC], int lane,
                                                   DecI4Warp<C> &w) {
     const int t = lane & 3;
 #pragma unroll
@@ -324,7 +359,7 @@ __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const 
         mag = max(mag & 0xffffu, mag >> 16);
         mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
         mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-        const float top = p.fp16 ? unpack16<true>(mag).x : unpack16<false>(mag).x;
+        const float top = unpack16<kFP16>(mag).x;
         const uint32_t ex = max(__float_as_uint(top) >> 23, 20u);  // biased exponent
         const bool fine = ex < 127u + 112u;
         const float up = __uint_as_float((264u - min(ex, 238u)) << 23);
@@ -339,7 +374,7 @@ __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const 
             float x[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 f = p.fp16 ? unpack16<true>(ws[e]) : unpack16<false>(ws[e]);
+                const float2 f = unpack16<kFP16>(ws[e]);
                 x[2 * e] = f.x * up;
                 x[2 * e + 1] = f.y * up;
             }
@@ -379,6 +414,14 @@ __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const 
     }
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) w.inv[g] = 0.f;
+}
+
+template <class C>
+__device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const uint4 (&raw)[C::NT][C::NC], int lane,
+                                                  DecI4Warp<C> &w) {
+    if constexpr (C::kFew) dec_i4_q_unit<C, C::kFine>(p, raw, lane, w);
+    else if (p.fp16) dec_i4_q_unit<C, true>(p, raw, lane, w);
+    else dec_i4_q_unit<C, false>(p, raw, lane, w);
 }
 
 // log2 of the largest of a key's V scales relative to their references (a:
@@ -963,7 +1006,7 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     const uint32_t bars = ptx::smem_addr(bar_mem);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::ST; ++s) {
-            ptx::mbar_init(bar_addr(bars, C::B_FULL + s), 1);
+            ptx::mbar_init(bar_addr(bars, C::B_FULL + s), dec_i4_words_by_lanes(p) ? 1 + 32 : 1);  // (each lane's words, too)
             ptx::mbar_init(bar_addr(bars, C::B_EMPTY + s), C::WARPS);
         }
         ptx::mbar_init(bar_addr(bars, C::B_NEVER), 1);
