@@ -14,32 +14,45 @@
 // 0x00F000F0 two more, c 2^-20: a code costs 5/8 of an instruction.  The factor 16
 // between the two is taken out of q (whose odd components are 16 times smaller)
 // and of O's rows at the end.  Which components share a product's step is free,
-// so every product takes one group: 32 adjacent components, four words of 8, lane t
-// of four word t.  (Products by warps, mma.sync: the codes pass through registers
-// anyway, their fragments need no shared memory, and 16 keys and 8 rows to a
-// product are 0.3 of its rate at the memory's pace.)
+// so every product takes one chunk of 32 adjacent components of a group: four words
+// of 8, lane t of four word t.  These are products by warps (mma.sync m16n8k16, one
+// in 8 cycles of an SM's quarter): the codes pass through registers anyway, and what
+// they make needs no shared memory on its way in, and for up to 8 query rows a key's
+// products take a third of the time that its bytes take from memory.
 //   S^T = K Q^T: 16 keys x 8 rows per product, K words straight from shared memory.
 //   O^T = V^T P^T: ldmatrix transposes V by units of 16 bits, four codes of one
 //   key; the weights' fragment is S's, rounded to fp16 and turned by movmatrix.
-// Every other key's codes enter as 15 - c, with its weight negated (the
-// complement is part of the same masking instruction), so that O's sums, which
-// the tensor core cuts off rather than rounds, do not grow with the 7.5 that
-// codes are on average; what that leaves out goes with the zeros.
+// Half of the keys' codes enter O as 15 - c, with the weight negated (a complement
+// is part of the same masking instruction), so that O's sums, which the tensor core
+// cuts off rather than rounds, do not grow with the 7.5 that codes are on average;
+// what that leaves out goes with the zeros, whose products are begun anew each step
+// and summed in fp32.
 //
 // Weights.  What P V takes is p s / ref_g in fp16: 2^-11 of itself, and no finer
-// than 2^-25 of the row's largest product so far: rows are taken relative to a
-// running maximum M of x + log2 max_g (s / ref_g), which may stay up to 6 below
-// the true one, and each group's scales relative to a power of two that the
-// step's largest is kept within 2^8 of.  Both move rarely, by a branch of the
-// whole warp that rescales what it has summed.
+// than 2^-25 of about the row's largest product so far: rows are taken relative to a
+// running maximum M of x + log2 max_g (s / ref_g), 6 above it when it moves, and
+// each group's scales relative to a power of two that the step's largest is kept
+// within 2^8 of.  Both move rarely, by a branch of the whole warp that rescales what
+// it has summed.
 //
 // Work split: the line of 128-key tiles of fa_decode_fp8_kernel.cuh, an even
 // share of it per CTA, cut units merged by its second kernel.  One CTA: a ring of
-// tiles, K and V codes and words, that its eight warps take turns at filling; a
-// warp takes 16 keys of a tile (or fewer warps more keys, the others other rows)
-// and has a running maximum and sums of its own, so that nothing is exchanged
-// before the unit's end.  (With a ninth warp for the copies two CTAs' warps get 96
-// registers instead of 128.)
+// tiles, K and V codes and words, that its four warps take turns at filling; a warp
+// takes 32 keys of a tile, as two sixteens side by side (16 at a time where registers
+// do not hold their words; with more rows fewer warps more keys, the others other
+// rows), and has a running maximum and sums of its own, so that nothing is exchanged
+// before the unit's end, where half of the warps hand their sums to the other half at
+// a time.
+//
+// What bounds it (kv8: 64 requests, 32 heads on 8 K/V heads, up to 8,192 tokens, d 128,
+// bf16, groups of 32, 379 MB): the copies alone run at 57 us, the floor is 56 and the
+// kernel takes 84.  A step of 16 keys is 320 instructions of a warp, 88 of them masks and shifts at
+// half rate; the ALU is busy half of the time and the issue slots too, with three
+// warps to a scheduler, whose waits for one another's pipes and for their own results
+// fill the rest.  16 warps of one sixteen each (128 registers) take 103 us, 8 warps of
+// four sixteens 85 to 93, and copies by a ninth warp left two CTAs' warps 96 registers
+// and spilled (216).  Short units pay for their ends: 128 requests x 40 heads, nine
+// tiles to a unit, 262 us for a floor of 140.
 #pragma once
 
 #include <math.h>
@@ -74,7 +87,9 @@ struct DecI4Cfg {
     static constexpr bool kWide = D <= 128 && NT == 1;
     static constexpr int WARPS = 4;
     static constexpr int KW = WARPS / RG;         // warps along a tile's keys
-    static constexpr int H = D / G * NT <= 4 ? 2 : 1;  // sixteens of keys of a step, side by side, where registers hold their words
+    // Sixteens of keys of a step, side by side, where registers hold their words
+    // (kv8, one 103 us, two 84; 16 rows at d 64 106 and 97).
+    static constexpr int H = D / G * NT <= 4 ? 2 : 1;
     static constexpr int KEYS = 16 * H;
     static constexpr int BN = 128;
     static constexpr int SPT = BN / KEYS / KW;    // steps of a warp per tile
