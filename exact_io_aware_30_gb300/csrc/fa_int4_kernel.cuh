@@ -132,11 +132,12 @@ __device__ __forceinline__ Int4Group int4_quantise(const uint32_t (&w)[8], int l
 }
 
 // A thread stands for 16 adjacent values of one head of K or V and goes through
-// its CTA's rows, U in flight.  Bound by instructions (with 8 values a thread 206 for
-// 8 values, the issue slots 75 % busy): 40,008 rows x 8 heads at d 256 (430 MB) 172 us
-// with 8 values and plain divisions, 159 with extremes in pairs and quotients in
-// three steps, 112 with 16 values; four rows in flight 120, as registers leave fewer
-// warps.  128 rows x 40 heads 4.5 us: slots, then the later writers, then the stores.
+// its CTA's rows, U in flight.  Bound by instructions (with 8 values a thread it ran
+// 206 of them per row, the issue slots 75 % busy): 40,008 rows x 8 heads at d 256
+// (430 MB) 172 us with 8 values and plain divisions, 159 with extremes in pairs and
+// quotients in three steps, 112 with 16 values; four rows in flight 120, as registers
+// leave fewer warps.  128 rows x 40 heads 4.7 us: slots, then the later writers, then
+// the stores.
 template <bool kFP16, bool kVec>
 __global__ void __launch_bounds__(kInt4Threads) fa_cache_append_int4_kernel(const __grid_constant__ Int4AppendParams p) {
     __shared__ int s_slot[kInt4MaxRows + kInt4Look];

@@ -560,8 +560,9 @@ fa_status fa_cache_read_int4(const void *k_cache, const void *v_cache, const uns
  * 2^-34 of that.  A weight times its group's V scale is rounded to 11 bits before
  * P V (22 with fp16 q and up to four rows per K/V head), and to no finer than
  * 2^-25 of about the largest such product of the row (the groups' scales taken
- * relative to each group's usual one).  Sums are fp32.  Deterministic.  Two launches at most; the workspace's contents on entry
- * do not matter.  Arguments as for fa_decode_paged, except:
+ * relative to each group's usual one).  Sums are fp32.  Deterministic.  Two
+ * launches at most; the workspace's contents on entry do not matter.  Arguments
+ * as for fa_decode_paged, except:
  *
  *   k_cache, v_cache, k_scale, v_scale, group  as above; scales finite and >= 0
  *                or NaN
