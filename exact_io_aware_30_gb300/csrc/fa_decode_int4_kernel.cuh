@@ -848,7 +848,9 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
     {
 #pragma unroll
         for (int half = C::KW / 2; half > 0; half >>= 1) {
-            const uint32_t at = parts + (rg * (C::KW / 2) + kwi % half) * C::PART + lane * 16;
+            // (the last `half` places: a warp that hands its sums down writes where it has
+            // itself read the ones before, each lane its own; the others may still read)
+            const uint32_t at = parts + (rg * (C::KW / 2) + C::KW / 2 - half + kwi % half) * C::PART + lane * 16;
             if (kwi >= half && kwi < 2 * half) {
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n) {

@@ -208,6 +208,25 @@ def test_two_calls_give_the_same_bits_and_outputs_can_be_given():
         fa.decode_paged_int4(*dev, 2000, workspace=ws[:n - 1])
 
 
+@pytest.mark.parametrize("longest", [500, 900])  # units whole, units cut
+@pytest.mark.parametrize("H,Hkv,Sq,d,group,dtype", [(24, 24, 1, 128, 32, inputs.FP16), (24, 24, 1, 128, 64, inputs.BF16),
+                                                    (48, 24, 4, 64, 32, inputs.BF16), (24, 12, 8, 128, 32, inputs.FP16),
+                                                    (24, 24, 2, 256, 32, inputs.BF16), (12, 12, 16, 256, 64, inputs.FP16)])
+def test_many_short_units_give_the_same_bits_each_time(H, Hkv, Sq, d, group, dtype, longest):
+    """A CTA's warps hand their sums to each other at each unit's end, thousands of times per call: what one
+    hands on must not lie where another still reads.  Each of many calls gives the first's bits, and those are right."""
+    lens = [longest - 13 * i for i in range(32)]
+    p = _problem(len(lens), H, Hkv, Sq, d, group, 16, lens, dtype, seed=H + d + Sq)
+    dev = _device(p)
+    o, lse = fa.decode_paged_int4(*dev, longest)
+    _check(p, o, lse, "none", longest)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        again, again_lse = fa.decode_paged_int4(*dev, longest)
+        wrong += (again.view(torch.int16) != o.view(torch.int16)).sum() + (again_lse != lse).sum()
+    assert int(wrong) == 0
+
+
 def test_two_streams_at_once_and_two_graphs():
     ps = [_problem(4, 8, 2, 1, 128, 32, 16, [900 + i, 33, 1, 2000], inputs.BF16, seed=48 + i) for i in range(2)]
     devs = [_device(p) for p in ps]
