@@ -453,27 +453,31 @@ __device__ __forceinline__ float dec_i4_top(const float (&a)[C::NG]) {
 // than 2^8 away) and of the exponents (where a row's largest product is above
 // it) and rescales the sums.  vw: the V words of the lane's keys; s: their
 // scores' sums of products.  The whole warp.
+//   Where every group's reference rose, the exponents' may come down by as much, so
+// that products with later, lighter keys keep their bits.  A row's sum of weights
+// grows by that, and is kept below 2^kI4MostLog2: scales may be 2^240 apart, fp32's
+// sums not.  A row's sums take both steps at once, by the product of the factors, as one
+// of them alone could leave fp32's range.
+constexpr float kI4MostLog2 = 112.f;
+
 template <class C>
 __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw)[C::H][2][C::NG], const float (&s)[C::H][C::NT][2][C::E]) {
-    float rise = -INFINITY;  // log2 of the factor of the group that grows most
+    int rise = -1000;     // log2 of the factor of the group whose sums shrink least
+    float up[C::NG][2];   // the groups' factors, in two halves that are normal numbers
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
         float top = 0.f;
 #pragma unroll
         for (int h = 0; h < C::H; ++h) top = fmaxf(top, fmaxf(i4_scale(vw[h][0][g]), i4_scale(vw[h][1][g])));
         top = warp_max(top);  // (a NaN scale is passed over)
-        const uint32_t ex = min(max(__float_as_uint(top) >> 23, 13u), 253u);
-        const float old = w.inv[g] * (1.f / kI4Room), now = __uint_as_float((254u - ex) << 23);
+        const int ex = (int)min(max(__float_as_uint(top) >> 23, 13u), 253u);
+        const float old = w.inv[g] * (1.f / kI4Room), rel = top * old;
+        const int from = (int)(__float_as_uint(old) >> 23);  // (a power of two)
+        int to = from;
         if (old == 0.f) {
-            if (top > 0.f) w.inv[g] = now * kI4Room;
-            rise = fmaxf(rise, 0.f);
-            continue;
-        }
-        float factor = 1.f;
-        const float rel = top * old;
-        if (rel > 256.f) {
-            factor = now / old;  // < 1
-            w.inv[g] = now * kI4Room;
+            if (top > 0.f) w.inv[g] = __uint_as_float((uint32_t)(254 - ex) << 23) * kI4Room;
+        } else if (rel > 256.f) {
+            to = 254 - ex;
         } else if (rel < 0.00390625f && top > 0.f) {
             // downwards as far as the sums have room in fp32
             float most = 1.f;
@@ -488,25 +492,14 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
                 for (int z = 0; z < C::ZE; ++z) most = fmaxf(most, fabsf(w.zo[n][g][z]));
             }
             most = warp_max(most);
-            const uint32_t room = 200u - min(__float_as_uint(most) >> 23, 200u);  // up to 2^73
-            const uint32_t from = __float_as_uint(old) >> 23, to = min(254u - ex, from + room);
-            w.inv[g] = __uint_as_float(to << 23) * kI4Room;
-            factor = __uint_as_float((to - from + 127u) << 23);
+            const int room = 200 - (int)min(__float_as_uint(most) >> 23, 200u);  // up to 2^73
+            to = min(254 - ex, from + room);
         }
-        if (factor != 1.f) {
-#pragma unroll
-            for (int n = 0; n < C::NT; ++n) {
-#pragma unroll
-                for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w.o[n][c][h][e] *= factor;
-#pragma unroll
-                for (int z = 0; z < C::ZE; ++z) w.zo[n][g][z] *= factor;
-            }
-        }
-        rise = fmaxf(rise, lg2_approx(factor));
+        if (to != from) w.inv[g] = __uint_as_float((uint32_t)to << 23) * kI4Room;
+        const int shift = to - from, half = shift >> 1;
+        up[g][0] = __uint_as_float((uint32_t)(127 + half) << 23);
+        up[g][1] = __uint_as_float((uint32_t)(127 + shift - half) << 23);
+        rise = max(rise, shift);
     }
     float la[C::H][2];
 #pragma unroll
@@ -529,26 +522,35 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            // (where every group's reference rose, the exponents' may come down by as much)
-            const float old = w.m[n][e] + fminf(rise, 0.f), now = top > old ? top + kI4Ahead : old;
+            float old = w.m[n][e];
+            if (rise < 0) {  // (in the whole warp)
+                float l = w.l[n][e];
+                l = fmaxf(l, __shfl_xor_sync(0xffffffffu, l, 4));
+                l = fmaxf(l, __shfl_xor_sync(0xffffffffu, l, 8));
+                l = fmaxf(l, __shfl_xor_sync(0xffffffffu, l, 16));
+                old -= fminf((float)-rise, fmaxf(kI4MostLog2 - lg2_approx(fmaxf(l, 1.f)), 0.f));
+            }
+            const float now = top > old ? top + kI4Ahead : old;
             const float f = ptx::ex2_approx(w.m[n][e] - now);
             w.m[n][e] = now;
             w.l[n][e] *= f;
 #pragma unroll
-            for (int g = 0; g < C::NG; ++g)
+            for (int g = 0; g < C::NG; ++g) {
+                const float both = up[g][0] * f * up[g][1];
 #pragma unroll
-                for (int z = e; z < C::ZE; z += C::E) w.zo[n][g][z] *= f;
+                for (int z = e; z < C::ZE; z += C::E) w.zo[n][g][z] *= both;
 #pragma unroll
-            for (int c = 0; c < C::NC; ++c)
+                for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    w.o[n][c][h][e] *= f;
-                    w.o[n][c][h][2 + e] *= f;
-                    if constexpr (C::kFine) {
-                        w.o[n][c][h][1] *= f;
-                        w.o[n][c][h][3] *= f;
+                    for (int h = 0; h < 2; ++h) {
+                        w.o[n][c][h][e] *= both;
+                        w.o[n][c][h][2 + e] *= both;
+                        if constexpr (C::kFine) {
+                            w.o[n][c][h][1] *= both;
+                            w.o[n][c][h][3] *= both;
+                        }
                     }
-                }
+            }
         }
 }
 
