@@ -1158,6 +1158,9 @@ __global__ void __launch_bounds__(kDecFp8MergeThreads<RC>)
     int rows;
     const size_t row0 = dec_fp8_row0(p, cb, ckvh, cchunk, &rows);
     if (r >= rows) return;
+    // O's sum takes 2^-9 of each weight: with fewer partials than 2^9 (one of a CTA,
+    // three CTAs an SM) it stays finite where their mean does.
+    constexpr float kPart = 1.f / 512.f;
     float acc[PER], sum = 0.f, top = -INFINITY;
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
@@ -1176,7 +1179,7 @@ __global__ void __launch_bounds__(kDecFp8MergeThreads<RC>)
             const float w0 = __shfl_sync(0xffffffffu, weight, 0), w1 = __shfl_sync(0xffffffffu, weight, 1);
             sum = w0 + w1;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w1, row1_v[e], w0 * row0_v[e]);
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w1 * kPart, row1_v[e], w0 * kPart * row0_v[e]);
             i = 2;
         }
         // several partials' loads at a time, then their sums in order (one request
@@ -1198,13 +1201,13 @@ __global__ void __launch_bounds__(kDecFp8MergeThreads<RC>)
                 sum += w;
 #pragma unroll
                 for (int e = 0; e < PER; e += 2) {
-                    acc[e] = fmaf(w, v[j][e / 2].x, acc[e]);
-                    acc[e + 1] = fmaf(w, v[j][e / 2].y, acc[e + 1]);
+                    acc[e] = fmaf(w * kPart, v[j][e / 2].x, acc[e]);
+                    acc[e + 1] = fmaf(w * kPart, v[j][e / 2].y, acc[e + 1]);
                 }
             }
         }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / (sum * kPart);
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + (row0 + r) * D + lane * PER);
 #pragma unroll
     for (int e = 0; e < PER; e += 2) dst[e / 2] = pack2b<kFP16>(acc[e] * inv, acc[e + 1] * inv);

@@ -821,6 +821,11 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
         for (int e = 0; e < C::E; ++e) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) w.l[n][e] += __shfl_xor_sync(0xffffffffu, w.l[n][e], o);
+            // The reference goes to where the sum of weights is in [1/8, 1/4): sums of values near the
+            // largest numbers stay finite, and those of the warps can be compared by their references.
+            const int to = w.l[n][e] > 0.f ? min((int)(__float_as_uint(w.l[n][e]) >> 23) - 124, 126) : 0;
+            w.m[n][e] += (float)to;
+            w.l[n][e] *= __uint_as_float((uint32_t)(127 - to) << 23);
 #pragma unroll
             for (int g = 0; g < C::NG; ++g) {
                 float z = w.zo[n][g][e];
@@ -831,18 +836,23 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
                     z = __shfl_sync(0xffffffffu, z, 8 * (g & 3) + t);
                     if constexpr (C::ZE == 2 * C::E) z += __shfl_sync(0xffffffffu, w.zo[n][g][C::ZE - C::E + e], 16 + 8 * g + t);
                 }
-                // (the sums are kI4Room / ref too large)
+                // (the sums are kI4Room / ref too large, too; half of the step on either side of the
+                // difference, as all of it could leave fp32's range)
                 const uint32_t inv = __float_as_uint(w.inv[g]);
-                const float ref = inv == 0 ? 0.f : __uint_as_float((254u << 23) - inv);
+                const int step = 127 - (int)(inv >> 23) - to, half = step >> 1;
+                const float first = __uint_as_float((uint32_t)(127 + half) << 23);
+                const float second = inv == 0 ? 0.f : __uint_as_float((uint32_t)(127 + step - half) << 23);
+                const float lower = 16777216.f * first, upper = 1048576.f * first;
+                z *= first;
 #pragma unroll
                 for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
                     if constexpr (C::kFine)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) w.o[n][c][x][0] += w.o[n][c][x][1], w.o[n][c][x][2] += w.o[n][c][x][3];
-                    w.o[n][c][0][e] = ref * fmaf(w.o[n][c][0][e], 16777216.f, -z);
-                    w.o[n][c][0][2 + e] = ref * fmaf(w.o[n][c][0][2 + e], 1048576.f, -z);
-                    w.o[n][c][1][e] = ref * fmaf(w.o[n][c][1][e], 16777216.f, -z);
-                    w.o[n][c][1][2 + e] = ref * fmaf(w.o[n][c][1][2 + e], 1048576.f, -z);
+                    w.o[n][c][0][e] = second * fmaf(w.o[n][c][0][e], lower, -z);
+                    w.o[n][c][0][2 + e] = second * fmaf(w.o[n][c][0][2 + e], upper, -z);
+                    w.o[n][c][1][e] = second * fmaf(w.o[n][c][1][e], lower, -z);
+                    w.o[n][c][1][2 + e] = second * fmaf(w.o[n][c][1][2 + e], upper, -z);
                 }
             }
         }

@@ -87,7 +87,7 @@ def test_rows_that_do_not_see_the_key_whose_scale_is_far_larger(low, high, H, Sq
 @pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
 @pytest.mark.parametrize("H,Sq,d,group", ROWS)
 @pytest.mark.parametrize("scales,falls", [((-114, -43, 28, 99), 140.0), ((-114, -43, 28, 99), 60.0), ((-100, 10, -100, 20), 80.0),
-                                          ((-30, 34, 98, 110), 100.0), ((0, 30, 60, 90), 30.0)])
+                                          ((-30, 34, 98, 110), 100.0), ((0, 30, 60, 90), 30.0), ((-114, 113, -114, 113), 20.0)])
 def test_scores_that_fall_while_scales_rise(scales, falls, H, Sq, d, group, dtype):
     # tiles of 128 keys; the first keys of each have its scale and its score
     n = 385
@@ -95,4 +95,15 @@ def test_scores_that_fall_while_scales_rise(scales, falls, H, Sq, d, group, dtyp
     scores = 70.0 - falls * at + np.linspace(0, 1, n)
     p = _known(n, H, Sq, d, group, dtype, scores, 2.0 ** np.array(scales, np.float64)[at], H + d + 1)
     o, lse = fa.decode_paged_int4(*_device(p), n, scale=1.0, mask="none")
+    _check(p, o, lse, "none", n, n)
+
+
+@pytest.mark.parametrize("H,Sq,d,group", ROWS)
+@pytest.mark.parametrize("n", [33, 400, 1500])
+def test_many_even_keys_with_the_largest_values(n, H, Sq, d, group):
+    # a mean of values near the type's largest is finite, although their sum is not
+    p = _known(n, H, Sq, d, group, inputs.BF16, np.zeros(n), np.full(n, 2.0 ** 123), n + H)
+    p["vw"][:] = ref.words(np.full(d // group, 2.0 ** 123, np.float32), np.zeros(d // group))
+    o, lse = fa.decode_paged_int4(*_device(p), n, scale=1.0)
+    assert bool(torch.isfinite(o).all())
     _check(p, o, lse, "none", n, n)
