@@ -124,7 +124,7 @@ struct DecI4Cfg {
     static constexpr int B_EMPTY = ST;
     static constexpr int B_NEVER = 2 * ST;        // no arrivals (the stall test's wait)
     static constexpr int NUM_BARS = 2 * ST + 1;
-    static_assert(NUM_BARS * 8 + 32 * WARPS + 32 <= 512, "layout");
+    static_assert(NUM_BARS * 8 + 32 * WARPS + 16 + 4 * ST <= 512, "layout");
 };
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -937,7 +937,7 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
 
 template <class C>
 __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, uint32_t parts, uint32_t kept, uint32_t bars,
-                            int *copied, Ctl *ctl) {
+                            int *begun, Ctl *ctl) {
     const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5, rg = warp / C::KW, kwi = warp % C::KW;
     if (it.left <= 0) return;
     uint4 raw[C::NT][C::NC];
@@ -953,7 +953,7 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
         dec_i4_advance(p, ahead, warp);
         for (int n = warp; n < C::ST - 1; n += C::WARPS) {
             if (ahead.left > 0) {
-                if (lane == 0) atomicMax(copied, n + 1);
+                if (lane == 0) begun[n] = n + 1;
                 some = dec_i4_entry<C>(p, ahead, lane, entry);
                 dec_i4_copy<C>(p, ahead.kvh, some, entry, lane, ring + n * C::STAGE, bar_addr(bars, C::B_FULL + n));
             }
@@ -969,7 +969,8 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
     DecI4Warp<C> w;
     dec_i4_begin_unit<C>(p, raw, lane, w);
     bool begun_here = it.tile == 0, bad = false;
-    if (p.stall_test) bad = !wait_warp(bar_addr(bars, C::B_NEVER), 0, ctl, 92);
+    // (one warp's wait, so that the others wind down from wherever they are)
+    if (p.stall_test && warp == (int)(blockIdx.x % C::WARPS)) bad = !wait_warp(bar_addr(bars, C::B_NEVER), 0, ctl, 92);
     int slot = 0, turn = warp;      // turn: tiles until this warp's next copy
     uint32_t phase = 0;
     int t = 0;
@@ -994,7 +995,7 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
                 const int prev = slot == 0 ? C::ST - 1 : slot - 1;
                 bad = t > 0 && !wait_warp(bar_addr(bars, C::B_EMPTY + prev), slot == 0 ? phase ^ 1 : phase, ctl, 91);
                 if (!bad) {
-                    if (lane == 0) atomicMax(copied, t + C::ST);
+                    if (lane == 0) begun[prev] = t + C::ST;
                     dec_i4_copy<C>(p, coming.kvh, some, entry, lane, ring + prev * C::STAGE, bar_addr(bars, C::B_FULL + prev));
                     dec_i4_advance(p, coming, C::WARPS);
                     dec_i4_keep(coming, lane, kept);
@@ -1031,17 +1032,17 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     uint8_t *kept = parts + C::PARTS * C::PART;
     uint64_t *bar_mem = reinterpret_cast<uint64_t *>(kept + C::WARPS * kI4Kept);
     Ctl *ctl = reinterpret_cast<Ctl *>(bar_mem + C::NUM_BARS);
-    int *copied = reinterpret_cast<int *>(ctl + 1);  // tiles that copies were begun for
+    int *begun = reinterpret_cast<int *>(ctl + 1);  // [ST] 1 + the tile whose copy to a place was begun last; 0: none
     const uint32_t bars = ptx::smem_addr(bar_mem);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::ST; ++s) {
             ptx::mbar_init(bar_addr(bars, C::B_FULL + s), dec_i4_words_by_lanes(p) ? 1 + 32 : 1);  // (each lane's words, too)
             ptx::mbar_init(bar_addr(bars, C::B_EMPTY + s), C::WARPS);
+            begun[s] = 0;
         }
         ptx::mbar_init(bar_addr(bars, C::B_NEVER), 1);
         ctl->abort = 0;
         ctl->limit_ns = p.wait_limit_ns;
-        *copied = 0;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
         ptx::prefetch_tensormap(&p.tm_k);
@@ -1053,15 +1054,14 @@ __global__ void __launch_bounds__(C::NUM_THREADS, C::CTAS_PER_SM)
     // the merge may be set up now; it waits for this grid's end before it reads
     ptx::let_next_kernel_begin();
     dec_i4_warp<C>(p, it, ptx::smem_addr(ring), ptx::smem_addr(parts),
-                   ptx::smem_addr(kept) + (threadIdx.x >> 5) * kI4Kept, bars, copied, ctl);
+                   ptx::smem_addr(kept) + (threadIdx.x >> 5) * kI4Kept, bars, begun, ctl);
     __syncthreads();
-    // the CTA's memory stays until its last copies have landed, also where the
-    // warps gave up waiting for them
-    if (ctl->abort && threadIdx.x == 0) {
-        const int n = *copied;
-        for (int t = max(n - C::ST, 0); t < n; ++t)
-            wait_bar_drain(bar_addr(bars, C::B_FULL + t % C::ST), (t / C::ST) & 1);
-    }
+    // The CTA's memory stays until its last copies have landed, also where the
+    // warps gave up waiting for them.  (Where one gave up, tiles that were its turn
+    // are missing in between: each place has its own last tile.)
+    if (ctl->abort && threadIdx.x == 0)
+        for (int s = 0; s < C::ST; ++s)
+            if (const int n = begun[s]) wait_bar_drain(bar_addr(bars, C::B_FULL + s), ((n - 1) / C::ST) & 1);
 }
 
 }  // namespace fa
