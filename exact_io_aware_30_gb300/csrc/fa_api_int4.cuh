@@ -218,10 +218,19 @@ bool make_map_int4_codes(CUtensorMap *m, const void *base, int d, int bs, int Hk
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The kernel of a unit's rows (4, 8, 16 or 32): eights of rows per warp (at d = 256 a
+// warp's registers hold one) and groups of warps with different rows.
+constexpr int int4_warp_eights(int rc, int d) { return rc <= 8 || d == 256 ? 1 : 2; }
+constexpr int int4_row_groups(int rc, int d) { return rc <= 8 ? 1 : rc / (8 * int4_warp_eights(rc, d)); }
+
+struct DecInt4Plan : DecFp8Plan {
+    size_t sums_off = 0;  // 0: no unit is long enough to rest
+};
+
 // Rows of a K/V head: at most 4, 8 (a warp's columns), 16, or 32 in equal chunks of
 // at most that, the cache being read once more per chunk.
-DecFp8Plan plan_decode_int4(int B, int Hkv, int R, int d, int max_seq_len, int num_sms) {
-    DecFp8Plan pl;
+DecInt4Plan plan_decode_int4(int B, int Hkv, int R, int d, int max_seq_len, int num_sms) {
+    DecInt4Plan pl;
     pl.chunks = (R + 31) / 32;
     pl.rows_per_chunk = (R + pl.chunks - 1) / pl.chunks;
     if (pl.chunks > 1) pl.rows_per_chunk = (pl.rows_per_chunk + 7) / 8 * 8;  // (a warp has whole eights)
@@ -237,13 +246,18 @@ DecFp8Plan plan_decode_int4(int B, int Hkv, int R, int d, int max_seq_len, int n
         pl.part_o_off = (pl.part_lse_off + (size_t)2 * pl.grid * pl.rc * 4 + 255) / 256 * 256;
         pl.bytes = pl.part_o_off + (size_t)2 * pl.grid * pl.rc * d * 4;
     }
+    const int groups = int4_row_groups(pl.rc, d);
+    if (tiles > dec_i4_rest(groups)) {
+        pl.sums_off = pl.bytes;
+        pl.bytes += (size_t)pl.grid * groups * dec_i4_part(d, int4_warp_eights(pl.rc, d), pl.rc == 4 ? 1 : 2);
+    }
     return pl;
 }
 
 template <class C>
-fa_status launch_decode_int4_c(const DecInt4Params &p, const DecFp8Plan &pl, DeviceInfo &info, cudaStream_t stream) {
+fa_status launch_decode_int4_c(const DecInt4Params &p, const DecInt4Plan &pl, DeviceInfo &info, cudaStream_t stream) {
     constexpr int kind = C::kFine ? 0 : C::RC == 4 ? 1 : C::RC == 8 ? 2 : C::RC == 16 ? 3 : 4;
-    const int slot = ((C::D == 256 ? 2 : C::D == 128 ? 1 : 0) * 2 + (C::G == 64 ? 1 : 0)) * 5 + kind;
+    const int slot = (((C::D == 256 ? 2 : C::D == 128 ? 1 : 0) * 2 + (C::G == 64 ? 1 : 0)) * 2 + (C::kRests ? 1 : 0)) * 5 + kind;
     if (set_smem(fa_decode_int4_kernel<C>, C::SMEM_BYTES, info.attr_dec_int4[slot]) != FA_OK) return FA_ERR_CUDA;
     const fa_status st = launch_overlapped(fa_decode_int4_kernel<C>, dim3((unsigned)pl.grid), C::NUM_THREADS, C::SMEM_BYTES,
                                            1, stream, p);
@@ -253,16 +267,24 @@ fa_status launch_decode_int4_c(const DecInt4Params &p, const DecFp8Plan &pl, Dev
                              dim3((unsigned)(pl.grid - 1)), kDecFp8MergeThreads<C::RC>, 0, 1, stream, merge, pl.grid);
 }
 
-// 16 rows: two eights in a warp, or at d = 256, where a warp's registers hold one, in two warps.
-template <int D, int G>
-fa_status launch_decode_int4(const DecInt4Params &p, const DecFp8Plan &pl, DeviceInfo &info, cudaStream_t stream) {
-    constexpr int NT = D == 256 ? 1 : 2;
+template <int D, int G, bool kRests>
+fa_status launch_decode_int4_g(const DecInt4Params &p, const DecInt4Plan &pl, DeviceInfo &info, cudaStream_t stream) {
     if (pl.rc == 4)
-        return p.fp16 ? launch_decode_int4_c<DecI4Cfg<D, G, 1, 1, true, true>>(p, pl, info, stream)
-                      : launch_decode_int4_c<DecI4Cfg<D, G, 1, 1, true>>(p, pl, info, stream);
-    if (pl.rc == 8) return launch_decode_int4_c<DecI4Cfg<D, G, 1, 1>>(p, pl, info, stream);
-    if (pl.rc == 16) return launch_decode_int4_c<DecI4Cfg<D, G, NT, 2 / NT>>(p, pl, info, stream);
-    return launch_decode_int4_c<DecI4Cfg<D, G, NT, 4 / NT>>(p, pl, info, stream);
+        return p.fp16 ? launch_decode_int4_c<DecI4Cfg<D, G, 1, 1, true, true, kRests>>(p, pl, info, stream)
+                      : launch_decode_int4_c<DecI4Cfg<D, G, 1, 1, true, false, kRests>>(p, pl, info, stream);
+    if (pl.rc == 8) return launch_decode_int4_c<DecI4Cfg<D, G, 1, 1, false, false, kRests>>(p, pl, info, stream);
+    if (pl.rc == 16)
+        return launch_decode_int4_c<DecI4Cfg<D, G, int4_warp_eights(16, D), int4_row_groups(16, D), false, false, kRests>>(
+            p, pl, info, stream);
+    return launch_decode_int4_c<DecI4Cfg<D, G, int4_warp_eights(32, D), int4_row_groups(32, D), false, false, kRests>>(
+        p, pl, info, stream);
+}
+
+template <int D>
+fa_status launch_decode_int4(int group, const DecInt4Params &p, const DecInt4Plan &pl, DeviceInfo &info, cudaStream_t stream) {
+    if (group == 32)
+        return pl.sums_off ? launch_decode_int4_g<D, 32, true>(p, pl, info, stream) : launch_decode_int4_g<D, 32, false>(p, pl, info, stream);
+    return pl.sums_off ? launch_decode_int4_g<D, 64, true>(p, pl, info, stream) : launch_decode_int4_g<D, 64, false>(p, pl, info, stream);
 }
 
 fa_status check_dec_int4_sizes(int B, int H, int Hkv, int Sq, int d, int group, int block_size, int max_blocks,
@@ -293,7 +315,7 @@ fa_status decode_int4_impl(const void *q, const void *k_cache, const void *v_cac
     DeviceInfo *info = nullptr;
     st = device_info(&dev, &info);
     if (st != FA_OK) return st;
-    const DecFp8Plan pl = plan_decode_int4(B, Hkv, H / Hkv * Sq, d, max_seq_len, info->num_sms);
+    const DecInt4Plan pl = plan_decode_int4(B, Hkv, H / Hkv * Sq, d, max_seq_len, info->num_sms);
     const size_t need = pl.bytes;
     if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
     const size_t rows = (size_t)B * H * Sq, qo = rows * d * 2;
@@ -321,6 +343,7 @@ fa_status decode_int4_impl(const void *q, const void *k_cache, const void *v_cac
         p.part_lse = reinterpret_cast<float *>(ws + pl.part_lse_off);
         p.part_o = reinterpret_cast<float *>(ws + pl.part_o_off);
     }
+    if (pl.sums_off) p.sums = reinterpret_cast<float4 *>(ws + pl.sums_off);
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;
@@ -343,10 +366,9 @@ fa_status decode_int4_impl(const void *q, const void *k_cache, const void *v_cac
     if (log_enabled())
         std::fprintf(stderr, "[fa] fa_decode_paged_int4 d=%d group=%d B=%d H=%d Hkv=%d Sq=%d bs=%d max_len=%d rows=%d x %d grid=%d\n",
                      d, group, B, H, Hkv, Sq, block_size, max_seq_len, pl.rows_per_chunk, pl.chunks, pl.grid);
-    const bool g32 = group == 32;
-    if (d == 64) return g32 ? launch_decode_int4<64, 32>(p, pl, *info, stream) : launch_decode_int4<64, 64>(p, pl, *info, stream);
-    if (d == 128) return g32 ? launch_decode_int4<128, 32>(p, pl, *info, stream) : launch_decode_int4<128, 64>(p, pl, *info, stream);
-    return g32 ? launch_decode_int4<256, 32>(p, pl, *info, stream) : launch_decode_int4<256, 64>(p, pl, *info, stream);
+    if (d == 64) return launch_decode_int4<64>(group, p, pl, *info, stream);
+    if (d == 128) return launch_decode_int4<128>(group, p, pl, *info, stream);
+    return launch_decode_int4<256>(group, p, pl, *info, stream);
 }
 
 }  // namespace

@@ -65,10 +65,20 @@ namespace fa {
 
 struct DecInt4Params : DecFp8Params {  // (k_scale and v_scale are not used)
     const uint32_t *k_words, *v_words;  // [num_blocks, Hkv, bs, d / G]
+    float4 *sums;                       // [G, RG, PART / 16]: what a CTA's unit has summed in front of its last rest
     int fp16;
 };
 
-template <int D_, int G_, int NT_, int RG_, bool kFew_ = false, bool kFine_ = false>
+// Tiles of a unit after which a warp's sums are laid down and begun anew: 4,096 keys
+// of a warp, 256 products into each sum of O.  The tensor core cuts a sum off at each
+// of them, always towards 0, and the weights' sum is rounded 512 times; over a million
+// keys of about even weight lse was off by 2e-4 and O by 2^-10 and more.
+constexpr int dec_i4_rest(int row_groups) { return 32 * (4 / row_groups); }
+
+// Bytes of a warp's sums: nt eights of rows, of each of which a lane has e.
+constexpr int dec_i4_part(int d, int nt, int e) { return (e * nt * d / 32 + nt) * 512; }
+
+template <int D_, int G_, int NT_, int RG_, bool kFew_, bool kFine_, bool kRests_>
 struct DecI4Cfg {
     static constexpr int D = D_;
     static constexpr int G = G_;                  // components per group
@@ -93,6 +103,10 @@ struct DecI4Cfg {
     static constexpr int KEYS = 16 * H;
     static constexpr int BN = 128;
     static constexpr int SPT = BN / KEYS / KW;    // steps of a warp per tile
+    // A kernel of its own: with rests in all of them 128 requests x 40 heads took
+    // 269 us for 264, drafts at d 256 109 for 104.
+    static constexpr bool kRests = kRests_;
+    static constexpr int REST = dec_i4_rest(RG);
     // Which key of a step stands in row i + 8k of the products of sixteen h: SI i +
     // SK k + sixteen(h).  With two words to a key, 16 bytes hold those of two, and
     // the order is such that the transposed words have the zeros where their
@@ -110,7 +124,7 @@ struct DecI4Cfg {
     static constexpr int WORDS = BN * NG * 4;     // bytes of a tile's words
     static constexpr int O_V = TILE, O_KW = 2 * TILE, O_VW = O_KW + WORDS;  // places in a stage
     static constexpr int STAGE = (O_VW + WORDS + 1023) / 1024 * 1024;
-    static constexpr int PART = (E * NT * NC + NT) * 512;  // a warp's sums, on their way to another's
+    static constexpr int PART = dec_i4_part(D, NT, E);  // a warp's sums, on their way to another's
     static constexpr int PARTS = WARPS / 2;
     static constexpr int CTAS_PER_SM = kWide ? 3 : 2;
     static constexpr int BUDGET = (227 / CTAS_PER_SM - 1) * 1024;
@@ -809,11 +823,57 @@ __device__ __forceinline__ void dec_i4_meet(int rg) {
     else ptx::named_bar_sync(4, C::KW * 32);
 }
 
-// The unit's end.  A row group's warps hand their sums down, half of them to the
-// other half at a time; the last writes the rows out, or a partial of them.
+// A warp's sums as float4s of each lane: put(k, x) stores the k-th, get(k) loads it.
+template <class C, class Put>
+__device__ __forceinline__ void dec_i4_lay_down(const DecI4Warp<C> &w, Put put) {
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) {
+        put(C::E * C::NT * C::NC + n, make_float4(w.m[n][0], w.m[n][C::E - 1], w.l[n][0], w.l[n][C::E - 1]));
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+            for (int e = 0; e < C::E; ++e)
+                put((n * C::NC + c) * C::E + e,
+                    make_float4(w.o[n][c][0][e], w.o[n][c][0][2 + e], w.o[n][c][1][e], w.o[n][c][1][2 + e]));
+    }
+}
+
+// Adds such sums to a warp's.  (kMany: of any number of pieces, so that the sum of weights is kept below 1.)
+template <class C, bool kMany, class Get>
+__device__ __forceinline__ void dec_i4_join(DecI4Warp<C> &w, Get get) {
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) {
+        const float4 ml = get(C::E * C::NT * C::NC + n);
+        float mine[C::E], theirs[C::E];  // what the two sides' sums are multiplied by
+#pragma unroll
+        for (int e = 0; e < C::E; ++e) {
+            const float m = e ? ml.y : ml.x, top = fmaxf(w.m[n][e], m);
+            mine[e] = ptx::ex2_approx(w.m[n][e] - top);
+            theirs[e] = ptx::ex2_approx(m - top);
+            w.m[n][e] = top;
+            w.l[n][e] = fmaf(w.l[n][e], mine[e], (e ? ml.w : ml.z) * theirs[e]);
+            if (kMany && w.l[n][e] >= 1.f) w.l[n][e] *= 0.5f, mine[e] *= 0.5f, theirs[e] *= 0.5f, w.m[n][e] += 1.f;
+        }
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+            for (int e = 0; e < C::E; ++e) {
+                const float4 y = get((n * C::NC + c) * C::E + e);
+                float(&o)[2][4] = w.o[n][c];
+                o[0][e] = fmaf(o[0][e], mine[e], y.x * theirs[e]);
+                o[0][2 + e] = fmaf(o[0][2 + e], mine[e], y.y * theirs[e]);
+                o[1][e] = fmaf(o[1][e], mine[e], y.z * theirs[e]);
+                o[1][2 + e] = fmaf(o[1][2 + e], mine[e], y.w * theirs[e]);
+            }
+    }
+}
+
+// The unit's end, or a rest within it.  A row group's warps hand their sums down, half
+// of them to the other half at a time; the last adds what it laid down at earlier
+// rests and writes the rows out, or a partial of them, or lays them down.
 template <class C>
 __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const DecFp8It &it, DecI4Warp<C> &w, int rg, int kwi,
-                                                int lane, bool whole, bool begun_here, uint32_t parts) {
+                                                int lane, bool whole, bool begun_here, bool rested, bool rests, uint32_t parts) {
     const int i = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
@@ -863,48 +923,21 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
             // (the last `half` places: a warp that hands its sums down writes where it has
             // itself read the ones before, each lane its own; the others may still read)
             const uint32_t at = parts + (rg * (C::KW / 2) + C::KW / 2 - half + kwi % half) * C::PART + lane * 16;
-            if (kwi >= half && kwi < 2 * half) {
-#pragma unroll
-                for (int n = 0; n < C::NT; ++n) {
-                    sts_float4(at + (C::E * C::NT * C::NC + n) * 512, w.m[n][0], w.m[n][C::E - 1], w.l[n][0], w.l[n][C::E - 1]);
-#pragma unroll
-                    for (int c = 0; c < C::NC; ++c)
-#pragma unroll
-                        for (int e = 0; e < C::E; ++e)
-                            sts_float4(at + ((n * C::NC + c) * C::E + e) * 512, w.o[n][c][0][e], w.o[n][c][0][2 + e], w.o[n][c][1][e],
-                                       w.o[n][c][1][2 + e]);
-                }
-            }
+            if (kwi >= half && kwi < 2 * half)
+                dec_i4_lay_down<C>(w, [&](int k, float4 x) { sts_float4(at + k * 512, x.x, x.y, x.z, x.w); });
             dec_i4_meet<C>(rg);
-            if (kwi < half) {
-#pragma unroll
-                for (int n = 0; n < C::NT; ++n) {
-                    const float4 ml = lds_float4(at + (C::E * C::NT * C::NC + n) * 512);
-                    float mine[C::E], theirs[C::E];  // what the two sides' sums are multiplied by
-#pragma unroll
-                    for (int e = 0; e < C::E; ++e) {
-                        const float m = e ? ml.y : ml.x, top = fmaxf(w.m[n][e], m);
-                        mine[e] = ptx::ex2_approx(w.m[n][e] - top);
-                        theirs[e] = ptx::ex2_approx(m - top);
-                        w.m[n][e] = top;
-                        w.l[n][e] = fmaf(w.l[n][e], mine[e], (e ? ml.w : ml.z) * theirs[e]);
-                    }
-#pragma unroll
-                    for (int c = 0; c < C::NC; ++c)
-#pragma unroll
-                        for (int e = 0; e < C::E; ++e) {
-                            const float4 y = lds_float4(at + ((n * C::NC + c) * C::E + e) * 512);
-                            float(&o)[2][4] = w.o[n][c];
-                            o[0][e] = fmaf(o[0][e], mine[e], y.x * theirs[e]);
-                            o[0][2 + e] = fmaf(o[0][2 + e], mine[e], y.y * theirs[e]);
-                            o[1][e] = fmaf(o[1][e], mine[e], y.z * theirs[e]);
-                            o[1][2 + e] = fmaf(o[1][2 + e], mine[e], y.w * theirs[e]);
-                        }
-                }
-            }
+            if (kwi < half) dec_i4_join<C, false>(w, [&](int k) { return lds_float4(at + k * 512); });
         }
     }
     if (kwi != 0) return;
+    if constexpr (C::kRests) {
+        float4 *sums = p.sums + ((size_t)blockIdx.x * C::RG + rg) * (C::PART / 16) + lane;
+        if (rested) dec_i4_join<C, true>(w, [&](int k) { return sums[k * 32]; });
+        if (rests) {
+            dec_i4_lay_down<C>(w, [&](int k, float4 x) { sums[k * 32] = x; });
+            return;
+        }
+    }
     int rows;
     const size_t row0 = dec_fp8_row0(p, it.b, it.kvh, it.chunk, &rows);
     const size_t slot = 2 * (size_t)blockIdx.x + (begun_here ? 1 : 0);
@@ -972,6 +1005,7 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
     // (one warp's wait, so that the others wind down from wherever they are)
     if (p.stall_test && warp == (int)(blockIdx.x % C::WARPS)) bad = !wait_warp(bar_addr(bars, C::B_NEVER), 0, ctl, 92);
     int slot = 0, turn = warp;      // turn: tiles until this warp's next copy
+    int tiles = 0;                  // of the unit so far
     uint32_t phase = 0;
     int t = 0;
     for (;;) {
@@ -1007,15 +1041,16 @@ __device__ void dec_i4_warp(const DecInt4Params &p, DecFp8It it, uint32_t ring, 
         ++t;
         if (++slot == C::ST) slot = 0, phase ^= 1;
         const bool ends = it.tile + 1 == it.nt, done = it.left == 1;
-        if (ends || done) {
+        const bool rests = C::kRests && ++tiles % C::REST == 0 && !ends && !done;
+        if (ends || done || rests) {
             DecFp8It next = it;
             dec_fp8_step(p, next);
             if (!done) dec_i4_load_q<C>(p, next, rg, lane, raw);
-            dec_i4_end_unit<C>(p, it, w, rg, kwi, lane, begun_here && ends, begun_here, parts);
+            dec_i4_end_unit<C>(p, it, w, rg, kwi, lane, begun_here && ends, begun_here, tiles > C::REST, rests, parts);
             if (done) break;
             it = next;
             dec_i4_begin_unit<C>(p, raw, lane, w);
-            begun_here = true;
+            if (ends) begun_here = true, tiles = 0;
         } else {
             ++it.tile;
             --it.left;

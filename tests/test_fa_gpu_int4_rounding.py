@@ -1,0 +1,100 @@
+"""Attention over the 4-bit paged cache: what a weight's rounding and the sums of very long requests leave of O."""
+import numpy as np
+import pytest
+
+import int4_reference as ref
+import test_fa_gpu_int4 as base
+from exact_io_aware_30_gb300 import fa, inputs
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+_problem, _device, _dev, _t16 = base._problem, base._device, base._dev, base._t16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from exact_io_aware_30_gb300 import build
+    build.build()
+    fa.load()
+    torch.cuda.set_device(0)
+    yield
+    torch.cuda.synchronize()
+    assert fa.device_error() == fa.FA_OK
+
+
+def _scores(p, scores):
+    """Every row's scores by token, |score| <= 15 steps of bf16 (scale 1): q is the first unit vector."""
+    q = np.zeros(p["q"].shape, np.float32)
+    q[..., 0] = 1.0
+    p["q"] = inputs.to_bits(q, p["dtype"])
+    bs = p["bs"]
+    for b, L in enumerate(p["lens"]):
+        for j in range(int(L)):
+            block, at = p["table"][b, j // bs], j % bs
+            p["kw"][block, :, at], p["kc"][block, :, at] = 0, 0
+            p["kc"][block, :, at, 0] = 0x0F
+            p["kw"][block, :, at, 0] = ref.words(inputs.bits_to_f64(inputs.to_bits(
+                np.array([scores[j] / 15], np.float32), inputs.BF16), inputs.BF16).astype(np.float32), [0.0])[0]
+
+
+@pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
+@pytest.mark.parametrize("H,d,group", [(2, 128, 32), (4, 64, 64), (8, 128, 64), (32, 256, 32)])
+@pytest.mark.parametrize("down", [14.0, 17.0, 20.0])
+def test_a_first_key_that_outweighs_very_many_even_ones(down, H, d, group, dtype):
+    """Key 0 stands `down` (natural logarithm) above 131,071 even keys, whose table names one block again and again.
+    Their products lie 1.44 down below the row's largest: of the keys that share a warp's references with key 0, at
+    most 4,096, each is off by at most 2^-31 of that (2^-37, 6 ahead); the others' references are their own.  Beside
+    it a weight's 2^-11, the scores' share, 2^-15 of the sums, and one rounding of O."""
+    n, bs = 1 << 17, 128
+    rng = np.random.default_rng(int(down) + H)
+    p = _problem(1, H, 1, 1, d, group, bs, [2 * bs], dtype, seed=H, junk=False)
+    _scores(p, np.where(np.arange(2 * bs) == 0, down, 0.0))
+    table = np.full((1, n // bs), p["table"][0, 1], np.int32)
+    table[0, 0] = p["table"][0, 0]
+    dev = _device(p)
+    dev[5], dev[6] = _dev(table), _dev(np.array([n], np.int32))
+    o, lse = fa.decode_paged_int4(*dev, n, scale=1.0)
+    v = ref.gathered(p["vc"], p["vw"], p["table"][0], 2 * bs, bs)[0]
+    k = ref.gathered(p["kc"], p["kw"], p["table"][0], 2 * bs, bs)[0]
+    top = k[0, 0]
+    w = np.exp(k[:, 0] - top) * np.where(np.arange(2 * bs) < bs, 1, n // bs - 1)
+    want, spread, total = w @ v / w.sum(), w @ np.abs(v) / w.sum(), top + np.log(w.sum())
+    s, z = [np.concatenate([x[int(p["table"][0, i]), 0] for i in range(2)]) for x in ref.unpack_words(p["vw"])]
+    size = np.repeat(s * (15 + np.abs(z)), group, -1)
+    big = w @ size / w.sum()
+    tol = 2.0 ** -18 * 2 * top + 2.0 ** -20 * (1 + total)
+    assert float((lse.double() - total).abs().max()) <= tol
+    bound = (2.0 ** -11 + 2 * tol) * spread + 2.0 ** -15 * big + 4096 * 2.0 ** -31 * size.max(0) + base.U[dtype] * np.abs(want) + 2.0 ** -25
+    err = np.abs(o.double().cpu().numpy()[0, :, 0] - want)
+    assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("H,d,group,n", [(32, 256, 32, 1 << 20), (32, 128, 64, 1 << 20), (16, 256, 64, 1 << 20), (8, 64, 32, 1 << 21),
+                                         (4, 128, 32, 1 << 21)])
+def test_sums_over_very_long_requests_whose_codes_are_large(H, d, group, n):
+    """A unit per CTA, of so many keys that a sum cut off at each of their products, by up to 2^-23 of what it holds,
+    could lose 2^-8 of itself.  All codes are near 15.  The sums are allowed 2^-15 of sum p s (15 + |z|) (at most 256
+    products in a row, 2^-23 of what is held at each, and 512 pieces of them), those of the weights 2^-15 (512 in a row
+    and 512 pieces, 2^-25 each on the mean), a weight 2^-11 of its value, and the scores' share as in the other tests."""
+    B, bs = 152 * 3, 128
+    rng = np.random.default_rng(H + d)
+    p = _problem(1, H, 1, 1, d, group, bs, [bs], inputs.FP16, seed=d, junk=False, q_size=0.02)
+    p["vc"][:] = ref.pack(rng.integers(14, 16, (*p["vc"].shape[:-1], d)))
+    s, _ = ref.unpack_words(p["vw"])
+    p["vw"][:] = ref.words(s, rng.integers(7, 9, s.shape))
+    want, want_lse, spread, reach, big = [x[0, :, 0] for x in ref.decode(
+        inputs.bits_to_f64(p["q"], inputs.FP16), p["kc"], p["vc"], p["kw"], p["vw"], p["table"], p["lens"], bs,
+        1 / np.sqrt(d), "none", bs)]
+    dev = _device(p)
+    table = torch.full((1, n // bs), int(p["table"][0, 0]), dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    q = dev[0].expand(B, -1, -1, -1).contiguous()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    o, lse = fa.decode_paged_int4(q, *dev[1:5], table, lens, n)
+    want_lse = want_lse + np.log(n // bs)  # the same keys again and again
+    tol = 2.0 ** -18 * reach + 2.0 ** -20 * (1 + np.abs(want_lse)) + 2.0 ** -15
+    assert np.all(np.abs(lse[..., 0].double().cpu().numpy() - want_lse) <= tol)
+    bound = (2.0 ** -11 + 2 * tol[:, None]) * spread + 2.0 ** -15 * big + base.U[inputs.FP16] * np.abs(want)
+    err = np.abs(o[:, :, 0].double().cpu().numpy() - want)
+    assert np.all(err <= bound), float((err / bound).max())
