@@ -78,7 +78,7 @@ constexpr int dec_i4_rest(int row_groups) { return 32 * (4 / row_groups); }
 // Bytes of a warp's sums: nt eights of rows, of each of which a lane has e.
 constexpr int dec_i4_part(int d, int nt, int e) { return (e * nt * d / 32 + nt) * 512; }
 
-template <int D_, int G_, int NT_, int RG_, bool kFew_, bool kFine_, bool kRests_>
+template <int D_, int G_, int NT_, int RG_, bool kFew_, bool kRests_>
 struct DecI4Cfg {
     static constexpr int D = D_;
     static constexpr int G = G_;                  // components per group
@@ -87,11 +87,11 @@ struct DecI4Cfg {
     // Up to four rows stand in every other column of a product, so that a lane has
     // one of them and the work on the weights halves.
     static constexpr bool kFew = kFew_;
-    // The columns between them then hold what rounding a weight to fp16 lost, where
-    // O is fp16, whose own rounding is no coarser (128 requests x 40 heads: the error
-    // of O 1.33 -> 1.00 times that rounding, 266 -> 273 us).
-    static constexpr bool kFine = kFine_;
-    static_assert(kFew || !kFine, "a column for the rest");
+    // The columns between them hold what rounding a weight to fp16 lost, so that it has
+    // 22 bits, not 11.  fp16, 128 requests x 40 heads: the error of O 1.33 -> 1.00 times
+    // its own rounding, 266 -> 273 us when it came.  bf16: two keys that nearly cancel
+    // leave less than 2^-17 of their values in place of 2^-12, kv8 83 -> 87.6 us, with
+    // groups of 64 72 -> 74.
     static constexpr int E = kFew ? 1 : 2;        // rows of each eight columns that are a lane's
     static constexpr int RC = 4 * E * NT * RG;    // rows per unit
     static constexpr bool kWide = D <= 128 && NT == 1;
@@ -448,8 +448,7 @@ __device__ __forceinline__ void dec_i4_q_unit(const DecInt4Params &p, const uint
 template <class C>
 __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const uint4 (&raw)[C::NT][C::NC], int lane,
                                                   DecI4Warp<C> &w) {
-    if constexpr (C::kFew) dec_i4_q_unit<C, C::kFine>(p, raw, lane, w);
-    else if (p.fp16) dec_i4_q_unit<C, true>(p, raw, lane, w);
+    if (p.fp16) dec_i4_q_unit<C, true>(p, raw, lane, w);
     else dec_i4_q_unit<C, false>(p, raw, lane, w);
 }
 
@@ -559,7 +558,7 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
                     for (int h = 0; h < 2; ++h) {
                         w.o[n][c][h][e] *= both;
                         w.o[n][c][h][2 + e] *= both;
-                        if constexpr (C::kFine) {
+                        if constexpr (C::kFew) {
                             w.o[n][c][h][1] *= both;
                             w.o[n][c][h][3] *= both;
                         }
@@ -752,9 +751,9 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
             const float a0 = a[h][0][g], a1 = -a[h][1][g];
 #pragma unroll
             for (int n = 0; n < C::NT; ++n) {
-                uint32_t h0 = ptx::pack_f16x2(s[h][n][0][0] * a0, C::kFew ? 0.f : s[h][n][0][C::E - 1] * a0);
-                uint32_t h1 = ptx::pack_f16x2(s[h][n][1][0] * a1, C::kFew ? 0.f : s[h][n][1][C::E - 1] * a1);
-                if constexpr (C::kFine) {  // the other column holds what the rounding lost
+                uint32_t h0 = ptx::pack_f16x2(s[h][n][0][0] * a0, s[h][n][0][C::E - 1] * a0);
+                uint32_t h1 = ptx::pack_f16x2(s[h][n][1][0] * a1, s[h][n][1][C::E - 1] * a1);
+                if constexpr (C::kFew) {  // the other column holds what the rounding lost
                     h0 = ptx::pack_f16x2(s[h][n][0][0] * a0, s[h][n][0][0] * a0 - unpack16<true>(h0).x);
                     h1 = ptx::pack_f16x2(s[h][n][1][0] * a1, s[h][n][1][0] * a1 - unpack16<true>(h1).x);
                 }
@@ -765,7 +764,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                     const float z0 = i4_zero(vw[h][0][g]), z1 = 15.f - i4_zero(vw[h][1][g]);
                     const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
                     w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
-                    if constexpr (!C::kFew || C::kFine) w.zo[n][g][C::E - 1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][C::E - 1]));
+                    w.zo[n][g][C::E - 1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][C::E - 1]));
                 } else if constexpr (C::kPairs && H == 1) {
                     const uint32_t f[4] = {zr[0][0], 0u, kFifteen, zr[0][0] ^ kMinus};
                     mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
@@ -789,7 +788,7 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if (e < C::E || C::kFine) w.zo[n][g][(k * C::E + (C::kFew ? 0 : e)) % C::ZE] += zs[n][2 * k + e];
+                        w.zo[n][g][(k * C::E + (C::kFew ? 0 : e)) % C::ZE] += zs[n][2 * k + e];
         }
 #pragma unroll
         for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
@@ -906,7 +905,7 @@ __device__ __forceinline__ void dec_i4_end_unit(const DecInt4Params &p, const De
                 z *= first;
 #pragma unroll
                 for (int c = g * C::G / 32; c < (g + 1) * C::G / 32; ++c) {
-                    if constexpr (C::kFine)
+                    if constexpr (C::kFew)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) w.o[n][c][x][0] += w.o[n][c][x][1], w.o[n][c][x][2] += w.o[n][c][x][3];
                     w.o[n][c][0][e] = second * fmaf(w.o[n][c][0][e], lower, -z);

@@ -558,7 +558,7 @@ fa_status fa_cache_read_int4(const void *k_cache, const void *v_cache, const uns
  * attention over the values of its codes, q and o in 16 bits.  q enters exactly,
  * but for components below 2^-24 of their row's largest: those may be off by
  * 2^-34 of that.  A weight times its group's V scale is rounded to 11 bits before
- * P V (22 with fp16 q and up to four rows per K/V head), and to no finer than
+ * P V (22 with up to four rows per K/V head), and to no finer than
  * 2^-25 of about the largest such product of the row (the groups' scales taken
  * relative to each group's usual one).  Sums are fp32.  Deterministic.  Two
  * launches at most; the workspace's contents on entry do not matter.  Arguments

@@ -24,6 +24,24 @@ def _lib():
     assert fa.device_error() == fa.FA_OK
 
 
+def _check_fine(p, o, lse, max_len, scale, mask="none"):
+    """Up to four rows per K/V head a weight times its scale is held in two fp16 numbers, 2^-22 of it; the second's
+    smallest half step is 2^-25, no more than that of a product of 2^-3 or more, 2^9 below a row's largest (2^6 at
+    least when it is summed), and here all lie nearer.  The rest as in the attention's other tests: the scores', the
+    sums' 2^-17 of sum p s (15 + |z|) (2^-23 of what is held at each of at most 64 products), and one rounding of O."""
+    q = inputs.bits_to_f64(p["q"], p["dtype"])
+    want, want_lse, spread, reach, big = ref.decode(q, p["kc"], p["vc"], p["kw"], p["vw"], p["table"], p["lens"],
+                                                    max_len, scale, mask, p["bs"])
+    tol = 2.0 ** -18 * reach + 2.0 ** -20 * (1 + np.abs(want_lse))
+    err = np.abs(lse.double().cpu().numpy() - want_lse)
+    assert np.all(err <= tol), float((err / tol).max())
+    bound = (2.0 ** -22 + 2 * tol[..., None]) * spread + 2.0 ** -17 * big + base.U[p["dtype"]] * np.abs(want)
+    if p["dtype"] == inputs.FP16:
+        bound = bound + 2.0 ** -25
+    err = np.abs(o.double().cpu().numpy() - want)
+    assert np.all(err <= bound), float((err / bound).max())
+
+
 def _scores(p, scores):
     """Every row's scores by token, |score| <= 15 steps of bf16 (scale 1): q is the first unit vector."""
     q = np.zeros(p["q"].shape, np.float32)
@@ -37,6 +55,50 @@ def _scores(p, scores):
             p["kc"][block, :, at, 0] = 0x0F
             p["kw"][block, :, at, 0] = ref.words(inputs.bits_to_f64(inputs.to_bits(
                 np.array([scores[j] / 15], np.float32), inputs.BF16), inputs.BF16).astype(np.float32), [0.0])[0]
+
+
+@pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
+@pytest.mark.parametrize("H,Hkv,Sq", [(2, 2, 1), (4, 2, 1), (4, 1, 1), (2, 2, 4)])
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)])
+def test_up_to_four_rows_two_keys_that_nearly_cancel(d, group, H, Hkv, Sq, dtype):
+    # V of the second key is that of the first with its sign turned: O is the difference of two weights times V,
+    # and a weight rounded to 11 bits would be seen in it
+    p = _problem(8, H, Hkv, Sq, d, group, 16, [2] * 8, dtype, seed=d + H, q_size=0.002)
+    for b in range(8):
+        block = p["table"][b, 0]
+        p["vc"][block, :, 1] = 0xFF - p["vc"][block, :, 0]
+        s, z = ref.unpack_words(p["vw"][block, :, 0])
+        p["vw"][block, :, 0] = ref.words(s, np.rint(z))
+        p["vw"][block, :, 1] = ref.words(s, 15 - np.rint(z))
+    o, lse = fa.decode_paged_int4(*_device(p), 2)
+    _check_fine(p, o, lse, 2, 1 / np.sqrt(d))
+
+
+@pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)])
+@pytest.mark.parametrize("n", [1, 7, 40, 129, 520])
+def test_up_to_four_rows_of_few_keys(n, d, group, dtype):
+    p = _problem(3, 4, 1, 1, d, group, 16, [n, max(1, n - 1), n], dtype, seed=n + d, q_size=0.05)
+    o, lse = fa.decode_paged_int4(*_device(p), n)
+    _check_fine(p, o, lse, n, 1 / np.sqrt(d))
+
+
+@pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)])
+@pytest.mark.parametrize("rise", [6.0, 9.0])
+def test_up_to_four_rows_whose_references_move(rise, d, group, dtype):
+    # a key in every 32 carries the weight, and those of a tile lie above those of the tile in front, so that all
+    # sums are rescaled (the rest of the weights too); the last tile's values are 0, so that O is what the tiles in
+    # front of it left
+    n = 4 * 128
+    p = _problem(1, 4, 1, 1, d, group, 16, [n], dtype, seed=d, junk=False)
+    _scores(p, np.where(np.arange(n) % 32 == 0, 20.0 + rise * (np.arange(n) // 128), 0.0))
+    for j in range(n - 128, n):
+        block, at = p["table"][0, j // 16], j % 16
+        p["vc"][block, 0, at] = 0x88
+        p["vw"][block, 0, at] = ref.words(np.ones(d // group, np.float32), np.full(d // group, 8.0))
+    o, lse = fa.decode_paged_int4(*_device(p), n, scale=1.0)
+    _check_fine(p, o, lse, n, 1.0)
 
 
 @pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
