@@ -28,12 +28,16 @@
 // what that leaves out goes with the zeros, whose products are begun anew each step
 // and summed in fp32.
 //
-// Weights.  What P V takes is p s / ref_g in fp16: 2^-11 of itself, and no finer
-// than 2^-25 of about the row's largest product so far: rows are taken relative to a
-// running maximum M of x + log2 max_g (s / ref_g), 6 above it when it moves, and
-// each group's scales relative to a power of two that the step's largest is kept
-// within 2^8 of.  Both move rarely, by a branch of the whole warp that rescales what
-// it has summed.
+// Weights.  What P V takes is p s / ref_g in fp16: 2^-11 of itself (with up to four
+// rows 2^-22, in two numbers), and no finer than 2^-25 where 2^12 stands for the row's
+// reference: rows are taken relative to a running maximum M of x + log2 max_g (s /
+// ref_g), 6 above it when it moves, and each group's scales relative to a power of two
+// that the step's largest is kept within 2^8 of.  So the smallest half step is 2^-31 of
+// the row's largest product where a group's scales are alike, and at most 2^-23.  Both
+// move rarely, by a branch of the whole warp that rescales what it has summed.
+//
+// Sums.  The tensor core cuts a sum off, towards 0, at each product into it; after 256
+// products (4,096 keys of a warp) the sums are laid down and begun anew (REST).
 //
 // Work split: the line of 128-key tiles of fa_decode_fp8_kernel.cuh, an even
 // share of it per CTA, cut units merged by its second kernel.  One CTA: a ring of
