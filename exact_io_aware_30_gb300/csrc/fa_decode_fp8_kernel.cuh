@@ -310,7 +310,6 @@ __device__ DecFp8It dec_fp8_begin(const DecFp8Params &p, long long *scratch) {
             scratch[W + 1] = at;
             scratch[W + 2] = L;
             scratch[W + 3] = dec_fp8_len(p, b + 1);
-            scratch[W + 4] = n;
         }
         __syncthreads();
         if (scratch[W] >= 0) break;  // (lo lies in some request)
@@ -319,7 +318,7 @@ __device__ DecFp8It dec_fp8_begin(const DecFp8Params &p, long long *scratch) {
     }
     it.b = (int)scratch[W];
     it.L = (int)scratch[W + 2];
-    it.nt = (int)scratch[W + 4];
+    it.nt = dec_fp8_tiles(it.L);
     it.next_len = (int)scratch[W + 3];
     const long long off = lo - scratch[W + 1] * hc;
     const int unit = (int)(off / it.nt);
