@@ -35,7 +35,7 @@ struct Int4AppendParams {
     const int *slot_map;        // [T]
     long long slots;            // num_blocks * bs
     int T, Hkv, d_log2, g_log2, bs_log2, rows_per_cta;
-    int items_log2;             // threads along a row's (K or V, head, vector of 8) items
+    int items_log2;             // threads along a row's (K or V, head, vector of 16) items
 };
 
 // The integer nearest to y (ties to even), |y| < 2^22: in [2^23, 2^24) the step
