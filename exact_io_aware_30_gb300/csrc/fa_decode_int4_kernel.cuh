@@ -480,7 +480,7 @@ constexpr float kI4MostLog2 = 112.f;
 template <class C>
 __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw)[C::H][2][C::NG], const float (&s)[C::H][C::NT][2][C::E]) {
     int rise = -1000;     // log2 of the factor of the group whose sums shrink least
-    float up[C::NG][2];   // the groups' factors, in two halves that are normal numbers
+    int shift[C::NG];     // log2 of the groups' factors
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
         float top = 0.f;
@@ -513,10 +513,8 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
             to = min(254 - ex, from + room);
         }
         if (to != from) w.inv[g] = __uint_as_float((uint32_t)to << 23) * kI4Room;
-        const int shift = to - from, half = shift >> 1;
-        up[g][0] = __uint_as_float((uint32_t)(127 + half) << 23);
-        up[g][1] = __uint_as_float((uint32_t)(127 + shift - half) << 23);
-        rise = max(rise, shift);
+        shift[g] = to - from;
+        rise = max(rise, shift[g]);
     }
     float la[C::H][2];
 #pragma unroll
@@ -553,7 +551,8 @@ __device__ __forceinline__ void dec_i4_move(DecI4Warp<C> &w, const uint32_t (&vw
             w.l[n][e] *= f;
 #pragma unroll
             for (int g = 0; g < C::NG; ++g) {
-                const float both = up[g][0] * f * up[g][1];
+                const int half = shift[g] >> 1;  // (in halves, which are normal numbers)
+                const float both = __uint_as_float((uint32_t)(127 + half) << 23) * f * __uint_as_float((uint32_t)(127 + shift[g] - half) << 23);
 #pragma unroll
                 for (int z = e; z < C::ZE; z += C::E) w.zo[n][g][z] *= both;
 #pragma unroll
