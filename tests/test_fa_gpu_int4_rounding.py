@@ -160,3 +160,51 @@ def test_sums_over_very_long_requests_whose_codes_are_large(H, d, group, n):
     bound = (2.0 ** -11 + 2 * tol[:, None]) * spread + 2.0 ** -15 * big + base.U[inputs.FP16] * np.abs(want)
     err = np.abs(o[:, :, 0].double().cpu().numpy() - want)
     assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("mask", ["causal", "none"])
+@pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
+@pytest.mark.parametrize("H,Hkv,Sq,d,group,n", [(32, 4, 4, 256, 32, 1 << 20), (16, 4, 1, 128, 32, 1 << 21), (64, 4, 1, 128, 64, 1 << 21),
+                                                (32, 4, 1, 64, 32, 1 << 21), (40, 4, 4, 128, 32, 1 << 20)])
+def test_long_units_that_are_cut_and_rest(H, Hkv, Sq, d, group, n, dtype, mask):
+    """Units longer than a CTA's share, and shares longer than sums are kept: partials of pieces.  A second request is
+    short.  Each call gives the same bits, replayed from a graph too.  Bounds as above."""
+    bs = 128
+    lens = [n - 37, 300]
+    p = _problem(1, H, Hkv, Sq, d, group, bs, [3 * bs], dtype, seed=H + d, junk=False, q_size=0.02)
+    dev = _device(p)
+    table = torch.full((2, n // bs), -1, dtype=torch.int32)
+    table[0] = torch.from_numpy(p["table"][0])[torch.arange(n // bs) % 3]
+    table[1, :3] = torch.from_numpy(p["table"][0])
+    q, table = dev[0].expand(2, -1, -1, -1).contiguous(), table.cuda()
+    given = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = fa.decode_paged_int4(q, *dev[1:5], table, given, n, mask=mask)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = fa.decode_paged_int4(q, *dev[1:5], table, given, n, mask=mask)
+    for _ in range(2):
+        graph.replay()
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    k, v = [ref.gathered(p[c], p[w], p["table"][0], 3 * bs, bs) for c, w in (("kc", "kw"), ("vc", "vw"))]
+    sizes = []
+    for w in ("kw", "vw"):
+        s, z = ref.unpack_words(np.concatenate([p[w][int(p["table"][0, i])] for i in range(3)], 1))
+        sizes.append(np.repeat(s * (15 + np.abs(z)), group, -1))  # [Hkv, 384, d]
+    x = inputs.bits_to_f64(p["q"], dtype)[0]
+    for b, L in enumerate(lens):
+        for h in range(H):
+            g = h // (H // Hkv)
+            for i in range(Sq):
+                seen = L if mask == "none" else L - Sq + 1 + i
+                times = seen // (3 * bs) + (np.arange(3 * bs) < seen % (3 * bs))
+                score = x[h, i] @ k[g].T / np.sqrt(d)
+                top = score[times > 0].max()
+                w = times * np.exp(score - top)
+                total = top + np.log(w.sum())
+                w = w / w.sum()
+                tol = 2.0 ** -18 * (np.abs(x[h, i]) @ sizes[0][g].T).max() / np.sqrt(d) + 2.0 ** -20 * (1 + abs(total)) + 2.0 ** -15
+                assert abs(float(lse[b, h, i]) - total) <= tol
+                want = w @ v[g]
+                bound = (2.0 ** -11 + 2 * tol) * (w @ np.abs(v[g])) + 2.0 ** -15 * (w @ sizes[1][g]) + \
+                    base.U[dtype] * np.abs(want) + 2.0 ** -25
+                assert np.all(np.abs(o[b, h, i].double().cpu().numpy() - want) <= bound)
