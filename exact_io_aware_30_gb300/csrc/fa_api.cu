@@ -47,7 +47,7 @@ struct DeviceInfo {
     bool attr_dec[6] = {false, false, false, false, false, false};
     bool attr_fp8[3] = {false, false, false};  // 8-bit forward, d = 64, 128, 256
     bool attr_dec_fp8[36] = {};  // 8-bit cache decode: d = 64, 128, 256 x bf16, fp16 x rows
-    bool attr_dec_int4[48] = {};  // 4-bit cache decode: d = 64, 128, 256 x groups of 32, 64 x long units x rows
+    bool attr_dec_int4[84] = {};  // 4-bit cache decode: d = 64, 128, 256 x groups of 32, 64 x long units x rows
     bool attr_gemv[12] = {};  // few-row decode: d = 64, 128, 256 x bf16, fp16 x 1, 2 rows
 };
 

@@ -256,8 +256,8 @@ DecInt4Plan plan_decode_int4(int B, int Hkv, int R, int d, int max_seq_len, int 
 
 template <class C>
 fa_status launch_decode_int4_c(const DecInt4Params &p, const DecInt4Plan &pl, DeviceInfo &info, cudaStream_t stream) {
-    constexpr int kind = C::RC == 4 ? 0 : C::RC == 8 ? 1 : C::RC == 16 ? 2 : 3;
-    const int slot = (((C::D == 256 ? 2 : C::D == 128 ? 1 : 0) * 2 + (C::G == 64 ? 1 : 0)) * 2 + (C::kRests ? 1 : 0)) * 4 + kind;
+    constexpr int kind = C::RC == 4 ? 0 : (C::RC == 8 ? 1 : C::RC == 16 ? 3 : 5) + (C::kTwice ? 1 : 0);
+    const int slot = (((C::D == 256 ? 2 : C::D == 128 ? 1 : 0) * 2 + (C::G == 64 ? 1 : 0)) * 2 + (C::kRests ? 1 : 0)) * 7 + kind;
     if (set_smem(fa_decode_int4_kernel<C>, C::SMEM_BYTES, info.attr_dec_int4[slot]) != FA_OK) return FA_ERR_CUDA;
     const fa_status st = launch_overlapped(fa_decode_int4_kernel<C>, dim3((unsigned)pl.grid), C::NUM_THREADS, C::SMEM_BYTES,
                                            1, stream, p);
@@ -267,15 +267,21 @@ fa_status launch_decode_int4_c(const DecInt4Params &p, const DecInt4Plan &pl, De
                              dim3((unsigned)(pl.grid - 1)), kDecFp8MergeThreads<C::RC>, 0, 1, stream, merge, pl.grid);
 }
 
+template <int D, int G, int RC, bool kRests>
+fa_status launch_decode_int4_rc(const DecInt4Params &p, const DecInt4Plan &pl, DeviceInfo &info, cudaStream_t stream) {
+    constexpr int NT = int4_warp_eights(RC, D), RG = int4_row_groups(RC, D);
+    if constexpr (RC == 4) return launch_decode_int4_c<DecI4Cfg<D, G, NT, RG, true, false, kRests>>(p, pl, info, stream);
+    else
+        return p.fp16 ? launch_decode_int4_c<DecI4Cfg<D, G, NT, RG, false, true, kRests>>(p, pl, info, stream)
+                      : launch_decode_int4_c<DecI4Cfg<D, G, NT, RG, false, false, kRests>>(p, pl, info, stream);
+}
+
 template <int D, int G, bool kRests>
 fa_status launch_decode_int4_g(const DecInt4Params &p, const DecInt4Plan &pl, DeviceInfo &info, cudaStream_t stream) {
-    if (pl.rc == 4) return launch_decode_int4_c<DecI4Cfg<D, G, 1, 1, true, kRests>>(p, pl, info, stream);
-    if (pl.rc == 8) return launch_decode_int4_c<DecI4Cfg<D, G, 1, 1, false, kRests>>(p, pl, info, stream);
-    if (pl.rc == 16)
-        return launch_decode_int4_c<DecI4Cfg<D, G, int4_warp_eights(16, D), int4_row_groups(16, D), false, kRests>>(
-            p, pl, info, stream);
-    return launch_decode_int4_c<DecI4Cfg<D, G, int4_warp_eights(32, D), int4_row_groups(32, D), false, kRests>>(
-        p, pl, info, stream);
+    if (pl.rc == 4) return launch_decode_int4_rc<D, G, 4, kRests>(p, pl, info, stream);
+    if (pl.rc == 8) return launch_decode_int4_rc<D, G, 8, kRests>(p, pl, info, stream);
+    if (pl.rc == 16) return launch_decode_int4_rc<D, G, 16, kRests>(p, pl, info, stream);
+    return launch_decode_int4_rc<D, G, 32, kRests>(p, pl, info, stream);
 }
 
 template <int D>

@@ -29,7 +29,7 @@
 // and summed in fp32.
 //
 // Weights.  What P V takes is p s / ref_g in fp16: 2^-11 of itself (with up to four
-// rows 2^-22, in two numbers), and no finer than 2^-25 where 2^12 stands for the row's
+// rows, or fp16 q, 2^-22, in two numbers), and no finer than 2^-25 where 2^12 stands for the row's
 // reference: rows are taken relative to a running maximum M of x + log2 max_g (s /
 // ref_g), 6 above it when it moves, and each group's scales relative to a power of two
 // that the step's largest is kept within 2^8 of.  So the smallest half step is 2^-31 of
@@ -37,7 +37,7 @@
 // move rarely, by a branch of the whole warp that rescales what it has summed.
 //
 // Sums.  The tensor core cuts a sum off, towards 0, at each product into it; after 256
-// products (4,096 keys of a warp) the sums are laid down and begun anew (REST).
+// products (4,096 keys of a warp; 512 with those of weights' rests) the sums are laid down and begun anew (REST).
 //
 // Work split: the line of 128-key tiles of fa_decode_fp8_kernel.cuh, an even
 // share of it per CTA, cut units merged by its second kernel.  One CTA: a ring of
@@ -74,7 +74,7 @@ struct DecInt4Params : DecFp8Params {  // (k_scale and v_scale are not used)
 };
 
 // Tiles of a unit after which a warp's sums are laid down and begun anew: 4,096 keys
-// of a warp, 256 products into each sum of O.  The tensor core cuts a sum off at each
+// of a warp, 256 products into each sum of O (512 with kTwice).  The tensor core cuts a sum off at each
 // of them, always towards 0, and the weights' sum is rounded 512 times; over a million
 // keys of about even weight lse was off by 2e-4 and O by 2^-10 and more.
 constexpr int dec_i4_rest(int row_groups) { return 32 * (4 / row_groups); }
@@ -82,7 +82,7 @@ constexpr int dec_i4_rest(int row_groups) { return 32 * (4 / row_groups); }
 // Bytes of a warp's sums: nt eights of rows, of each of which a lane has e.
 constexpr int dec_i4_part(int d, int nt, int e) { return (e * nt * d / 32 + nt) * 512; }
 
-template <int D_, int G_, int NT_, int RG_, bool kFew_, bool kRests_>
+template <int D_, int G_, int NT_, int RG_, bool kFew_, bool kTwice_, bool kRests_>
 struct DecI4Cfg {
     static constexpr int D = D_;
     static constexpr int G = G_;                  // components per group
@@ -96,6 +96,12 @@ struct DecI4Cfg {
     // its own rounding, 266 -> 273 us when it came.  bf16: two keys that nearly cancel
     // leave less than 2^-17 of their values in place of 2^-12, kv8 83 -> 87.6 us, with
     // groups of 64 72 -> 74.
+    // With more rows, and where O is fp16, whose own rounding is no coarser than a
+    // weight's, that rest takes the products a second time, over the same codes: the
+    // error of O 1.15 to 1.8 -> 1.00 times its own rounding, 64 requests x 8 heads of 8 rows
+    // 93 -> 111 us, of 8 at d 64 58 -> 65, of 32 245 -> 328.
+    static constexpr bool kTwice = kTwice_;
+    static_assert(!(kFew && kTwice), "one place for the rest");
     static constexpr int E = kFew ? 1 : 2;        // rows of each eight columns that are a lane's
     static constexpr int RC = 4 * E * NT * RG;    // rows per unit
     static constexpr bool kWide = D <= 128 && NT == 1;
@@ -452,7 +458,7 @@ __device__ __forceinline__ void dec_i4_q_unit(const DecInt4Params &p, const uint
 template <class C>
 __device__ __forceinline__ void dec_i4_begin_unit(const DecInt4Params &p, const uint4 (&raw)[C::NT][C::NC], int lane,
                                                   DecI4Warp<C> &w) {
-    if (p.fp16) dec_i4_q_unit<C, true>(p, raw, lane, w);
+    if (C::kTwice || (C::kFew && p.fp16)) dec_i4_q_unit<C, true>(p, raw, lane, w);
     else dec_i4_q_unit<C, false>(p, raw, lane, w);
 }
 
@@ -746,7 +752,8 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
     uint32_t raw[H][4];
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
-        uint32_t pf[H][C::NT][2];
+        constexpr int PF = C::kTwice ? 2 : 1;
+        uint32_t pf[PF][H][C::NT][2];
         float zs[C::NT][4];
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -754,33 +761,42 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
             const float a0 = a[h][0][g], a1 = -a[h][1][g];
 #pragma unroll
             for (int n = 0; n < C::NT; ++n) {
-                uint32_t h0 = ptx::pack_f16x2(s[h][n][0][0] * a0, s[h][n][0][C::E - 1] * a0);
-                uint32_t h1 = ptx::pack_f16x2(s[h][n][1][0] * a1, s[h][n][1][C::E - 1] * a1);
+                float p0[2], p1[2];
+#pragma unroll
+                for (int e = 0; e < C::E; ++e) p0[e] = s[h][n][0][e] * a0, p1[e] = s[h][n][1][e] * a1;
                 if constexpr (C::kFew) {  // the other column holds what the rounding lost
-                    h0 = ptx::pack_f16x2(s[h][n][0][0] * a0, s[h][n][0][0] * a0 - unpack16<true>(h0).x);
-                    h1 = ptx::pack_f16x2(s[h][n][1][0] * a1, s[h][n][1][0] * a1 - unpack16<true>(h1).x);
+                    p0[1] = p0[0] - unpack16<true>(ptx::pack_f16x2(p0[0], p0[0])).x;
+                    p1[1] = p1[0] - unpack16<true>(ptx::pack_f16x2(p1[0], p1[0])).x;
                 }
-                pf[h][n][0] = movmatrix_trans(h0);
-                pf[h][n][1] = movmatrix_trans(h1);
-                // (the zeros meet the rounded weights, so that a weight's rounding is of its value's share only)
-                if constexpr (!C::ZMMA) {
-                    const float z0 = i4_zero(vw[h][0][g]), z1 = 15.f - i4_zero(vw[h][1][g]);
-                    const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
-                    w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
-                    w.zo[n][g][C::E - 1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][C::E - 1]));
-                } else if constexpr (C::kPairs && H == 1) {
-                    const uint32_t f[4] = {zr[0][0], 0u, kFifteen, zr[0][0] ^ kMinus};
-                    mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
-                } else if constexpr (C::kPairs) {
-                    const uint32_t z0 = zr[0][2 * (h >> 1)], z1 = zr[0][2 * (h >> 1) + 1] ^ kMinus;
-                    const uint32_t f[4] = {h & 1 ? 0u : z0, h & 1 ? z0 : 0u, h & 1 ? kFifteen : z1, h & 1 ? z1 : kFifteen};
-                    if (h == 0) mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
-                    else mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
-                } else {
-                    const int q = C::NG > 4 ? 2 * h + g / 4 : h / 2, x = C::NG > 4 ? 0 : 2 * (h & 1);
-                    const uint32_t f[4] = {zr[q][x], 0u, zr[q][x + 1] ^ kMinus, kFifteen};
-                    if (h == 0) mma_16816_first(zs[n], f, pf[h][n][0], pf[h][n][1]);
-                    else mma_16816(zs[n], f, pf[h][n][0], pf[h][n][1]);
+#pragma unroll
+                for (int x = 0; x < PF; ++x) {
+                    const uint32_t h0 = ptx::pack_f16x2(p0[0], p0[1]), h1 = ptx::pack_f16x2(p1[0], p1[1]);
+                    pf[x][h][n][0] = movmatrix_trans(h0);
+                    pf[x][h][n][1] = movmatrix_trans(h1);
+                    // (the zeros meet the rounded weights, so that a weight's rounding is of its value's share only)
+                    if constexpr (!C::ZMMA) {
+                        const float z0 = i4_zero(vw[h][0][g]), z1 = 15.f - i4_zero(vw[h][1][g]);
+                        const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
+                        w.zo[n][g][0] = fmaf(f0.x, z0, fmaf(f1.x, z1, w.zo[n][g][0]));
+                        w.zo[n][g][C::E - 1] = fmaf(f0.y, z0, fmaf(f1.y, z1, w.zo[n][g][C::E - 1]));
+                    } else {
+                        uint32_t f[4];
+                        if constexpr (C::kPairs && H == 1) {
+                            f[0] = zr[0][0], f[1] = 0u, f[2] = kFifteen, f[3] = zr[0][0] ^ kMinus;
+                        } else if constexpr (C::kPairs) {
+                            const uint32_t z0 = zr[0][2 * (h >> 1)], z1 = zr[0][2 * (h >> 1) + 1] ^ kMinus;
+                            f[0] = h & 1 ? 0u : z0, f[1] = h & 1 ? z0 : 0u, f[2] = h & 1 ? kFifteen : z1, f[3] = h & 1 ? z1 : kFifteen;
+                        } else {
+                            const int q = C::NG > 4 ? 2 * h + g / 4 : h / 2, y = C::NG > 4 ? 0 : 2 * (h & 1);
+                            f[0] = zr[q][y], f[1] = 0u, f[2] = zr[q][y + 1] ^ kMinus, f[3] = kFifteen;
+                        }
+                        if (h == 0 && x == 0) mma_16816_first(zs[n], f, pf[x][h][n][0], pf[x][h][n][1]);
+                        else mma_16816(zs[n], f, pf[x][h][n][0], pf[x][h][n][1]);
+                    }
+                    if constexpr (C::kTwice) {
+                        const float2 f0 = unpack16<true>(h0), f1 = unpack16<true>(h1);
+                        p0[0] -= f0.x, p0[1] -= f0.y, p1[0] -= f1.x, p1[1] -= f1.y;
+                    }
                 }
             }
         }
@@ -807,7 +823,9 @@ __device__ __forceinline__ void dec_i4_keys(DecI4Warp<C> &w, int key, int L, int
                 for (int h = 0; h < H; ++h) {
                     const uint32_t f[4] = {lo[h] & 0x000f000fu, lo[h] & 0x00f000f0u, ~hi[h] & 0x000f000fu, ~hi[h] & 0x00f000f0u};
 #pragma unroll
-                    for (int n = 0; n < C::NT; ++n) mma_16816(w.o[n][c][x], f, pf[h][n][0], pf[h][n][1]);
+                    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                        for (int y = 0; y < PF; ++y) mma_16816(w.o[n][c][x], f, pf[y][h][n][0], pf[y][h][n][1]);
                     lo[h] >>= 8;
                     hi[h] >>= 8;
                 }

@@ -558,14 +558,14 @@ fa_status fa_cache_read_int4(const void *k_cache, const void *v_cache, const uns
  * attention over the values of its codes, q and o in 16 bits.  q enters exactly,
  * but for components below 2^-24 of their row's largest: those may be off by
  * 2^-34 of that.  A weight times its group's V scale is rounded to 11 bits before
- * P V (22 with up to four rows per K/V head), and to no finer than 2^-23 of the
- * row's largest such product, both relative to a reference of their own group's
- * scales (2^-31 where these are alike).  The reference is within 2^8 of the
- * largest scale of 16 or 32 keys, so that a group whose scales lie that far below it
- * may lose 2^-15 of its own largest product.  Sums are fp32; those of products are
- * cut off, not rounded, at each of at most 256 in a row (2^-15 of the sum of the
- * weights times s (15 + |z|)).  Deterministic.  Two launches at most; the
- * workspace's contents on entry do not matter.  Arguments as for
+ * P V (22 with fp16 q, and in bf16 with up to four rows per K/V head), and to no
+ * finer than 2^-23 of the row's largest such product, both relative to a reference
+ * of their own group's scales (2^-31 where these are alike).  The reference is
+ * within 2^8 of the largest scale of 16 or 32 keys, so that a group whose scales lie
+ * that far below it may lose 2^-15 of its own largest product.  Sums are fp32; those
+ * of products are cut off, not rounded, at each of at most 512 in a row (2^-15 of
+ * the sum of the weights times s (15 + |z|)).  Deterministic.  Two launches at most;
+ * the workspace's contents on entry do not matter.  Arguments as for
  * fa_decode_paged, except:
  *
  *   k_cache, v_cache, k_scale, v_scale, group  as above; scales finite and >= 0

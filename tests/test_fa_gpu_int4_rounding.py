@@ -25,7 +25,7 @@ def _lib():
 
 
 def _check_fine(p, o, lse, max_len, scale, mask="none"):
-    """Up to four rows per K/V head a weight times its scale is held in two fp16 numbers, 2^-22 of it; the second's
+    """With fp16, and up to four rows per K/V head in bf16 too, a weight times its scale is held in two fp16 numbers, 2^-22 of it; the second's
     smallest half step is 2^-25, no more than that of a product of 2^-3 or more, 2^9 below a row's largest (2^6 at
     least when it is summed), and here all lie nearer.  The rest as in the attention's other tests: the scores', the
     sums' 2^-17 of sum p s (15 + |z|) (2^-23 of what is held at each of at most 64 products), and one rounding of O."""
@@ -57,41 +57,57 @@ def _scores(p, scores):
                 np.array([scores[j] / 15], np.float32), inputs.BF16), inputs.BF16).astype(np.float32), [0.0])[0]
 
 
-@pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
-@pytest.mark.parametrize("H,Hkv,Sq", [(2, 2, 1), (4, 2, 1), (4, 1, 1), (2, 2, 4)])
-@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)])
-def test_up_to_four_rows_two_keys_that_nearly_cancel(d, group, H, Hkv, Sq, dtype):
-    # V of the second key is that of the first with its sign turned: O is the difference of two weights times V,
-    # and a weight rounded to 11 bits would be seen in it
-    p = _problem(8, H, Hkv, Sq, d, group, 16, [2] * 8, dtype, seed=d + H, q_size=0.002)
-    for b in range(8):
+def _cancel(p):
+    """V of each request's second key becomes that of its first with the sign turned: O is the difference of two
+    weights times V, and a weight rounded to 11 bits would be seen in it."""
+    for b in range(len(p["lens"])):
         block = p["table"][b, 0]
         p["vc"][block, :, 1] = 0xFF - p["vc"][block, :, 0]
         s, z = ref.unpack_words(p["vw"][block, :, 0])
         p["vw"][block, :, 0] = ref.words(s, np.rint(z))
         p["vw"][block, :, 1] = ref.words(s, 15 - np.rint(z))
+
+
+@pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
+@pytest.mark.parametrize("H,Hkv,Sq", [(2, 2, 1), (4, 2, 1), (4, 1, 1), (2, 2, 4)])
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)])
+def test_up_to_four_rows_two_keys_that_nearly_cancel(d, group, H, Hkv, Sq, dtype):
+    p = _problem(8, H, Hkv, Sq, d, group, 16, [2] * 8, dtype, seed=d + H, q_size=0.002)
+    _cancel(p)
     o, lse = fa.decode_paged_int4(*_device(p), 2)
     _check_fine(p, o, lse, 2, 1 / np.sqrt(d))
 
 
-@pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
+@pytest.mark.parametrize("H,Hkv,Sq", [(5, 1, 1), (16, 2, 1), (16, 1, 1), (8, 1, 4), (8, 1, 5)])
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)])
+def test_fp16_more_rows_two_keys_that_nearly_cancel(d, group, H, Hkv, Sq):
+    p = _problem(8, H, Hkv, Sq, d, group, 16, [2] * 8, inputs.FP16, seed=d + H, q_size=0.002)
+    _cancel(p)
+    o, lse = fa.decode_paged_int4(*_device(p), 2)
+    _check_fine(p, o, lse, 2, 1 / np.sqrt(d))
+
+
+ROWS = [(4, 1, inputs.BF16), (4, 1, inputs.FP16), (8, 1, inputs.FP16), (16, 1, inputs.FP16), (16, 2, inputs.FP16), (8, 5, inputs.FP16)]
+
+
+@pytest.mark.parametrize("H,Sq,dtype", ROWS)
 @pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)])
 @pytest.mark.parametrize("n", [1, 7, 40, 129, 520])
-def test_up_to_four_rows_of_few_keys(n, d, group, dtype):
-    p = _problem(3, 4, 1, 1, d, group, 16, [n, max(1, n - 1), n], dtype, seed=n + d, q_size=0.05)
+def test_few_keys(n, d, group, H, Sq, dtype):
+    p = _problem(3, H, 1, Sq, d, group, 16, [n, max(1, n - 1), n], dtype, seed=n + d, q_size=0.05)
     o, lse = fa.decode_paged_int4(*_device(p), n)
     _check_fine(p, o, lse, n, 1 / np.sqrt(d))
 
 
-@pytest.mark.parametrize("dtype", [inputs.BF16, inputs.FP16])
+@pytest.mark.parametrize("H,Sq,dtype", ROWS)
 @pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)])
 @pytest.mark.parametrize("rise", [6.0, 9.0])
-def test_up_to_four_rows_whose_references_move(rise, d, group, dtype):
+def test_references_that_move(rise, d, group, H, Sq, dtype):
     # a key in every 32 carries the weight, and those of a tile lie above those of the tile in front, so that all
     # sums are rescaled (the rest of the weights too); the last tile's values are 0, so that O is what the tiles in
     # front of it left
     n = 4 * 128
-    p = _problem(1, 4, 1, 1, d, group, 16, [n], dtype, seed=d, junk=False)
+    p = _problem(1, H, 1, Sq, d, group, 16, [n], dtype, seed=d, junk=False)
     _scores(p, np.where(np.arange(n) % 32 == 0, 20.0 + rise * (np.arange(n) // 128), 0.0))
     for j in range(n - 128, n):
         block, at = p["table"][0, j // 16], j % 16
@@ -137,7 +153,7 @@ def test_a_first_key_that_outweighs_very_many_even_ones(down, H, d, group, dtype
                                          (4, 128, 32, 1 << 21)])
 def test_sums_over_very_long_requests_whose_codes_are_large(H, d, group, n):
     """A unit per CTA, of so many keys that a sum cut off at each of their products, by up to 2^-23 of what it holds,
-    could lose 2^-8 of itself.  All codes are near 15.  The sums are allowed 2^-15 of sum p s (15 + |z|) (at most 256
+    could lose 2^-8 of itself.  All codes are near 15.  The sums are allowed 2^-15 of sum p s (15 + |z|) (at most 512
     products in a row, 2^-23 of what is held at each, and 512 pieces of them), those of the weights 2^-15 (512 in a row
     and 512 pieces, 2^-25 each on the mean), a weight 2^-11 of its value, and the scores' share as in the other tests."""
     B, bs = 152 * 3, 128
