@@ -50,13 +50,13 @@
 //
 // What bounds it (kv8: 64 requests, 32 heads on 8 K/V heads, up to 8,192 tokens, d 128,
 // bf16, groups of 32, 379 MB): the copies alone run at 57 us, the floor is 56 and the
-// kernel takes 84.  A step of 16 keys is 320 instructions of a warp, 88 of them masks and shifts at
-// half rate; the ALU is busy half of the time and the issue slots too, with three
-// warps to a scheduler, whose waits for one another's pipes and for their own results
-// fill the rest.  16 warps of one sixteen each (128 registers) take 103 us, 8 warps of
-// four sixteens 85 to 93, and copies by a ninth warp left two CTAs' warps 96 registers
-// and spilled (216).  Short units pay for their ends: 128 requests x 40 heads, nine
-// tiles to a unit, 262 us for a floor of 140.
+// kernel takes 87.5.  16 keys are 358 instructions of a warp, a quarter of them masks and
+// shifts at half rate; the ALU is busy half of the time and the issue slots too, with
+// three warps to a scheduler, whose waits for one another's pipes and for their own
+// results fill the rest.  Before weights kept their rests it took 84 us, 16 warps of one
+// sixteen each (128 registers) 103, 8 warps of four sixteens 85 to 93; copies by a ninth
+// warp left two CTAs' warps 96 registers and spilled (216).  Short units pay for their
+// ends: 128 requests x 40 heads, nine tiles to a unit, 268 us for a floor of 140.
 #pragma once
 
 #include <math.h>
